@@ -563,6 +563,92 @@ nvfp4_status nvfp4_decode_attention(const void* q, const uint8_t* k_packed,
                                     void* out, float* workspace, size_t workspace_bytes,
                                     void* stream);
 
+/* ------------------------------------------------------------------------
+ * Token rows into expert order and back (BF16, FP16, FP32), with gradients.
+ *
+ * route_pos int32 [T, topk] is the position of each route's row in the
+ * route-ordered buffer of R rows (as nvfp4_moe_route writes it); a negative
+ * position is a route that was dropped and is neither read nor written.  The
+ * live positions are distinct.  A position >= R is skipped and recorded as
+ * NVFP4_ERR_DEVICE_CHECK.  expert_offsets, where given, is nvfp4_moe_route's
+ * [E + 1]: the rows from expert_offsets[E] on belong to no route and are set
+ * to zero; NULL leaves rows without a route unwritten.  D >= 1 and any row
+ * stride >= D; rows whose base, stride and width are multiples of 16 bytes
+ * move by 16-byte accesses, others by element.  Sums are FP32 in a fixed
+ * order (k ascending), rounded once: results repeat bit for bit.
+ * ------------------------------------------------------------------------ */
+typedef enum nvfp4_dtype { NVFP4_BF16 = 0, NVFP4_FP16 = 1, NVFP4_FP32 = 2 } nvfp4_dtype;
+
+/* out[route_pos[t, k], :] = x[t, :].  x [T, D] (row stride ld), out [R, D]. */
+nvfp4_status nvfp4_tokens_dispatch(const void* x, int64_t ld, const int32_t* route_pos,
+                                   const int32_t* expert_offsets, int32_t E, int64_t T,
+                                   int32_t topk, int64_t R, int64_t D, int32_t dtype, void* out,
+                                   void* stream);
+
+/* out[t, :] = sum_k weights[t, k] * y[route_pos[t, k], :]; weights FP32
+ * [T, topk], or NULL for ones (the gradient of the dispatch).  y [R, D] (row
+ * stride ld), out [T, D]; a token without a live route gets zeros. */
+nvfp4_status nvfp4_tokens_combine(const void* y, int64_t ld, const int32_t* route_pos,
+                                  const float* weights, int64_t T, int32_t topk, int64_t R,
+                                  int64_t D, int32_t dtype, void* out, void* stream);
+
+/* Gradient of the combine: dy[route_pos[t, k], :] = weights[t, k] * dout[t, :]
+ * ([R, D], type of dout) and dw[t, k] = sum_c dout[t, c] * y[route_pos[t, k], c]
+ * (FP32 [T, topk], zero for a dropped route). */
+nvfp4_status nvfp4_tokens_combine_grad(const void* dout, int64_t ld, const void* y, int64_t ld_y,
+                                       const int32_t* route_pos, const float* weights,
+                                       const int32_t* expert_offsets, int32_t E, int64_t T,
+                                       int32_t topk, int64_t R, int64_t D, int32_t dtype,
+                                       void* dy, float* dw, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products with 8-bit (E4M3) weights, one FP32 scale per 128 x 128 block of
+ * the weights and per 1 x 128 block of the activations:
+ *
+ *   y[m, n] = sum_b sa[b, m] * sw[n / 128, b] * sum_{k in block b} qa[m, k] * qw[n, k]
+ *
+ * FP32 accumulation, one rounding to the output's type.  Codes are E4M3
+ * bytes, row-major and dense: activations [M, K], weights [N, K] (grouped:
+ * [E, N, K]).  Scales: activations [ceil(K/128), M] (K block major, so that
+ * the scales of neighbouring rows are neighbours), weights [ceil(N/128),
+ * ceil(K/128)] (grouped: one such matrix per expert).  K % 16 == 0 and 16-byte
+ * aligned codes; M, N and the last blocks are free.
+ * ------------------------------------------------------------------------ */
+#define NVFP4_FP8_SILU_MUL 1u   /* quantise SiLU(x[:, :cols]) * x[:, cols:]        */
+
+/* Activations -> codes and scales: a = max(amax of the block, 2^-100), scale =
+ * a / 448, code = E4M3(448 x / a) rounded once (nearest, ties to even).  x
+ * BF16 or FP16 [rows, cols] (row stride ld, % 8 == 0; with NVFP4_FP8_SILU_MUL
+ * [rows, 2 * cols], gate half first, the product formed in FP32).  route_pos
+ * (int32 [rows, fanout], or NULL): row i is written to the rows route_pos[i, :]
+ * of codes and scales (out_rows rows), negative positions are skipped; NULL:
+ * fanout must be 1 and out_rows == rows.  A block that holds an infinity or
+ * NaN quantises to values that make its row's products NaN. */
+nvfp4_status nvfp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                                int32_t dtype, uint32_t flags, const int32_t* route_pos,
+                                int32_t fanout, uint8_t* codes, float* scales, int64_t out_rows,
+                                void* stream);
+
+/* Weights [E, N, K] (BF16, FP16 or FP32, dense) -> codes and block scales by
+ * the same formula over 128 x 128 blocks (prepared once). */
+nvfp4_status nvfp4_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K,
+                                        int32_t dtype, uint8_t* codes, float* scales,
+                                        void* stream);
+
+/* One matrix: C [M, N] (row stride ldc, of type dtype). */
+nvfp4_status nvfp4_fp8_gemm(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
+                            void* C, int64_t M, int64_t N, int64_t K, int64_t ldc, int32_t dtype,
+                            void* stream);
+
+/* Grouped by expert: rows [expert_offsets[e], expert_offsets[e + 1]) of A [R,
+ * K] meet expert e's weights (E <= 1024); out [R, N] in route order.  Rows from
+ * expert_offsets[E] on are zero.  Offsets that are not monotone inside [0, R]
+ * are recorded as NVFP4_ERR_DEVICE_CHECK and their expert is skipped. */
+nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uint8_t* W,
+                                    const float* sW, const int32_t* expert_offsets, int32_t E,
+                                    int64_t R, int64_t N, int64_t K, void* out, int64_t ldc,
+                                    int32_t dtype, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

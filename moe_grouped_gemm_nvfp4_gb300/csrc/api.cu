@@ -12,6 +12,8 @@
 #include "../../include/nvfp4.h"
 #include "kernels.h"
 #include "attention.h"
+#include "fp8.h"
+#include "tokens.h"
 
 namespace {
 
@@ -64,6 +66,7 @@ nvfp4_status device_state(DeviceState** out) {
       if (nvfp4::init_grouped_pair_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_attention_tc_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_route_attributes() != cudaSuccess) return cuda_fail();
+      if (nvfp4::init_fp8_gemm_attributes() != cudaSuccess) return cuda_fail();
     }
     if (!g_encode) {
       void* fn = nullptr;
@@ -185,6 +188,69 @@ nvfp4_status make_scale_map(CUtensorMap* m, const void* base, uint64_t rows, int
                               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
+}
+
+// Map over E4M3 codes [E, rows, K] (uint8), boxes of 128 bytes x box_rows rows
+// of one matrix, 128-byte swizzle.  Rows past a matrix and columns past K read
+// zeros.
+nvfp4_status make_fp8_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t E,
+                          uint32_t box_rows, uint32_t rank) {
+  const cuuint64_t dims[3] = {K, rows, E};
+  const cuuint64_t strides[2] = {K, K * rows};
+  const cuuint32_t box[3] = {128u, box_rows, 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
+}
+
+bool is_dtype(int32_t t) { return t == NVFP4_BF16 || t == NVFP4_FP16 || t == NVFP4_FP32; }
+bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+unsigned dtype_bytes(int32_t t) { return t == NVFP4_FP32 ? 4u : 2u; }
+
+nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
+                           const int32_t* offsets, int32_t E, int64_t rows, int64_t N, int64_t K,
+                           void* out, int64_t ldc, int32_t dtype, void* stream) {
+  if (!is_dtype(dtype) || E <= 0 || rows < 0 || N <= 0 || K <= 0 || ldc < N)
+    return NVFP4_ERR_INVALID_ARG;
+  if (!W || !sW || (rows > 0 && (!A || !sA || !out))) return NVFP4_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > (1LL << 30) || N > (1LL << 30) || rows > (1LL << 30) ||
+      E > nvfp4::kFp8MaxExperts)
+    return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned16(A) || !aligned16(W) || !aligned_to(sA, 4) || !aligned_to(sW, 4) ||
+      !aligned_to(offsets, 4) || !aligned_to(out, dtype_bytes(dtype)))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (rows == 0) return NVFP4_OK;
+  nvfp4::Fp8GemmArgs a{};
+  a.sa = sA;
+  a.lds = rows;
+  a.sw = sW;
+  a.offsets = offsets;
+  a.E = E;
+  a.rows = static_cast<int32_t>(rows);
+  a.N = static_cast<int32_t>(N);
+  a.K = static_cast<int32_t>(K);
+  a.nkb = static_cast<int32_t>((K + 127) / 128);
+  a.nnb = static_cast<int32_t>((N + 127) / 128);
+  a.out = out;
+  a.ldc = ldc;
+  a.out_type = dtype;
+  a.status = d->status;
+  a.timeout_ns = g_timeout_ns.load();
+  a.debug_flags = g_debug_flags.load();
+  CUtensorMap ta, tw;
+  const uint32_t box = static_cast<uint32_t>(nvfp4::fp8_tile_tokens(rows, offsets ? E : 0));
+  if (make_fp8_map(&ta, A, K, rows, 1, box, 2) != NVFP4_OK ||
+      make_fp8_map(&tw, W, K, N, E, 128, 3) != NVFP4_OK)
+    return NVFP4_ERR_UNSUPPORTED;
+  if (nvfp4::launch_fp8_gemm(ta, tw, a, d->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return cuda_fail();
+  return NVFP4_OK;
 }
 
 }  // namespace
@@ -1047,6 +1113,176 @@ nvfp4_status nvfp4_grouped_gemm_combine_noalloc(const uint8_t* A_tiles, const fl
     return cuda_fail();
   if (nvfp4::launch_combine_finalize(ws, T, N, out, d->sms, s) != cudaSuccess) return cuda_fail();
   return NVFP4_OK;
+}
+
+// ------------------------------------------------------------- token rows
+
+nvfp4_status nvfp4_tokens_dispatch(const void* x, int64_t ld, const int32_t* route_pos,
+                                   const int32_t* expert_offsets, int32_t E, int64_t T,
+                                   int32_t topk, int64_t R, int64_t D, int32_t dtype, void* out,
+                                   void* stream) {
+  if (T < 0 || topk <= 0 || R < 0 || D <= 0 || ld < D || !is_dtype(dtype))
+    return NVFP4_ERR_INVALID_ARG;
+  if (expert_offsets && E <= 0) return NVFP4_ERR_INVALID_ARG;
+  if ((T > 0 && (!x || !route_pos)) || (R > 0 && !out)) return NVFP4_ERR_INVALID_ARG;
+  const unsigned es = dtype_bytes(dtype);
+  if (R > 0x7FFFFFFFLL || !aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(route_pos, 4) ||
+      !aligned_to(expert_offsets, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (R == 0) return NVFP4_OK;
+  nvfp4::TokensArgs a{};
+  a.src = x;
+  a.ld = ld;
+  a.pos = route_pos;
+  a.live = expert_offsets ? expert_offsets + E : nullptr;
+  a.out = out;
+  a.T = T;
+  a.R = R;
+  a.D = D;
+  a.topk = topk;
+  a.status = d->status;
+  const cudaError_t e = nvfp4::launch_tokens_dispatch(a, dtype, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+nvfp4_status nvfp4_tokens_combine(const void* y, int64_t ld, const int32_t* route_pos,
+                                  const float* weights, int64_t T, int32_t topk, int64_t R,
+                                  int64_t D, int32_t dtype, void* out, void* stream) {
+  if (T < 0 || topk <= 0 || R < 0 || D <= 0 || ld < D || !is_dtype(dtype))
+    return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!route_pos || !out || (R > 0 && !y))) return NVFP4_ERR_INVALID_ARG;
+  const unsigned es = dtype_bytes(dtype);
+  if (R > 0x7FFFFFFFLL || !aligned_to(y, es) || !aligned_to(out, es) || !aligned_to(route_pos, 4) ||
+      !aligned_to(weights, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::TokensArgs a{};
+  a.src = y;
+  a.ld = ld;
+  a.pos = route_pos;
+  a.w = weights;
+  a.out = out;
+  a.T = T;
+  a.R = R;
+  a.D = D;
+  a.topk = topk;
+  a.status = d->status;
+  const cudaError_t e = nvfp4::launch_tokens_combine(a, dtype, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+nvfp4_status nvfp4_tokens_combine_grad(const void* dout, int64_t ld, const void* y, int64_t ld_y,
+                                       const int32_t* route_pos, const float* weights,
+                                       const int32_t* expert_offsets, int32_t E, int64_t T,
+                                       int32_t topk, int64_t R, int64_t D, int32_t dtype,
+                                       void* dy, float* dw, void* stream) {
+  if (T < 0 || topk <= 0 || R < 0 || D <= 0 || ld < D || ld_y < D || !is_dtype(dtype))
+    return NVFP4_ERR_INVALID_ARG;
+  if (expert_offsets && E <= 0) return NVFP4_ERR_INVALID_ARG;
+  if ((T > 0 && (!dout || !route_pos || !weights || !dw)) || (R > 0 && (!y || !dy)))
+    return NVFP4_ERR_INVALID_ARG;
+  const unsigned es = dtype_bytes(dtype);
+  if (R > 0x7FFFFFFFLL || !aligned_to(dout, es) || !aligned_to(y, es) || !aligned_to(dy, es) ||
+      !aligned_to(route_pos, 4) || !aligned_to(weights, 4) || !aligned_to(dw, 4) ||
+      !aligned_to(expert_offsets, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  nvfp4::TokensArgs a{};
+  a.src = dout;
+  a.ld = ld;
+  a.y = y;
+  a.ld_y = ld_y;
+  a.pos = route_pos;
+  a.w = weights;
+  a.live = expert_offsets && R > 0 ? expert_offsets + E : nullptr;
+  a.out = dy;
+  a.dw = dw;
+  a.T = T;
+  a.R = R;
+  a.D = D;
+  a.topk = topk;
+  a.status = d->status;
+  const cudaError_t e =
+      nvfp4::launch_tokens_combine_grad(a, dtype, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+// ---------------------------------------------------------- FP8 products
+
+nvfp4_status nvfp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                                int32_t dtype, uint32_t flags, const int32_t* route_pos,
+                                int32_t fanout, uint8_t* codes, float* scales, int64_t out_rows,
+                                void* stream) {
+  const int64_t width = (flags & NVFP4_FP8_SILU_MUL) ? 2 * cols : cols;
+  if (rows < 0 || cols <= 0 || ld < width || fanout <= 0 || out_rows < 0 || !is_dtype(dtype) ||
+      (flags & ~NVFP4_FP8_SILU_MUL))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!route_pos && (fanout != 1 || out_rows != rows)) return NVFP4_ERR_INVALID_ARG;
+  if ((rows > 0 && !x) || (out_rows > 0 && (!codes || !scales))) return NVFP4_ERR_INVALID_ARG;
+  if (dtype == NVFP4_FP32 || cols % 16 != 0 || ld % 8 != 0 || out_rows > 0x7FFFFFFFLL ||
+      cols > (1LL << 30) || !aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4) ||
+      !aligned_to(route_pos, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (rows == 0 || out_rows == 0) return NVFP4_OK;
+  nvfp4::Fp8QuantArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.route_pos = route_pos;
+  a.fanout = fanout;
+  a.silu = (flags & NVFP4_FP8_SILU_MUL) ? 1 : 0;
+  a.codes = codes;
+  a.scales = scales;
+  a.out_rows = out_rows;
+  a.status = d->status;
+  const cudaError_t e = nvfp4::launch_fp8_quantize(a, dtype, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+nvfp4_status nvfp4_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K,
+                                        int32_t dtype, uint8_t* codes, float* scales,
+                                        void* stream) {
+  if (E <= 0 || N <= 0 || K <= 0 || !is_dtype(dtype) || !w || !codes || !scales)
+    return NVFP4_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !aligned_to(w, dtype_bytes(dtype)) || !aligned_to(scales, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  const cudaError_t e = nvfp4::launch_fp8_quantize_weights(w, E, N, K, codes, scales, dtype,
+                                                           static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+nvfp4_status nvfp4_fp8_gemm(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
+                            void* C, int64_t M, int64_t N, int64_t K, int64_t ldc, int32_t dtype,
+                            void* stream) {
+  return fp8_gemm_impl(A, sA, W, sW, nullptr, 1, M, N, K, C, ldc, dtype, stream);
+}
+
+nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uint8_t* W,
+                                    const float* sW, const int32_t* expert_offsets, int32_t E,
+                                    int64_t R, int64_t N, int64_t K, void* out, int64_t ldc,
+                                    int32_t dtype, void* stream) {
+  if (!expert_offsets) return NVFP4_ERR_INVALID_ARG;
+  return fp8_gemm_impl(A, sA, W, sW, expert_offsets, E, R, N, K, out, ldc, dtype, stream);
 }
 
 }  // extern "C"

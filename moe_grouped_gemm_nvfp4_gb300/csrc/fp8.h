@@ -1,0 +1,55 @@
+// Internal launchers of the FP8 (E4M3, 128-wide scale blocks) kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace nvfp4 {
+
+constexpr int kFp8Block = 128;             // K elements (and weight rows) under one scale
+constexpr int kFp8MaxExperts = 1024;
+constexpr uint32_t kFp8SkipFirstStage = 1u;   // = kDebugSkipFirstStage (kernels.h)
+
+struct Fp8QuantArgs {
+  const void* x;                   // [rows, cols] (silu: [rows, 2 * cols], gate then up)
+  int64_t rows, cols, ld;
+  const int32_t* route_pos;        // [rows, fanout] positions of each row's copies; NULL: row i -> i
+  int32_t fanout;
+  int32_t silu;
+  uint8_t* codes;                  // [out_rows, cols]
+  float* scales;                   // [ceil(cols / 128), out_rows]
+  int64_t out_rows;
+  int* status;
+};
+
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K,
+                                        uint8_t* codes, float* scales, int dtype, cudaStream_t s);
+
+struct Fp8GemmArgs {
+  const float* sa;                 // [nkb, lds]: scale of row m's K block b at b * lds + m
+  int64_t lds;
+  const float* sw;                 // [E, nnb, nkb]
+  const int32_t* offsets;          // grouped: [E + 1]; NULL: one matrix
+  int32_t E;
+  int32_t rows;                    // M, or R
+  int32_t N, K;
+  int32_t nkb, nnb;                // 128-wide blocks of K and N
+  void* out;                       // [rows, ldc]
+  int64_t ldc;
+  int32_t out_type;                // nvfp4_dtype
+  int* status;
+  uint64_t timeout_ns;
+  uint32_t debug_flags;
+};
+
+// fp8_gemm.cu: 128 weight rows x up to 128 tokens a tile.  ta: codes of the
+// activations (boxes of fp8_tile_tokens() rows x 128 bytes), tw: of the
+// weights ([E, N, K], boxes of 128 x 128).
+cudaError_t init_fp8_gemm_attributes();
+int fp8_tile_tokens(int64_t rows, int32_t E);
+cudaError_t launch_fp8_gemm(const CUtensorMap& ta, const CUtensorMap& tw, const Fp8GemmArgs& a,
+                            int sms, cudaStream_t s);
+
+}  // namespace nvfp4

@@ -28,6 +28,11 @@ NVFP4_SF_ATOMS = 1
 NVFP4_GLOBAL_GIVEN = 2
 NVFP4_AMAX_DONE = 4
 
+NVFP4_BF16 = 0
+NVFP4_FP16 = 1
+NVFP4_FP32 = 2
+NVFP4_FP8_SILU_MUL = 1
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -76,6 +81,18 @@ _SIGS = {
     "nvfp4_prepack_sparse_weight_tiles": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
     "nvfp4_grouped_gemm_sparse": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I32, _I64,
                                                  _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "nvfp4_tokens_dispatch": (ctypes.c_int, [_P, _I64, _P, _P, _I32, _I64, _I32, _I64, _I64,
+                                             _I32, _P, _P]),
+    "nvfp4_tokens_combine": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _I64, _I64, _I32, _P,
+                                            _P]),
+    "nvfp4_tokens_combine_grad": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _I32, _I64, _I32,
+                                                 _I64, _I64, _I32, _P, _P, _P]),
+    "nvfp4_fp8_quantize": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _U32, _P, _I32, _P, _P,
+                                          _I64, _P]),
+    "nvfp4_fp8_quantize_weights": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _P, _P, _P]),
+    "nvfp4_fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P]),
+    "nvfp4_fp8_grouped_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _P,
+                                              _I64, _I32, _P]),
     "nvfp4_grouped_gemm_combine_noalloc": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I32,
                                                           _I64, _I64, _P, _P, _P, _P, _P]),
 }
@@ -350,6 +367,76 @@ def nvfp4_grouped_gemm_combine_noalloc(A_tiles, gA, W_tiles, gW, expert_offsets,
     _check("nvfp4_grouped_gemm_combine_noalloc", load().nvfp4_grouped_gemm_combine_noalloc(
         _ptr(A_tiles), _ptr(gA), _ptr(W_tiles), _ptr(gW), _ptr(expert_offsets), E, T, topk, N,
         K, _ptr(route_token), _ptr(route_slot), _ptr(topk_weights), _ptr(out), _stream(stream)))
+
+
+_DTYPES = {torch.bfloat16: NVFP4_BF16, torch.float16: NVFP4_FP16, torch.float32: NVFP4_FP32}
+
+
+def _dtype(t):
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"expected BF16, FP16 or FP32, got {t.dtype}") from None
+
+
+def nvfp4_tokens_dispatch(x, route_pos, expert_offsets, out, stream=None) -> None:
+    """out[route_pos[t, k]] = x[t]; expert_offsets int32 [E + 1] or None."""
+    T, topk = route_pos.shape
+    E = 0 if expert_offsets is None else expert_offsets.numel() - 1
+    _check("nvfp4_tokens_dispatch", load().nvfp4_tokens_dispatch(
+        _ptr(x), _row_stride(x), _ptr(route_pos), _ptr(expert_offsets), E, T, topk, out.shape[0],
+        x.shape[1], _dtype(x), _ptr(out), _stream(stream)))
+
+
+def nvfp4_tokens_combine(y, route_pos, weights, out, stream=None) -> None:
+    """out[t] = sum_k weights[t, k] * y[route_pos[t, k]]; weights FP32 or None (ones)."""
+    T, topk = route_pos.shape
+    _check("nvfp4_tokens_combine", load().nvfp4_tokens_combine(
+        _ptr(y), _row_stride(y), _ptr(route_pos), _ptr(weights), T, topk, y.shape[0], y.shape[1],
+        _dtype(y), _ptr(out), _stream(stream)))
+
+
+def nvfp4_tokens_combine_grad(dout, y, route_pos, weights, expert_offsets, dy, dw,
+                              stream=None) -> None:
+    """dy[route_pos[t, k]] = weights[t, k] * dout[t]; dw[t, k] = <dout[t], y[route_pos[t, k]]>."""
+    T, topk = route_pos.shape
+    E = 0 if expert_offsets is None else expert_offsets.numel() - 1
+    _check("nvfp4_tokens_combine_grad", load().nvfp4_tokens_combine_grad(
+        _ptr(dout), _row_stride(dout), _ptr(y), _row_stride(y), _ptr(route_pos), _ptr(weights),
+        _ptr(expert_offsets), E, T, topk, y.shape[0], y.shape[1], _dtype(dout), _ptr(dy),
+        _ptr(dw), _stream(stream)))
+
+
+def nvfp4_fp8_quantize(x, codes, scales, flags: int = 0, route_pos=None, stream=None) -> None:
+    """16-bit rows -> E4M3 codes [out_rows, cols] and scales [ceil(cols / 128), out_rows]."""
+    fanout = 1 if route_pos is None else route_pos.shape[1]
+    _check("nvfp4_fp8_quantize", load().nvfp4_fp8_quantize(
+        _ptr(x), x.shape[0], codes.shape[1], _row_stride(x), _dtype(x), flags, _ptr(route_pos),
+        fanout, _ptr(codes), _ptr(scales), codes.shape[0], _stream(stream)))
+
+
+def nvfp4_fp8_quantize_weights(w, codes, scales, stream=None) -> None:
+    """Weights [E, N, K] -> E4M3 codes and one scale per 128 x 128 block."""
+    E, N, K = w.shape
+    _check("nvfp4_fp8_quantize_weights", load().nvfp4_fp8_quantize_weights(
+        _ptr(w), E, N, K, _dtype(w), _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def nvfp4_fp8_gemm(A, sA, W, sW, C, stream=None) -> None:
+    """C [M, N] = (A, sA) . (W, sW)^T; W [N, K]."""
+    M, K = A.shape
+    _check("nvfp4_fp8_gemm", load().nvfp4_fp8_gemm(
+        _ptr(A), _ptr(sA), _ptr(W), _ptr(sW), _ptr(C), M, W.shape[0], K, _row_stride(C),
+        _dtype(C), _stream(stream)))
+
+
+def nvfp4_fp8_grouped_gemm(A, sA, W, sW, expert_offsets, out, stream=None) -> None:
+    """Rows of A [R, K] in expert order times their expert's weights; W [E, N, K]."""
+    R, K = A.shape
+    E, N, _ = W.shape
+    _check("nvfp4_fp8_grouped_gemm", load().nvfp4_fp8_grouped_gemm(
+        _ptr(A), _ptr(sA), _ptr(W), _ptr(sW), _ptr(expert_offsets), E, R, N, K, _ptr(out),
+        _row_stride(out), _dtype(out), _stream(stream)))
 
 
 # ------------------------------------------- allocating conveniences (torch)
