@@ -649,6 +649,28 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uin
                                     int64_t R, int64_t N, int64_t K, void* out, int64_t ldc,
                                     int32_t dtype, void* stream);
 
+/* Quantise and multiply in one call: y [M, N] = x . W^T for 16-bit rows x [M,
+ * K] (row stride ld), y of x's type.  The codes and scales of x lie in the
+ * caller's workspace (16-byte aligned, nvfp4_fp8_linear_workspace_bytes(M, K)
+ * bytes, overwritten).  The GEMM is launched to overlap the quantiser: its
+ * set-up and its first weight loads run meanwhile. */
+size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t K);
+
+nvfp4_status nvfp4_fp8_linear(const void* x, int64_t M, int64_t ld, int32_t dtype,
+                              const uint8_t* W, const float* sW, int64_t N, int64_t K, void* y,
+                              int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same grouped by expert: x [rows, K] in token order with route_pos
+ * [rows, fanout], or in route order (route_pos NULL, fanout 1, rows == R);
+ * flags as in nvfp4_fp8_quantize; y [R, N] in route order; workspace for R
+ * rows. */
+nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, int32_t dtype,
+                                     uint32_t flags, const int32_t* route_pos, int32_t fanout,
+                                     const uint8_t* W, const float* sW,
+                                     const int32_t* expert_offsets, int32_t E, int64_t R,
+                                     int64_t N, int64_t K, void* y, int64_t ldy, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -212,7 +212,7 @@ unsigned dtype_bytes(int32_t t) { return t == NVFP4_FP32 ? 4u : 2u; }
 
 nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
                            const int32_t* offsets, int32_t E, int64_t rows, int64_t N, int64_t K,
-                           void* out, int64_t ldc, int32_t dtype, void* stream) {
+                           void* out, int64_t ldc, int32_t dtype, bool overlap, void* stream) {
   if (!is_dtype(dtype) || E <= 0 || rows < 0 || N <= 0 || K <= 0 || ldc < N)
     return NVFP4_ERR_INVALID_ARG;
   if (!W || !sW || (rows > 0 && (!A || !sA || !out))) return NVFP4_ERR_INVALID_ARG;
@@ -240,6 +240,7 @@ nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, 
   a.out = out;
   a.ldc = ldc;
   a.out_type = dtype;
+  a.overlap = overlap ? 1 : 0;
   a.status = d->status;
   a.timeout_ns = g_timeout_ns.load();
   a.debug_flags = g_debug_flags.load();
@@ -248,9 +249,10 @@ nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, 
   if (make_fp8_map(&ta, A, K, rows, 1, box, 2) != NVFP4_OK ||
       make_fp8_map(&tw, W, K, N, E, 128, 3) != NVFP4_OK)
     return NVFP4_ERR_UNSUPPORTED;
-  if (nvfp4::launch_fp8_gemm(ta, tw, a, d->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return cuda_fail();
-  return NVFP4_OK;
+  const cudaError_t e =
+      nvfp4::launch_fp8_gemm(ta, tw, a, d->sms, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
 }
 
 }  // namespace
@@ -1274,7 +1276,7 @@ nvfp4_status nvfp4_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int
 nvfp4_status nvfp4_fp8_gemm(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
                             void* C, int64_t M, int64_t N, int64_t K, int64_t ldc, int32_t dtype,
                             void* stream) {
-  return fp8_gemm_impl(A, sA, W, sW, nullptr, 1, M, N, K, C, ldc, dtype, stream);
+  return fp8_gemm_impl(A, sA, W, sW, nullptr, 1, M, N, K, C, ldc, dtype, false, stream);
 }
 
 nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uint8_t* W,
@@ -1282,7 +1284,45 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uin
                                     int64_t R, int64_t N, int64_t K, void* out, int64_t ldc,
                                     int32_t dtype, void* stream) {
   if (!expert_offsets) return NVFP4_ERR_INVALID_ARG;
-  return fp8_gemm_impl(A, sA, W, sW, expert_offsets, E, R, N, K, out, ldc, dtype, stream);
+  return fp8_gemm_impl(A, sA, W, sW, expert_offsets, E, R, N, K, out, ldc, dtype, false, stream);
+}
+
+size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t K) {
+  if (rows < 0 || K < 0) return 0;
+  return static_cast<size_t>(rows) * (static_cast<size_t>(K) +
+                                      4 * static_cast<size_t>((K + 127) / 128));
+}
+
+nvfp4_status nvfp4_fp8_linear(const void* x, int64_t M, int64_t ld, int32_t dtype,
+                              const uint8_t* W, const float* sW, int64_t N, int64_t K, void* y,
+                              int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || K <= 0 || (M > 0 && !workspace)) return NVFP4_ERR_INVALID_ARG;
+  if (workspace_bytes < nvfp4_fp8_linear_workspace_bytes(M, K) || K % 16 != 0)
+    return NVFP4_ERR_UNSUPPORTED;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + M * K);
+  const nvfp4_status st =
+      nvfp4_fp8_quantize(x, M, K, ld, dtype, 0, nullptr, 1, codes, scales, M, stream);
+  if (st != NVFP4_OK) return st;
+  return fp8_gemm_impl(codes, scales, W, sW, nullptr, 1, M, N, K, y, ldy, dtype, true, stream);
+}
+
+nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, int32_t dtype,
+                                     uint32_t flags, const int32_t* route_pos, int32_t fanout,
+                                     const uint8_t* W, const float* sW,
+                                     const int32_t* expert_offsets, int32_t E, int64_t R,
+                                     int64_t N, int64_t K, void* y, int64_t ldy, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!expert_offsets || R < 0 || K <= 0 || (R > 0 && !workspace)) return NVFP4_ERR_INVALID_ARG;
+  if (workspace_bytes < nvfp4_fp8_linear_workspace_bytes(R, K) || K % 16 != 0)
+    return NVFP4_ERR_UNSUPPORTED;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + R * K);
+  const nvfp4_status st =
+      nvfp4_fp8_quantize(x, rows, K, ld, dtype, flags, route_pos, fanout, codes, scales, R, stream);
+  if (st != NVFP4_OK) return st;
+  return fp8_gemm_impl(codes, scales, W, sW, expert_offsets, E, R, N, K, y, ldy, dtype, rows > 0,
+                       stream);
 }
 
 }  // extern "C"

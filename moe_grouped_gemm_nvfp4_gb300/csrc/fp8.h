@@ -39,15 +39,17 @@ struct Fp8GemmArgs {
   void* out;                       // [rows, ldc]
   int64_t ldc;
   int32_t out_type;                // nvfp4_dtype
+  int32_t overlap;                 // start while the kernel before (the quantiser) still runs
   int* status;
   uint64_t timeout_ns;
   uint32_t debug_flags;
 };
 
-// fp8_gemm.cu: 128 weight rows x up to 128 tokens a tile.  ta: codes of the
-// activations (boxes of fp8_tile_tokens() rows x 128 bytes), tw: of the
-// weights ([E, N, K], boxes of 128 x 128).
+// fp8_gemm.cu.  ta: codes of the activations (boxes of fp8_tile_tokens() rows x
+// 128 bytes), tw: of the weights ([E, N, K], boxes of 128 x 128).
 cudaError_t init_fp8_gemm_attributes();
+// Tokens per tile (16, 32, 64 or 128) of a product over `rows` rows; E = 0: one
+// matrix.
 int fp8_tile_tokens(int64_t rows, int32_t E);
 cudaError_t launch_fp8_gemm(const CUtensorMap& ta, const CUtensorMap& tw, const Fp8GemmArgs& a,
                             int sms, cudaStream_t s);

@@ -17,44 +17,103 @@ __device__ __forceinline__ uint32_t idesc_e4m3(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] . B[smem]^T, K = 32, issued by one lane of a converged
-// warp.
-__device__ __forceinline__ void tc_mma_e4m3_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                                  uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .pred e;\n\t.reg .b32 l;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync l|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_elect(uint32_t dst, const void* tmap, uint32_t bar,
-                                                  int32_t x, int32_t y, int32_t z,
-                                                  uint64_t policy) {
+// The producer's and the MMA's loops run in one lane of their warp, picked once:
+// an elect per instruction and a vote per wait made the MMA warp the slowest
+// part of the kernel (800 cycles per K block of 256).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b32 l;\n\t"
       "elect.sync l|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}"
+      "selp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// D[tmem] = A[smem] . B[smem]^T over one K block: four K = 32 MMAs, 32 bytes
+// apart in the 128-byte swizzle.  Columns past K hold zeros.
+__device__ __forceinline__ void tc_mma_e4m3_k128(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred first, rest;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 first, 0, 0;\n\tsetp.ne.b32 rest, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, first;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, rest;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, rest;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, rest;\n\t}"
+      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int32_t x,
+                                            int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z),
          "l"(policy)
       : "memory");
 }
+// Two FP32 values in one 64-bit register, as the packed FMA takes them.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// acc += {t0, t1} * f.  volatile: not before the wait for the loads of t.
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint32_t t0, uint32_t t1, uint64_t f) {
+  asm volatile("{\n\t.reg .b64 t;\n\t"
+               "mov.b64 t, {%1, %2};\n\t"
+               "fma.rn.f32x2 %0, t, %3, %0;\n\t}"
+               : "+l"(acc) : "r"(t0), "r"(t1), "l"(f));
+}
 
-// acc += t * f on a pair of FP32 values (one instruction).
-__device__ __forceinline__ void fma_pair(float& a0, float& a1, uint32_t t0, uint32_t t1, float f0,
-                                         float f1) {
-  asm("{\n\t.reg .b64 a, t, f;\n\t"
-      "mov.b64 a, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\tmov.b64 f, {%4, %5};\n\t"
-      "fma.rn.f32x2 a, t, f, a;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1) : "r"(t0), "r"(t1), "f"(f0), "f"(f1));
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+}
+
+// Programmatic dependent launch: the GEMM may start while the quantiser before
+// it runs; it waits (until that grid has completed and its writes are visible)
+// before it touches codes or scales.  Returns at once otherwise.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One FP32 value as the output type's bits (16-bit types in the low half).
 __device__ __forceinline__ uint16_t f32_to_out16(float f, int type) {
   return type == NVFP4_FP16 ? __half_as_ushort(__float2half_rn(f)) : f32_to_bf16_rn(f);
+}
+
+// mbar_wait for waits that come once per K block: the clock is read only after
+// some tries, since the barrier usually completes within a few hundred cycles
+// and reading the global timer takes longer than that.
+__device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, CtaCtl* ctl, int* status) {
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, ctl, status);
+}
+
+// Two barriers at once: their first tries overlap.
+__device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                          uint32_t parity1, CtaCtl* ctl, int* status) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1) : "memory");
+  return ok || (wait_soon(bar0, parity0, ctl, status) && wait_soon(bar1, parity1, ctl, status));
 }
 
 // Waits for a phase regardless of the abort flag, bounded by the timeout
@@ -69,8 +128,11 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64
   return false;
 }
 
-// Work units in the order expert, weight tile, token tile (token tiles of one
-// weight tile are neighbours, so the second one finds the weights in L2).
+// Work units in the order expert, weight tile, token tile: token tiles of one
+// weight tile are neighbours, so that all but the first find the weights in L2.
+// One matrix: in groups of kTileGroup token tiles, whose activations then stay
+// in L2 while the weights pass.
+constexpr int kTileGroup = 32;
 struct UnitMap {
   const int* first;        // grouped: row offsets [E + 1] (shared memory); NULL: one matrix
   const int* tiles;        // grouped: token tiles of the experts before e [E + 1]
@@ -88,9 +150,11 @@ __device__ __forceinline__ Unit unit_at(const UnitMap& m, int u) {
   Unit r;
   if (!m.first) {
     r.e = 0;
-    r.nt = u / m.ttiles;
-    const int t = u - r.nt * m.ttiles;
-    r.row = t * m.width;
+    const int g = u / (kTileGroup * m.ntiles);            // group of token tiles
+    const int wide = min(kTileGroup, m.ttiles - g * kTileGroup);
+    const int local = u - g * kTileGroup * m.ntiles;
+    r.nt = local / wide;
+    r.row = (g * kTileGroup + local - r.nt * wide) * m.width;
     r.cnt = min(m.width, m.rows - r.row);
     return r;
   }
@@ -140,6 +204,137 @@ __device__ __forceinline__ void load_units(const int32_t* offsets, int E, int ro
     if (lane == 0) tiles[E] = base;
   }
   __syncthreads();
+}
+
+// One warp turns the scales of a unit's K blocks [kb0, kb1) into factors in
+// shared memory, sa[row] * sw for ROWS tokens, one set per accumulator buffer;
+// `put(b, phase)` waits until the buffer is free, `done(b)` tells the epilogue.
+// kAhead K blocks' loads are on their way while the group before is written: an
+// L2 read takes longer than a K block.
+constexpr int kAhead = 4;
+template <int ROWS, int BUFS, class Put, class Done>
+__device__ __forceinline__ bool factor_unit(const Fp8GemmArgs& a, const Unit& un, int kb0, int kb1,
+                                            uint32_t fac, int lane, int& buf, uint32_t& phase,
+                                            Put put, Done done) {
+  constexpr int kPer = (ROWS + 31) / 32;
+  const float* sw = a.sw + (static_cast<int64_t>(un.e) * a.nnb + un.nt) * a.nkb;
+  const float* sa = a.sa + kb0 * a.lds + un.row + lane;
+  const int rows = un.cnt - lane;                // rows of this lane: 32 * i < rows
+  float na[kAhead][kPer], nw[kAhead];
+  auto fetch = [&](int kb) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const bool in = kb + j < kb1;
+      nw[j] = in ? __ldg(sw + kb + j) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) na[j][i] = in && 32 * i < rows ? __ldg(sa + 32 * i) : 0.f;
+      sa += a.lds;
+    }
+  };
+  fetch(kb0);
+  for (int kb = kb0; kb < kb1; kb += kAhead) {
+    float f[kAhead][kPer];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) f[j][i] = na[j][i] * nw[j];
+    fetch(kb + kAhead);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (kb + j >= kb1) break;
+      if (!put(buf, phase)) return false;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) st_shared_f32(fac + 4 * (buf * 128 + lane + 32 * i), f[j][i]);
+      __syncwarp();
+      if (lane == 0) done(buf);
+      if (++buf == BUFS) { buf = 0; phase ^= 1u; }
+    }
+  }
+  return true;
+}
+
+// n K blocks of one unit added into acc (COLS FP32 values, packed in pairs),
+// 32 columns at a time, the next 32 on their way meanwhile.  `wait(b, phase)`
+// waits for buffer b's sums and factors (false: give up), `factor(b)` is this
+// thread's factor, `release(b)` hands the buffer back; buf and phase run on from
+// unit to unit.  False after a wait that gave up.
+template <int COLS, int BUFS, class Wait, class Factor, class Release>
+__device__ __forceinline__ bool add_unit(uint64_t (&acc)[COLS / 2], int n, uint32_t tbase,
+                                         int& buf, uint32_t& phase, Wait wait, Factor factor,
+                                         Release release) {
+  static_assert(COLS % 64 == 0, "the next block starts at r[0] again");
+  uint32_t r[2][32];
+  if (!wait(buf, phase)) return false;
+  tmem_ld32(tbase + buf * 128, r[0]);
+  float f = factor(buf);
+  for (int kb = 0; kb < n; ++kb) {
+    const uint32_t taddr = tbase + buf * 128;
+    const uint64_t ff = pack2(f, f);
+#pragma unroll
+    for (int c = 0; c < COLS / 32; ++c) {
+      tmem_ld_wait();
+      if (c + 1 < COLS / 32) {
+        tmem_ld32(taddr + 32 * (c + 1), r[(c + 1) & 1]);
+      } else {
+        release(buf);
+        if (++buf == BUFS) { buf = 0; phase ^= 1u; }
+        if (kb + 1 < n) {
+          if (!wait(buf, phase)) return false;
+          tmem_ld32(tbase + buf * 128, r[0]);
+          f = factor(buf);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        fma_pair(acc[(c * 32 + i) / 2], r[c & 1][i], r[c & 1][i + 1], ff);
+    }
+  }
+  return true;
+}
+
+// COLS neighbouring outputs of one row (those before column N).
+template <int COLS>
+__device__ __forceinline__ void store_row(const Fp8GemmArgs& a, int row, int n0,
+                                          const uint64_t (&acc2)[COLS / 2]) {
+  const int n = a.N - n0;
+  if (n <= 0) return;
+  float acc[COLS];
+#pragma unroll
+  for (int i = 0; i < COLS / 2; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
+  const int64_t at = static_cast<int64_t>(row) * a.ldc + n0;
+  if (a.out_type == NVFP4_FP32) {
+    float* dst = static_cast<float*>(a.out) + at;
+    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < COLS; i += 4) {
+      if (vec && i + 4 <= n) {
+        *reinterpret_cast<float4*>(dst + i) =
+            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < n) dst[i + j] = acc[i + j];
+      }
+    }
+  } else {
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + at;
+    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < COLS; i += 8) {
+      uint16_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = f32_to_out16(acc[i + j], a.out_type);
+      if (vec && i + 8 <= n) {
+        *reinterpret_cast<uint4*>(dst + i) =
+            make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                       h[6] | (h[7] << 16));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < n) dst[i + j] = h[j];
+      }
+    }
+  }
 }
 
 // Zeros the output rows from `first` on (routes that no expert took); one

@@ -54,6 +54,8 @@ struct BlockScale {
 
 template <int DT, bool SILU>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantArgs a, int chunks) {
+  // a GEMM launched to overlap this kernel may take its place on the SMs
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t row = task / chunks;

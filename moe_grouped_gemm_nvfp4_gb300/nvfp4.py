@@ -93,6 +93,11 @@ _SIGS = {
     "nvfp4_fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P]),
     "nvfp4_fp8_grouped_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _P,
                                               _I64, _I32, _P]),
+    "nvfp4_fp8_linear_workspace_bytes": (_SZ, [_I64, _I64]),
+    "nvfp4_fp8_linear": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _P, _I64, _I64, _P, _I64, _P,
+                                        _SZ, _P]),
+    "nvfp4_fp8_expert_linear": (ctypes.c_int, [_P, _I64, _I64, _I32, _U32, _P, _I32, _P, _P, _P,
+                                               _I32, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P]),
     "nvfp4_grouped_gemm_combine_noalloc": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I32,
                                                           _I64, _I64, _P, _P, _P, _P, _P]),
 }
@@ -142,6 +147,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized():      # the handle without a Stream object (3 us less)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -437,6 +444,30 @@ def nvfp4_fp8_grouped_gemm(A, sA, W, sW, expert_offsets, out, stream=None) -> No
     _check("nvfp4_fp8_grouped_gemm", load().nvfp4_fp8_grouped_gemm(
         _ptr(A), _ptr(sA), _ptr(W), _ptr(sW), _ptr(expert_offsets), E, R, N, K, _ptr(out),
         _row_stride(out), _dtype(out), _stream(stream)))
+
+
+def nvfp4_fp8_linear_workspace_bytes(rows: int, K: int) -> int:
+    return load().nvfp4_fp8_linear_workspace_bytes(rows, K)
+
+
+def nvfp4_fp8_linear(x, W, sW, y, workspace, stream=None) -> None:
+    """y [M, N] = x . (W, sW)^T with x quantised into the workspace (uint8)."""
+    M, K = x.shape
+    _check("nvfp4_fp8_linear", load().nvfp4_fp8_linear(
+        _ptr(x), M, _row_stride(x), _dtype(x), _ptr(W), _ptr(sW), W.shape[0], K, _ptr(y),
+        _row_stride(y), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def nvfp4_fp8_expert_linear(x, W, sW, expert_offsets, y, workspace, flags: int = 0,
+                            route_pos=None, stream=None) -> None:
+    """y [R, N]: the routes' rows times their expert's weights, x quantised into
+    the workspace (uint8) in route order."""
+    E, N, K = W.shape
+    fanout = 1 if route_pos is None else route_pos.shape[1]
+    _check("nvfp4_fp8_expert_linear", load().nvfp4_fp8_expert_linear(
+        _ptr(x), x.shape[0], _row_stride(x), _dtype(x), flags, _ptr(route_pos), fanout, _ptr(W),
+        _ptr(sW), _ptr(expert_offsets), E, y.shape[0], N, K, _ptr(y), _row_stride(y),
+        _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 # ------------------------------------------- allocating conveniences (torch)

@@ -17,8 +17,6 @@ The arithmetic runs in the CUDA kernels; sums are FP32 in a fixed order.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import nvfp4 as F
@@ -26,24 +24,33 @@ from . import nvfp4 as F
 
 def on_stream(stream):
     """Context in which torch allocates for `stream` (a torch stream or a raw
-    handle; None: the current one), so that memory freed on return is reused in
-    that stream's order."""
-    if stream is None:
-        return contextlib.nullcontext()
+    handle), so that memory freed on return is reused in that stream's order."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
 
 
-def rows_of(t, name):
+def empty(shape, dtype, device, stream=None):
+    """torch.empty in the order of `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rows_of(t, name, stream=None):
     """t as rows whose elements are neighbours (a copy only where they are not)."""
     if t.dim() != 2:
         raise ValueError(f"{name}: expected rows [n, D], got shape {tuple(t.shape)}")
-    if t.shape[1] == 0:
-        raise ValueError(f"{name}: rows of width 0")
     n, D = t.shape
-    if (D > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < D):
-        return t.contiguous()
+    if D == 0:
+        raise ValueError(f"{name}: rows of width 0")
+    ld, step = t.stride()
+    if (D > 1 and step != 1) or (n > 1 and ld < D):
+        if stream is None:
+            return t.contiguous()
+        with on_stream(stream):
+            return t.contiguous()
     return t
 
 
@@ -56,21 +63,23 @@ def check_routes(route_pos, expert_offsets=None):
         raise ValueError("expert_offsets: expected contiguous int32 [E + 1]")
 
 
-def _check_weights(weights, route_pos):
+def _weights(weights, route_pos, stream=None):
     if weights.shape != route_pos.shape or weights.dtype != torch.float32:
         raise ValueError("weights: expected FP32 of route_pos' shape")
+    if stream is None or weights.is_contiguous():
+        return weights.contiguous()
+    with on_stream(stream):
+        return weights.contiguous()
 
 
 def _dispatch(x, route_pos, expert_offsets, R, stream=None):
-    with on_stream(stream):
-        out = torch.empty((R, x.shape[1]), dtype=x.dtype, device=x.device)
+    out = empty((R, x.shape[1]), x.dtype, x.device, stream)
     F.nvfp4_tokens_dispatch(x, route_pos, expert_offsets, out, stream)
     return out
 
 
 def _combine(y, route_pos, weights, stream=None):
-    with on_stream(stream):
-        out = torch.empty((route_pos.shape[0], y.shape[1]), dtype=y.dtype, device=y.device)
+    out = empty((route_pos.shape[0], y.shape[1]), y.dtype, y.device, stream)
     F.nvfp4_tokens_combine(y, route_pos, weights, out, stream)
     return out
 
@@ -108,7 +117,7 @@ def dispatch(x, route_pos, expert_offsets=None, R=None, stream=None):
     past expert_offsets[E] are zero; without expert_offsets, rows that no route
     names are left unwritten."""
     check_routes(route_pos, expert_offsets)
-    x = rows_of(x, "x")
+    x = rows_of(x, "x", stream)
     if x.shape[0] != route_pos.shape[0]:
         raise ValueError(f"{x.shape[0]} rows for the routes of {route_pos.shape[0]} tokens")
     R = route_pos.numel() if R is None else R
@@ -121,7 +130,7 @@ def dispatch_grad(dout, route_pos, stream=None):
     """Gradient of `dispatch`: dout [R, D] -> [T, D], the sum over each token's
     routes."""
     check_routes(route_pos)
-    return _combine(rows_of(dout, "dout"), route_pos, None, stream)
+    return _combine(rows_of(dout, "dout", stream), route_pos, None, stream)
 
 
 def combine(y, route_pos, weights=None, expert_offsets=None, stream=None):
@@ -129,10 +138,9 @@ def combine(y, route_pos, weights=None, expert_offsets=None, stream=None):
     weights (FP32 [T, topk]) where given.  expert_offsets is used by the
     backward pass alone: the gradient's rows past expert_offsets[E] are zero."""
     check_routes(route_pos, expert_offsets)
-    y = rows_of(y, "y")
+    y = rows_of(y, "y", stream)
     if weights is not None:
-        _check_weights(weights, route_pos)
-        weights = weights.contiguous()
+        weights = _weights(weights, route_pos, stream)
     if stream is None and torch.is_grad_enabled() and (
             y.requires_grad or (weights is not None and weights.requires_grad)):
         if weights is None:
@@ -146,13 +154,11 @@ def combine_grad(dout, y, route_pos, weights, expert_offsets=None, stream=None):
     past expert_offsets[E] are zero; without expert_offsets, rows that no route
     names are left unwritten."""
     check_routes(route_pos, expert_offsets)
-    _check_weights(weights, route_pos)
-    dout, y = rows_of(dout, "dout"), rows_of(y, "y")
+    weights = _weights(weights, route_pos, stream)
+    dout, y = rows_of(dout, "dout", stream), rows_of(y, "y", stream)
     if dout.shape != (route_pos.shape[0], y.shape[1]) or dout.dtype != y.dtype:
         raise ValueError("dout: expected [T, D] of y's width and type")
-    with on_stream(stream):
-        weights = weights.contiguous()
-        dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
-        dw = torch.empty(route_pos.shape, dtype=torch.float32, device=y.device)
+    dy = empty(y.shape, y.dtype, y.device, stream)
+    dw = empty(route_pos.shape, torch.float32, y.device, stream)
     F.nvfp4_tokens_combine_grad(dout, y, route_pos, weights, expert_offsets, dy, dw, stream)
     return dy, dw
