@@ -1,15 +1,20 @@
-"""Builds the in-tree CUDA library `_lib/libnvfp4_gb300.so` for sm_103a.
+"""Builds the in-tree CUDA library `_lib/libnvfp4_gb300.so` for sm_103a and the
+native Python binding `_lib/_binding-<torch version>.so` of its hot calls.
 
 The translation units compile in parallel with nvcc, then link into
-one shared object with the CUDA runtime linked statically.  A build is
-skipped when the library is newer than every source and header.
+one shared object with the CUDA runtime linked statically; the binding is one
+C++ file against torch's headers.  A build is skipped when its output is newer
+than every source and header.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -34,6 +39,10 @@ NVCC_FLAGS = [
 ]
 
 
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(OUT_DIR, f"_binding-{torch.__version__}.so")
+
+
 def _nvcc() -> str:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     cand = os.path.join(cuda, "bin", "nvcc")
@@ -48,11 +57,49 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_stale() -> bool:
+    if not os.path.exists(BINDING_PATH):
+        return True
+    t = os.path.getmtime(BINDING_PATH)
+    return any(os.path.getmtime(d) > t
+               for d in (BINDING_SOURCE, os.path.join(ROOT, "include", "nvfp4.h")))
+
+
+def _build_binding(verbose: bool) -> None:
+    """g++ against torch's headers.  The C entry points stay undefined here: the
+    library is loaded first, with its symbols visible."""
+    base = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           *(f"-I{d}" for d in (os.path.join(base, "include"),
+                                os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                                sysconfig.get_paths()["include"], os.path.join(cuda, "include"))),
+           BINDING_SOURCE, "-o", tmp, f"-L{os.path.join(base, 'lib')}",
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles the library if needed and returns its path."""
-    if not force and not _stale():
-        return LIB_PATH
-    os.makedirs(OUT_DIR, exist_ok=True)
+    """Compiles the library and the binding if needed; returns the library's path."""
+    lib, binding = force or _stale(), force or _binding_stale()
+    if lib or binding:
+        os.makedirs(OUT_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        job = ex.submit(_build_binding, verbose) if binding else None
+        if lib:
+            _build_library(verbose)
+        if job is not None:
+            job.result()
+    return LIB_PATH
+
+
+def _build_library(verbose: bool) -> None:
     nvcc = _nvcc()
     objs = [os.path.join(OUT_DIR, s.replace(".cu", ".o")) for s in SOURCES]
 
@@ -76,7 +123,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -8,6 +8,8 @@ raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -15,6 +17,7 @@ import torch
 from . import build as _build
 
 _lib = None
+_native = None
 
 NVFP4_OK = 0
 NVFP4_ERR_INVALID_ARG = 1
@@ -120,13 +123,31 @@ def load() -> ctypes.CDLL:
         path = _build.build()
         if not os.path.exists(path):
             raise RuntimeError(f"NVFP4 CUDA library missing: {path}")
-        lib = ctypes.CDLL(path)
+        # global symbols: the native binding's C entry points are these
+        lib = ctypes.CDLL(path, mode=ctypes.RTLD_GLOBAL)
         for name, (res, args) in _SIGS.items():
             f = getattr(lib, name)
             f.restype = res
             f.argtypes = args
         _lib = lib
     return _lib
+
+
+def native():
+    """The native binding (csrc/binding.cpp): checks, output allocation and the C
+    call of the hot entry points in one native function each, on the current
+    stream."""
+    global _native
+    if _native is None:
+        load()
+        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_binding", _build.BINDING_PATH,
+                                                      loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.set_error(NVFP4Error)
+        _native = module
+    return _native
 
 
 def _row_stride(x):
