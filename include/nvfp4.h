@@ -572,9 +572,9 @@ nvfp4_status nvfp4_decode_attention(const void* q, const uint8_t* k_packed,
  * live positions are distinct.  A position >= R is skipped and recorded as
  * NVFP4_ERR_DEVICE_CHECK.  expert_offsets, where given, is nvfp4_moe_route's
  * [E + 1]: the rows from expert_offsets[E] on belong to no route and are set
- * to zero; NULL leaves rows without a route unwritten.  D >= 1 and any row
- * stride >= D; rows whose base, stride and width are multiples of 16 bytes
- * move by 16-byte accesses, others by element.  Sums are FP32 in a fixed
+ * to zero; NULL leaves rows without a route unwritten.  1 <= D <= 2^28 and any
+ * row stride >= D; rows whose base, stride and width are multiples of 16 bytes
+ * move fastest.  Sums are FP32 in a fixed
  * order (k ascending), rounded once: results repeat bit for bit.
  * ------------------------------------------------------------------------ */
 typedef enum nvfp4_dtype { NVFP4_BF16 = 0, NVFP4_FP16 = 1, NVFP4_FP32 = 2 } nvfp4_dtype;

@@ -1128,7 +1128,7 @@ nvfp4_status nvfp4_tokens_dispatch(const void* x, int64_t ld, const int32_t* rou
   if (expert_offsets && E <= 0) return NVFP4_ERR_INVALID_ARG;
   if ((T > 0 && (!x || !route_pos)) || (R > 0 && !out)) return NVFP4_ERR_INVALID_ARG;
   const unsigned es = dtype_bytes(dtype);
-  if (R > 0x7FFFFFFFLL || !aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(route_pos, 4) ||
+  if (R > 0x7FFFFFFFLL || D > (1LL << 28) || !aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(route_pos, 4) ||
       !aligned_to(expert_offsets, 4))
     return NVFP4_ERR_UNSUPPORTED;
   DeviceState* d = nullptr;
@@ -1143,7 +1143,7 @@ nvfp4_status nvfp4_tokens_dispatch(const void* x, int64_t ld, const int32_t* rou
   a.out = out;
   a.T = T;
   a.R = R;
-  a.D = D;
+  a.D = static_cast<int32_t>(D);
   a.topk = topk;
   a.status = d->status;
   const cudaError_t e = nvfp4::launch_tokens_dispatch(a, dtype, static_cast<cudaStream_t>(stream));
@@ -1158,7 +1158,7 @@ nvfp4_status nvfp4_tokens_combine(const void* y, int64_t ld, const int32_t* rout
     return NVFP4_ERR_INVALID_ARG;
   if (T > 0 && (!route_pos || !out || (R > 0 && !y))) return NVFP4_ERR_INVALID_ARG;
   const unsigned es = dtype_bytes(dtype);
-  if (R > 0x7FFFFFFFLL || !aligned_to(y, es) || !aligned_to(out, es) || !aligned_to(route_pos, 4) ||
+  if (R > 0x7FFFFFFFLL || D > (1LL << 28) || !aligned_to(y, es) || !aligned_to(out, es) || !aligned_to(route_pos, 4) ||
       !aligned_to(weights, 4))
     return NVFP4_ERR_UNSUPPORTED;
   DeviceState* d = nullptr;
@@ -1173,7 +1173,7 @@ nvfp4_status nvfp4_tokens_combine(const void* y, int64_t ld, const int32_t* rout
   a.out = out;
   a.T = T;
   a.R = R;
-  a.D = D;
+  a.D = static_cast<int32_t>(D);
   a.topk = topk;
   a.status = d->status;
   const cudaError_t e = nvfp4::launch_tokens_combine(a, dtype, static_cast<cudaStream_t>(stream));
@@ -1192,7 +1192,7 @@ nvfp4_status nvfp4_tokens_combine_grad(const void* dout, int64_t ld, const void*
   if ((T > 0 && (!dout || !route_pos || !weights || !dw)) || (R > 0 && (!y || !dy)))
     return NVFP4_ERR_INVALID_ARG;
   const unsigned es = dtype_bytes(dtype);
-  if (R > 0x7FFFFFFFLL || !aligned_to(dout, es) || !aligned_to(y, es) || !aligned_to(dy, es) ||
+  if (R > 0x7FFFFFFFLL || D > (1LL << 28) || !aligned_to(dout, es) || !aligned_to(y, es) || !aligned_to(dy, es) ||
       !aligned_to(route_pos, 4) || !aligned_to(weights, 4) || !aligned_to(dw, 4) ||
       !aligned_to(expert_offsets, 4))
     return NVFP4_ERR_UNSUPPORTED;
@@ -1211,7 +1211,7 @@ nvfp4_status nvfp4_tokens_combine_grad(const void* dout, int64_t ld, const void*
   a.dw = dw;
   a.T = T;
   a.R = R;
-  a.D = D;
+  a.D = static_cast<int32_t>(D);
   a.topk = topk;
   a.status = d->status;
   const cudaError_t e =

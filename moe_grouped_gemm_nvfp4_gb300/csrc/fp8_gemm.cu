@@ -51,8 +51,9 @@ struct Cfg {
   static constexpr int kBarBytes = 8 * (2 * kStages + 2 * kBufs + 1);
   static constexpr int kCtlOffset = kBarOffset + kBarBytes;
   static constexpr int kSmemBytes = kCtlOffset + 64 + 1024;   // + alignment slack
-  // K-split sums: a row of 128 columns per token, one word of padding
-  static constexpr int kRedStride = 129;
+  // K-split sums: a row of 128 columns per token, four words of padding (rows of
+  // neighbouring lanes then lie in different banks for 16-byte accesses)
+  static constexpr int kRedStride = 132;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(NT * kRedStride * 4 <= kStages * kStageBytes, "the K-split sums reuse the stages");
 };
@@ -63,9 +64,10 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
@@ -272,9 +274,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       if constexpr (SPLIT) {
         // every MMA and copy of this CTA has completed: the stages are free
         if (row < NT) {
-          float* red = reinterpret_cast<float*>(smem) + row * C::kRedStride + c0;
+          float4* red =
+              reinterpret_cast<float4*>(smem + 4 * (row * C::kRedStride + c0));
 #pragma unroll
-          for (int i = 0; i < C::kCols / 2; ++i) unpack2(acc[i], red[2 * i], red[2 * i + 1]);
+          for (int i = 0; i < C::kCols / 4; ++i) {
+            float4 v;
+            unpack2(acc[2 * i], v.x, v.y);
+            unpack2(acc[2 * i + 1], v.z, v.w);
+            red[i] = v;
+          }
         }
       } else if (row < un.cnt) {
         store_row<C::kCols>(a, un.row + row, un.nt * 128 + c0, acc);
@@ -286,15 +294,39 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     __syncwarp();
     cluster_sync_all();
     if (u0 < units) {
-      // each CTA adds up the ranks' sums of its share of the tokens
+      // each CTA adds up the ranks' sums of its share of the tokens, four columns
+      // a thread; the reads of other CTAs take long, so those of two tokens and
+      // all ranks are in flight together
       const Unit un = unit_at(um, u0);
-      const int n = threadIdx.x & 127;
-      for (int t = rank + nsplit * static_cast<int>(threadIdx.x >> 7); t < un.cnt;
-           t += nsplit * (C::kThreads / 128)) {
-        float v = 0.f;
-        for (int j = 0; j < nsplit; ++j)
-          v += ld_cluster_f32(mapa_shared(sbase + (t * C::kRedStride + n) * 4, j));
-        if (un.nt * 128 + n < a.N) store_out(a, un.row + t, un.nt * 128 + n, v);
+      const int n = 4 * (threadIdx.x & 31);
+      constexpr int kGroups = C::kThreads / 32;
+      constexpr int kTogether = 2, kRanks = 8;
+      const int step = nsplit * kGroups;
+      for (int t0 = rank + nsplit * static_cast<int>(threadIdx.x >> 5); t0 < un.cnt;
+           t0 += kTogether * step) {
+        float4 v[kTogether][kRanks];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+          for (int j = 0; j < kRanks; ++j)
+            v[i][j] = j < nsplit && t0 + i * step < un.cnt
+                          ? ld_cluster_f4(mapa_shared(
+                                sbase + 4 * ((t0 + i * step) * C::kRedStride + n), j))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          if (t0 + i * step >= un.cnt) break;
+          float4 o = v[i][0];
+#pragma unroll
+          for (int j = 1; j < kRanks; ++j) {
+            o.x += v[i][j].x; o.y += v[i][j].y; o.z += v[i][j].z; o.w += v[i][j].w;
+          }
+          const int row = un.row + t0 + i * step, col = un.nt * 128 + n;
+          if (col < a.N) store_out(a, row, col, o.x);
+          if (col + 1 < a.N) store_out(a, row, col + 1, o.y);
+          if (col + 2 < a.N) store_out(a, row, col + 2, o.z);
+          if (col + 3 < a.N) store_out(a, row, col + 3, o.w);
+        }
       }
     }
     cluster_sync_all();

@@ -16,7 +16,8 @@ struct TokensArgs {
   const int32_t* live;             // rows [*live, R) of the output are zeroed; NULL: none
   void* out;                       // dispatch: [R, D]; combine: [T, D]; grad: dy [R, D]
   float* dw;                       // grad: [T, topk]
-  int64_t T, R, D;
+  int64_t T, R;
+  int32_t D;
   int32_t topk;
   int* status;
 };

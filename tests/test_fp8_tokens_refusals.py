@@ -33,6 +33,7 @@ def test_tokens_refusals():
                     dict(dt=-1), dict(pos=None)):
             assert call(**bad) == inv, (call, bad)
         assert call(R=1 << 31) == uns
+        assert call(D=(1 << 28) + 1, ld=1 << 29, **({"ldy": 1 << 29} if call is grad else {})) == uns
     assert dispatch(x=None) == inv and dispatch(out=None) == inv and dispatch(E=0) == inv
     assert combine(y=None) == inv and combine(out=None) == inv
     for name in ("d", "y", "w", "dy", "dw"):
