@@ -24,11 +24,12 @@ LIB_PATH = os.path.join(OUT_DIR, "libnvfp4_gb300.so")
 SOURCES = ["api.cu", "quantize.cu", "route.cu", "gemm.cu", "gemm_pair.cu", "gemm_pair_grouped.cu",
            "sparse.cu",
            "attention.cu", "attention_tc.cu", "attention_tc_wide.cu",
-           "tokens.cu", "fp8_quantize.cu", "fp8_gemm.cu"]
+           "tokens.cu", "fp8_quantize.cu", "fp8_gemm.cu",
+           "fp8_rows.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "format.cuh", "attention.h",
                                                 "attention_tc_common.cuh",
                                                 "rows.cuh", "tokens.h", "fp8.h",
-                                                "fp8_common.cuh")] + [
+                                                "fp8_common.cuh", "fp8_quant.cuh")] + [
     os.path.join(ROOT, "include", "nvfp4.h")]
 
 NVCC_FLAGS = [

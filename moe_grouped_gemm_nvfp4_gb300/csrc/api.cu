@@ -67,6 +67,7 @@ nvfp4_status device_state(DeviceState** out) {
       if (nvfp4::init_attention_tc_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_route_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_fp8_gemm_attributes() != cudaSuccess) return cuda_fail();
+      if (nvfp4::init_fp8_rows_attributes() != cudaSuccess) return cuda_fail();
     }
     if (!g_encode) {
       void* fn = nullptr;
@@ -210,9 +211,47 @@ bool is_dtype(int32_t t) { return t == NVFP4_BF16 || t == NVFP4_FP16 || t == NVF
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 unsigned dtype_bytes(int32_t t) { return t == NVFP4_FP32 ? 4u : 2u; }
 
-nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
-                           const int32_t* offsets, int32_t E, int64_t rows, int64_t N, int64_t K,
-                           void* out, int64_t ldc, int32_t dtype, bool overlap, void* stream) {
+nvfp4_status check_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                            uint32_t flags, const int32_t* route_pos, int32_t fanout,
+                            const uint8_t* codes, const float* scales, int64_t out_rows) {
+  const int64_t width = (flags & NVFP4_FP8_SILU_MUL) ? 2 * cols : cols;
+  if (rows < 0 || cols <= 0 || ld < width || fanout <= 0 || out_rows < 0 || !is_dtype(dtype) ||
+      (flags & ~NVFP4_FP8_SILU_MUL))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!route_pos && (fanout != 1 || out_rows != rows)) return NVFP4_ERR_INVALID_ARG;
+  if ((rows > 0 && !x) || (out_rows > 0 && (!codes || !scales))) return NVFP4_ERR_INVALID_ARG;
+  if (dtype == NVFP4_FP32 || cols % 16 != 0 || ld % 8 != 0 || out_rows > 0x7FFFFFFFLL ||
+      cols > (1LL << 30) || !aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4) ||
+      !aligned_to(route_pos, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+nvfp4_status fp8_quantize_impl(DeviceState* d, const void* x, int64_t rows, int64_t cols,
+                               int64_t ld, int32_t dtype, uint32_t flags, const int32_t* route_pos,
+                               int32_t fanout, uint8_t* codes, float* scales, int64_t out_rows,
+                               void* stream) {
+  if (rows == 0 || out_rows == 0) return NVFP4_OK;
+  nvfp4::Fp8QuantArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.route_pos = route_pos;
+  a.fanout = fanout;
+  a.silu = (flags & NVFP4_FP8_SILU_MUL) ? 1 : 0;
+  a.codes = codes;
+  a.scales = scales;
+  a.out_rows = out_rows;
+  a.status = d->status;
+  const cudaError_t e = nvfp4::launch_fp8_quantize(a, dtype, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+nvfp4_status check_gemm(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
+                        const int32_t* offsets, int32_t E, int64_t rows, int64_t N, int64_t K,
+                        const void* out, int64_t ldc, int32_t dtype) {
   if (!is_dtype(dtype) || E <= 0 || rows < 0 || N <= 0 || K <= 0 || ldc < N)
     return NVFP4_ERR_INVALID_ARG;
   if (!W || !sW || (rows > 0 && (!A || !sA || !out))) return NVFP4_ERR_INVALID_ARG;
@@ -222,9 +261,13 @@ nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, 
   if (!aligned16(A) || !aligned16(W) || !aligned_to(sA, 4) || !aligned_to(sW, 4) ||
       !aligned_to(offsets, 4) || !aligned_to(out, dtype_bytes(dtype)))
     return NVFP4_ERR_UNSUPPORTED;
-  DeviceState* d = nullptr;
-  const nvfp4_status st = device_state(&d);
-  if (st != NVFP4_OK) return st;
+  return NVFP4_OK;
+}
+
+nvfp4_status fp8_gemm_impl(DeviceState* d, const uint8_t* A, const float* sA, const uint8_t* W,
+                           const float* sW, const int32_t* offsets, int32_t E, int64_t rows,
+                           int64_t N, int64_t K, void* out, int64_t ldc, int32_t dtype,
+                           bool overlap, void* stream) {
   if (rows == 0) return NVFP4_OK;
   nvfp4::Fp8GemmArgs a{};
   a.sa = sA;
@@ -253,6 +296,67 @@ nvfp4_status fp8_gemm_impl(const uint8_t* A, const float* sA, const uint8_t* W, 
       nvfp4::launch_fp8_gemm(ta, tw, a, d->sms, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
   return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+// Quantise and multiply: few rows in one launch, others by the quantiser and the
+// tensor-core GEMM, which starts while the quantiser runs.
+nvfp4_status fp8_linear_impl(const void* x, int64_t rows, int64_t ld, int32_t dtype, uint32_t flags,
+                             const int32_t* route_pos, int32_t fanout, const uint8_t* W,
+                             const float* sW, const int32_t* offsets, int32_t E, int64_t R,
+                             int64_t N, int64_t K, void* y, int64_t ldy, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (R < 0 || K <= 0 || (R > 0 && !workspace)) return NVFP4_ERR_INVALID_ARG;
+  if (workspace_bytes < nvfp4_fp8_linear_workspace_bytes(R, K)) return NVFP4_ERR_UNSUPPORTED;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + R * K);
+  nvfp4_status st = check_quantize(x, rows, K, ld, dtype, flags, route_pos, fanout, codes, scales, R);
+  if (st == NVFP4_OK) st = check_gemm(codes, scales, W, sW, offsets, E, R, N, K, y, ldy, dtype);
+  if (st != NVFP4_OK) return st;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (R == 0) return NVFP4_OK;
+  const int64_t n_pos = route_pos ? rows * fanout : 0;
+  if (rows > 0 && nvfp4::fp8_few_rows(R, n_pos, N, K, offsets != nullptr)) {
+    nvfp4::Fp8RowsArgs a{};
+    a.x = x;
+    a.ld = ld;
+    a.silu = (flags & NVFP4_FP8_SILU_MUL) ? 1 : 0;
+    a.route_pos = route_pos;
+    a.n_pos = static_cast<int32_t>(n_pos);
+    a.fanout = fanout;
+    a.w = W;
+    a.sw = sW;
+    a.offsets = offsets;
+    a.E = E;
+    a.R = static_cast<int32_t>(R);
+    a.N = static_cast<int32_t>(N);
+    a.K = static_cast<int32_t>(K);
+    a.nkb = static_cast<int32_t>((K + 127) / 128);
+    a.nnb = static_cast<int32_t>((N + 127) / 128);
+    a.out = y;
+    a.ldc = ldy;
+    a.status = d->status;
+    return nvfp4::launch_fp8_rows(a, dtype, d->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? NVFP4_OK
+               : cuda_fail();
+  }
+  st = fp8_quantize_impl(d, x, rows, K, ld, dtype, flags, route_pos, fanout, codes, scales, R,
+                         stream);
+  if (st != NVFP4_OK) return st;
+  return fp8_gemm_impl(d, codes, scales, W, sW, offsets, E, R, N, K, y, ldy, dtype, rows > 0,
+                       stream);
+}
+
+nvfp4_status fp8_gemm_checked(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
+                              const int32_t* offsets, int32_t E, int64_t rows, int64_t N,
+                              int64_t K, void* out, int64_t ldc, int32_t dtype, void* stream) {
+  const nvfp4_status bad = check_gemm(A, sA, W, sW, offsets, E, rows, N, K, out, ldc, dtype);
+  if (bad != NVFP4_OK) return bad;
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  return fp8_gemm_impl(d, A, sA, W, sW, offsets, E, rows, N, K, out, ldc, dtype, false, stream);
 }
 
 }  // namespace
@@ -1226,35 +1330,14 @@ nvfp4_status nvfp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64
                                 int32_t dtype, uint32_t flags, const int32_t* route_pos,
                                 int32_t fanout, uint8_t* codes, float* scales, int64_t out_rows,
                                 void* stream) {
-  const int64_t width = (flags & NVFP4_FP8_SILU_MUL) ? 2 * cols : cols;
-  if (rows < 0 || cols <= 0 || ld < width || fanout <= 0 || out_rows < 0 || !is_dtype(dtype) ||
-      (flags & ~NVFP4_FP8_SILU_MUL))
-    return NVFP4_ERR_INVALID_ARG;
-  if (!route_pos && (fanout != 1 || out_rows != rows)) return NVFP4_ERR_INVALID_ARG;
-  if ((rows > 0 && !x) || (out_rows > 0 && (!codes || !scales))) return NVFP4_ERR_INVALID_ARG;
-  if (dtype == NVFP4_FP32 || cols % 16 != 0 || ld % 8 != 0 || out_rows > 0x7FFFFFFFLL ||
-      cols > (1LL << 30) || !aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4) ||
-      !aligned_to(route_pos, 4))
-    return NVFP4_ERR_UNSUPPORTED;
+  const nvfp4_status bad =
+      check_quantize(x, rows, cols, ld, dtype, flags, route_pos, fanout, codes, scales, out_rows);
+  if (bad != NVFP4_OK) return bad;
   DeviceState* d = nullptr;
   const nvfp4_status st = device_state(&d);
   if (st != NVFP4_OK) return st;
-  if (rows == 0 || out_rows == 0) return NVFP4_OK;
-  nvfp4::Fp8QuantArgs a{};
-  a.x = x;
-  a.rows = rows;
-  a.cols = cols;
-  a.ld = ld;
-  a.route_pos = route_pos;
-  a.fanout = fanout;
-  a.silu = (flags & NVFP4_FP8_SILU_MUL) ? 1 : 0;
-  a.codes = codes;
-  a.scales = scales;
-  a.out_rows = out_rows;
-  a.status = d->status;
-  const cudaError_t e = nvfp4::launch_fp8_quantize(a, dtype, static_cast<cudaStream_t>(stream));
-  if (e == cudaErrorInvalidConfiguration) return NVFP4_ERR_UNSUPPORTED;
-  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+  return fp8_quantize_impl(d, x, rows, cols, ld, dtype, flags, route_pos, fanout, codes, scales,
+                           out_rows, stream);
 }
 
 nvfp4_status nvfp4_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K,
@@ -1276,7 +1359,7 @@ nvfp4_status nvfp4_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int
 nvfp4_status nvfp4_fp8_gemm(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
                             void* C, int64_t M, int64_t N, int64_t K, int64_t ldc, int32_t dtype,
                             void* stream) {
-  return fp8_gemm_impl(A, sA, W, sW, nullptr, 1, M, N, K, C, ldc, dtype, false, stream);
+  return fp8_gemm_checked(A, sA, W, sW, nullptr, 1, M, N, K, C, ldc, dtype, stream);
 }
 
 nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uint8_t* W,
@@ -1284,7 +1367,7 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uin
                                     int64_t R, int64_t N, int64_t K, void* out, int64_t ldc,
                                     int32_t dtype, void* stream) {
   if (!expert_offsets) return NVFP4_ERR_INVALID_ARG;
-  return fp8_gemm_impl(A, sA, W, sW, expert_offsets, E, R, N, K, out, ldc, dtype, false, stream);
+  return fp8_gemm_checked(A, sA, W, sW, expert_offsets, E, R, N, K, out, ldc, dtype, stream);
 }
 
 size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t K) {
@@ -1296,15 +1379,8 @@ size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t K) {
 nvfp4_status nvfp4_fp8_linear(const void* x, int64_t M, int64_t ld, int32_t dtype,
                               const uint8_t* W, const float* sW, int64_t N, int64_t K, void* y,
                               int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
-  if (M < 0 || K <= 0 || (M > 0 && !workspace)) return NVFP4_ERR_INVALID_ARG;
-  if (workspace_bytes < nvfp4_fp8_linear_workspace_bytes(M, K) || K % 16 != 0)
-    return NVFP4_ERR_UNSUPPORTED;
-  uint8_t* codes = static_cast<uint8_t*>(workspace);
-  float* scales = reinterpret_cast<float*>(codes + M * K);
-  const nvfp4_status st =
-      nvfp4_fp8_quantize(x, M, K, ld, dtype, 0, nullptr, 1, codes, scales, M, stream);
-  if (st != NVFP4_OK) return st;
-  return fp8_gemm_impl(codes, scales, W, sW, nullptr, 1, M, N, K, y, ldy, dtype, true, stream);
+  return fp8_linear_impl(x, M, ld, dtype, 0, nullptr, 1, W, sW, nullptr, 1, M, N, K, y, ldy,
+                         workspace, workspace_bytes, stream);
 }
 
 nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, int32_t dtype,
@@ -1313,16 +1389,9 @@ nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, in
                                      const int32_t* expert_offsets, int32_t E, int64_t R,
                                      int64_t N, int64_t K, void* y, int64_t ldy, void* workspace,
                                      size_t workspace_bytes, void* stream) {
-  if (!expert_offsets || R < 0 || K <= 0 || (R > 0 && !workspace)) return NVFP4_ERR_INVALID_ARG;
-  if (workspace_bytes < nvfp4_fp8_linear_workspace_bytes(R, K) || K % 16 != 0)
-    return NVFP4_ERR_UNSUPPORTED;
-  uint8_t* codes = static_cast<uint8_t*>(workspace);
-  float* scales = reinterpret_cast<float*>(codes + R * K);
-  const nvfp4_status st =
-      nvfp4_fp8_quantize(x, rows, K, ld, dtype, flags, route_pos, fanout, codes, scales, R, stream);
-  if (st != NVFP4_OK) return st;
-  return fp8_gemm_impl(codes, scales, W, sW, expert_offsets, E, R, N, K, y, ldy, dtype, rows > 0,
-                       stream);
+  if (!expert_offsets) return NVFP4_ERR_INVALID_ARG;
+  return fp8_linear_impl(x, rows, ld, dtype, flags, route_pos, fanout, W, sW, expert_offsets, E, R,
+                         N, K, y, ldy, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

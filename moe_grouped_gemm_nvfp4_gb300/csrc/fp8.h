@@ -27,6 +27,30 @@ cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int dtype, cudaStream_t s
 cudaError_t launch_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K,
                                         uint8_t* codes, float* scales, int dtype, cudaStream_t s);
 
+// fp8_rows.cu: quantisation and product of few rows in one launch, on the CUDA
+// cores: up to kFp8FewRows rows of one matrix, or kFp8FewRoutes routes.
+constexpr int kFp8FewRows = 4;
+constexpr int kFp8FewRoutes = 16;
+struct Fp8RowsArgs {
+  const void* x;                   // [T, K] (silu: [T, 2 K]), row stride ld
+  int64_t ld;
+  int32_t silu;
+  const int32_t* route_pos;        // grouped: [n_pos], or NULL
+  int32_t n_pos, fanout;
+  const uint8_t* w;
+  const float* sw;                 // [E, nnb, nkb]
+  const int32_t* offsets;          // grouped: [E + 1]; NULL: one matrix
+  int32_t E;
+  int32_t R;                       // rows of the output
+  int32_t N, K, nkb, nnb;
+  void* out;                       // [R, ldc], type of x
+  int64_t ldc;
+  int* status;
+};
+cudaError_t init_fp8_rows_attributes();
+bool fp8_few_rows(int64_t R, int64_t n_pos, int64_t N, int64_t K, bool grouped);
+cudaError_t launch_fp8_rows(const Fp8RowsArgs& a, int dtype, int sms, cudaStream_t s);
+
 struct Fp8GemmArgs {
   const float* sa;                 // [nkb, lds]: scale of row m's K block b at b * lds + m
   int64_t lds;

@@ -2,55 +2,20 @@
 //
 // Activations, one scale per row and 128 columns: a = max |x| over the block
 // (at least 2^-100), scale = a / 448, code = E4M3(448 x / a), rounded once from
-// the real quotient (nearest, ties to even).  For the 16-bit input types the
-// quotient is computed so that the code is the real quotient's: p = 0.875 x is
-// exact (448 = 0.875 * 2^9), q0 = p * (1 / a') with a' = a / 512 is within two
-// ulp, and one residual step q0 + (p - q0 a') / a' (Markstein's FMA correction)
-// returns a quotient that is representable exactly; an E4M3 rounding border has
-// five significant bits, so it is met exactly or missed by at least 2^-16 of
-// its value, far more than the step's error.  No overflow: p and a' are at most
-// FLT_MAX / 1, and q0 at most 448 (1 + 2^-22).
+// the real quotient (nearest, ties to even; fp8_quant.cuh).
 //
 // A lane holds 16 consecutive elements (two 16-byte loads, one 16-byte store),
 // eight lanes a block, so the maximum needs three shuffles.  A row that goes to
 // several route positions is read and rounded once and written to each.  Bound:
 // HBM (2 bytes read + fanout * (1 + 4/128) written per element).
 #include "fp8.h"
-#include "rows.cuh"
+#include "fp8_quant.cuh"
 
 namespace nvfp4 {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100
-
-// Four floats -> four E4M3 codes, the first in the low byte.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-      "mov.b32 %0, {lo, hi};\n\t}"
-      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-
-// a' and 1 / a' of a block with largest magnitude amax.
-struct BlockScale {
-  float unit, inv, scale;
-  __device__ __forceinline__ explicit BlockScale(float amax) {
-    const float a = fmaxf(amax, kAmaxFloor);
-    unit = a * 0.001953125f;
-    inv = __frcp_rn(unit);
-    scale = __fdiv_rn(a, 448.f);
-  }
-  __device__ __forceinline__ float quotient(float x) const {
-    const float p = x * 0.875f;
-    const float q = p * inv;
-    return fmaf(fmaf(-q, unit, p), inv, q);
-  }
-};
 
 template <int DT, bool SILU>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantArgs a, int chunks) {
@@ -64,29 +29,12 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
   const bool on = c < a.cols;                      // cols % 16 == 0: all 16 or none
   float v[16];
   if (on) {
-    Pack<DT, 8> lo, hi;
-    lo.load(a.x, row * a.ld + c);
-    hi.load(a.x, row * a.ld + c + 8);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { v[i] = lo.get(i); v[8 + i] = hi.get(i); }
-    if constexpr (SILU) {
-      lo.load(a.x, row * a.ld + a.cols + c);
-      hi.load(a.x, row * a.ld + a.cols + c + 8);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = v[i] / (1.f + __expf(-v[i])) * lo.get(i);
-        v[8 + i] = v[8 + i] / (1.f + __expf(-v[8 + i])) * hi.get(i);
-      }
-    }
+    load_row16<DT, SILU>(a.x, row * a.ld, a.cols, c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0.f;
   }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  const float amax = block_amax(v);
   if (!on) return;
   const BlockScale b(amax);
   uint4 q;

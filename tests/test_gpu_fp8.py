@@ -151,7 +151,8 @@ def weights(seed, E, N, K):
 
 # one token to several tiles of every width; ragged N and K; few units over a
 # long K (the sum over a cluster) and many
-DENSE = [(1, 128, 128), (1, 4096, 6144), (2, 1, 16), (7, 100, 48), (16, 256, 1024), (17, 130, 272),
+DENSE = [(1, 128, 128), (1, 4096, 6144), (2, 1, 16), (2, 640, 1040), (3, 130, 272), (4, 4096, 6144),
+         (4, 257, 8192), (7, 100, 48), (16, 256, 1024), (17, 130, 272),
          (32, 512, 4096), (33, 384, 144), (65, 1000, 528), (64, 128, 8192), (81, 257, 400),
          (129, 640, 1552), (333, 2056, 1552), (1000, 384, 256), (300, 6000, 128)]
 
@@ -242,6 +243,48 @@ def test_expert_linear(T, topk, E, N, K, dropped):
     assert F.nvfp4_device_status() == F.NVFP4_OK
 
 
+@pytest.mark.parametrize("T,topk,E,N,K", [(3, 4, 8, 130, 272), (50, 4, 8, 257, 400)])
+def test_expert_linear_of_gated_halves(T, topk, E, N, K):
+    """SiLU(gate) * up inside the call: the same codes as the quantiser's."""
+    w, ws = weights(N, E, N, K)
+    pos, off = routes(T + N, T, topk, E, 0.25)
+    R = T * topk
+    gu = normal(K, (R, 2 * K), torch.bfloat16) * 2
+    gu[int(off[-1]):] = float("nan")
+    y = fp8.expert_linear(gu, w, ws, off, silu_mul=True)
+    codes, scales = fp8.quantize_rows(gu, silu_mul=True)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if b > a:
+            ref, mag = product(codes[a:b], scales[:, a:b], w[e], ws[e])
+            check(y[a:b], ref, mag, K, f"expert {e}")
+    assert not y[int(off[-1]):].any()
+    x = normal(1, (T, 2 * K), torch.bfloat16)       # gathered from token order as well
+    rows = torch.zeros((R, 2 * K), dtype=torch.bfloat16, device="cuda")
+    for k in range(topk):
+        ok = pos[:, k] >= 0
+        rows[pos[ok, k].long()] = x[ok]
+    got = fp8.expert_linear(x, w, ws, off, pos, silu_mul=True)
+    assert torch.equal(got, fp8.expert_linear(rows, w, ws, off, silu_mul=True))
+    assert F.nvfp4_device_status() == F.NVFP4_OK
+
+
+def test_few_routes_report_bad_routing():
+    E, N, K, R = 4, 128, 256, 8
+    w, ws = weights(3, E, N, K)
+    x = normal(1, (R, K), torch.bfloat16)
+    good = torch.tensor([0, 2, 4, 6, 8], dtype=torch.int32).cuda()
+    want = fp8.expert_linear(x, w, ws, good)
+    y = fp8.expert_linear(x, w, ws, torch.tensor([0, 2, 4, 9, 8], dtype=torch.int32).cuda())
+    assert F.nvfp4_device_status() == F.NVFP4_ERR_DEVICE_CHECK
+    assert torch.equal(y[:4], want[:4])
+    pos = torch.arange(R, dtype=torch.int32).view(4, 2).cuda()
+    pos[3, 1] = R + 5
+    fp8.expert_linear(x[:4], w, ws, good, pos)
+    assert F.nvfp4_device_status() == F.NVFP4_ERR_DEVICE_CHECK
+    assert F.nvfp4_device_status() == F.NVFP4_OK
+
+
 def test_skewed_experts():
     """One expert with most rows, several with none, the first and last empty."""
     E, N, K, R = 9, 384, 656, 1500
@@ -318,7 +361,7 @@ def test_streams_and_capture():
     assert torch.equal(b, fp8.linear(x, w[0], ws[0]))
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 128, 2048), (64, 20000, 256), (500, 512, 1024)])
+@pytest.mark.parametrize("M,N,K", [(5, 128, 2048), (64, 20000, 256), (500, 512, 1024)])
 def test_expired_wait_is_reported(M, N, K):
     """A stage that never fills: the kernel gives up within its limit, records
     it and returns; the next call is right again."""
