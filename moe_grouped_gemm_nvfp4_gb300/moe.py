@@ -17,6 +17,7 @@ from dataclasses import dataclass
 
 import torch
 
+from . import fp8, tokens
 from . import nvfp4 as F
 
 
@@ -314,3 +315,36 @@ class CapturedStep:
     def replay(self):
         self.graph.replay()
         return self.outputs
+
+
+class Fp8MLP:
+    """One expert MLP pass over FP8 weights (fp8.quantize_weights, or a
+    checkpoint's codes and 128 x 128 scales): gate_up codes [E, 2 I, K] and scales,
+    down codes [E, N, I] and scales, each a pair.
+
+    step() routes, multiplies the gathered tokens by gate_up, quantises
+    SiLU(gate) * up into the down products and sums each token's routes.  It
+    enqueues kernels only and keeps no buffers, so it can be captured."""
+
+    def __init__(self, gate_up, down):
+        (w1, _), (w2, _) = gate_up, down
+        if w1.dim() != 3 or w2.dim() != 3 or w1.shape[0] != w2.shape[0] \
+                or w1.shape[1] != 2 * w2.shape[2]:
+            raise ValueError("expected gate_up codes [E, 2 I, K] and down codes [E, N, I]")
+        self.gate_up, self.down = gate_up, down
+
+    def route(self, topk_ids, stream=None):
+        """topk_ids int32 [T, k] -> (expert_offsets [E + 1], route_pos [T, k])."""
+        offsets, _, _, pos = F.moe_route(topk_ids, self.gate_up[0].shape[0], stream)
+        return offsets, pos.view(topk_ids.shape)
+
+    def step(self, x, topk_ids, topk_weights, stream=None):
+        """x [T, K] BF16 or FP16, topk_ids int32 [T, k], topk_weights FP32 [T, k]
+        -> [T, N] in x's type."""
+        if stream is not None:
+            with tokens.on_stream(stream):
+                return self.step(x, topk_ids, topk_weights)
+        offsets, pos = self.route(topk_ids)
+        gate_up = fp8.expert_linear(x, *self.gate_up, offsets, pos)
+        y = fp8.expert_linear(gate_up, *self.down, offsets, silu_mul=True)
+        return tokens.combine(y, pos, topk_weights)
