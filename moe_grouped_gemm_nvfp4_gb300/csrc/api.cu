@@ -191,13 +191,13 @@ nvfp4_status make_scale_map(CUtensorMap* m, const void* base, uint64_t rows, int
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
 }
 
-// Map over E4M3 codes [E, rows, K] (uint8), boxes of 128 bytes x box_rows rows
+// Map over E4M3 codes [E, rows, K] (uint8, row stride ld), boxes of 128 bytes x box_rows rows
 // of one matrix, 128-byte swizzle.  Rows past a matrix and columns past K read
 // zeros.
-nvfp4_status make_fp8_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t E,
-                          uint32_t box_rows, uint32_t rank) {
+nvfp4_status make_fp8_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t ld, uint64_t rows,
+                          uint64_t E, uint32_t box_rows, uint32_t rank) {
   const cuuint64_t dims[3] = {K, rows, E};
-  const cuuint64_t strides[2] = {K, K * rows};
+  const cuuint64_t strides[2] = {ld, ld * rows};
   const cuuint32_t box[3] = {128u, box_rows, 1u};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims,
@@ -210,6 +210,9 @@ nvfp4_status make_fp8_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t
 bool is_dtype(int32_t t) { return t == NVFP4_BF16 || t == NVFP4_FP16 || t == NVFP4_FP32; }
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 unsigned dtype_bytes(int32_t t) { return t == NVFP4_FP32 ? 4u : 2u; }
+
+// Row stride of the activations' codes in a workspace.
+int64_t fp8_code_stride(int64_t K) { return (K + 127) / 128 * 128; }
 
 nvfp4_status check_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
                             uint32_t flags, const int32_t* route_pos, int32_t fanout,
@@ -229,8 +232,8 @@ nvfp4_status check_quantize(const void* x, int64_t rows, int64_t cols, int64_t l
 
 nvfp4_status fp8_quantize_impl(DeviceState* d, const void* x, int64_t rows, int64_t cols,
                                int64_t ld, int32_t dtype, uint32_t flags, const int32_t* route_pos,
-                               int32_t fanout, uint8_t* codes, float* scales, int64_t out_rows,
-                               void* stream) {
+                               int32_t fanout, uint8_t* codes, int64_t ldq, float* scales,
+                               int64_t out_rows, void* stream) {
   if (rows == 0 || out_rows == 0) return NVFP4_OK;
   nvfp4::Fp8QuantArgs a{};
   a.x = x;
@@ -241,6 +244,7 @@ nvfp4_status fp8_quantize_impl(DeviceState* d, const void* x, int64_t rows, int6
   a.fanout = fanout;
   a.silu = (flags & NVFP4_FP8_SILU_MUL) ? 1 : 0;
   a.codes = codes;
+  a.ldq = ldq;
   a.scales = scales;
   a.out_rows = out_rows;
   a.status = d->status;
@@ -264,8 +268,8 @@ nvfp4_status check_gemm(const uint8_t* A, const float* sA, const uint8_t* W, con
   return NVFP4_OK;
 }
 
-nvfp4_status fp8_gemm_impl(DeviceState* d, const uint8_t* A, const float* sA, const uint8_t* W,
-                           const float* sW, const int32_t* offsets, int32_t E, int64_t rows,
+nvfp4_status fp8_gemm_impl(DeviceState* d, const uint8_t* A, int64_t lda, const float* sA,
+                           const uint8_t* W, const float* sW, const int32_t* offsets, int32_t E, int64_t rows,
                            int64_t N, int64_t K, void* out, int64_t ldc, int32_t dtype,
                            bool overlap, void* stream) {
   if (rows == 0) return NVFP4_OK;
@@ -289,8 +293,8 @@ nvfp4_status fp8_gemm_impl(DeviceState* d, const uint8_t* A, const float* sA, co
   a.debug_flags = g_debug_flags.load();
   CUtensorMap ta, tw;
   const uint32_t box = static_cast<uint32_t>(nvfp4::fp8_tile_tokens(rows, offsets ? E : 0));
-  if (make_fp8_map(&ta, A, K, rows, 1, box, 2) != NVFP4_OK ||
-      make_fp8_map(&tw, W, K, N, E, 128, 3) != NVFP4_OK)
+  if (make_fp8_map(&ta, A, K, lda, rows, 1, box, 2) != NVFP4_OK ||
+      make_fp8_map(&tw, W, K, K, N, E, 128, 3) != NVFP4_OK)
     return NVFP4_ERR_UNSUPPORTED;
   const cudaError_t e =
       nvfp4::launch_fp8_gemm(ta, tw, a, d->sms, static_cast<cudaStream_t>(stream));
@@ -307,8 +311,11 @@ nvfp4_status fp8_linear_impl(const void* x, int64_t rows, int64_t ld, int32_t dt
                              size_t workspace_bytes, void* stream) {
   if (R < 0 || K <= 0 || (R > 0 && !workspace)) return NVFP4_ERR_INVALID_ARG;
   if (workspace_bytes < nvfp4_fp8_linear_workspace_bytes(R, K)) return NVFP4_ERR_UNSUPPORTED;
+  // rows of codes on 128-byte lines: a row that starts inside one costs the GEMM a
+  // fifth sector and a second line for every box row (see fp8_code_stride)
+  const int64_t ldq = fp8_code_stride(K);
   uint8_t* codes = static_cast<uint8_t*>(workspace);
-  float* scales = reinterpret_cast<float*>(codes + R * K);
+  float* scales = reinterpret_cast<float*>(codes + R * ldq);
   nvfp4_status st = check_quantize(x, rows, K, ld, dtype, flags, route_pos, fanout, codes, scales, R);
   if (st == NVFP4_OK) st = check_gemm(codes, scales, W, sW, offsets, E, R, N, K, y, ldy, dtype);
   if (st != NVFP4_OK) return st;
@@ -341,10 +348,10 @@ nvfp4_status fp8_linear_impl(const void* x, int64_t rows, int64_t ld, int32_t dt
                ? NVFP4_OK
                : cuda_fail();
   }
-  st = fp8_quantize_impl(d, x, rows, K, ld, dtype, flags, route_pos, fanout, codes, scales, R,
+  st = fp8_quantize_impl(d, x, rows, K, ld, dtype, flags, route_pos, fanout, codes, ldq, scales, R,
                          stream);
   if (st != NVFP4_OK) return st;
-  return fp8_gemm_impl(d, codes, scales, W, sW, offsets, E, R, N, K, y, ldy, dtype, rows > 0,
+  return fp8_gemm_impl(d, codes, ldq, scales, W, sW, offsets, E, R, N, K, y, ldy, dtype, rows > 0,
                        stream);
 }
 
@@ -356,7 +363,7 @@ nvfp4_status fp8_gemm_checked(const uint8_t* A, const float* sA, const uint8_t* 
   DeviceState* d = nullptr;
   const nvfp4_status st = device_state(&d);
   if (st != NVFP4_OK) return st;
-  return fp8_gemm_impl(d, A, sA, W, sW, offsets, E, rows, N, K, out, ldc, dtype, false, stream);
+  return fp8_gemm_impl(d, A, K, sA, W, sW, offsets, E, rows, N, K, out, ldc, dtype, false, stream);
 }
 
 }  // namespace
@@ -1336,8 +1343,8 @@ nvfp4_status nvfp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64
   DeviceState* d = nullptr;
   const nvfp4_status st = device_state(&d);
   if (st != NVFP4_OK) return st;
-  return fp8_quantize_impl(d, x, rows, cols, ld, dtype, flags, route_pos, fanout, codes, scales,
-                           out_rows, stream);
+  return fp8_quantize_impl(d, x, rows, cols, ld, dtype, flags, route_pos, fanout, codes, cols,
+                           scales, out_rows, stream);
 }
 
 nvfp4_status nvfp4_fp8_quantize_weights(const void* w, int32_t E, int64_t N, int64_t K,
@@ -1372,7 +1379,7 @@ nvfp4_status nvfp4_fp8_grouped_gemm(const uint8_t* A, const float* sA, const uin
 
 size_t nvfp4_fp8_linear_workspace_bytes(int64_t rows, int64_t K) {
   if (rows < 0 || K < 0) return 0;
-  return static_cast<size_t>(rows) * (static_cast<size_t>(K) +
+  return static_cast<size_t>(rows) * (static_cast<size_t>(fp8_code_stride(K)) +
                                       4 * static_cast<size_t>((K + 127) / 128));
 }
 

@@ -17,7 +17,8 @@ struct Fp8QuantArgs {
   const int32_t* route_pos;        // [rows, fanout] positions of each row's copies; NULL: row i -> i
   int32_t fanout;
   int32_t silu;
-  uint8_t* codes;                  // [out_rows, cols]
+  uint8_t* codes;                  // [out_rows, cols], row stride ldq
+  int64_t ldq;
   float* scales;                   // [ceil(cols / 128), out_rows]
   int64_t out_rows;
   int* status;

@@ -21,11 +21,10 @@
 // NT rows of activations per stage), warp 1 tensor memory and MMA, warp 2 the
 // factors (shared memory, one set per accumulator buffer; its arrival counts
 // on the buffer's barrier beside the MMA's), warp 3 zeros the output rows past
-// the last expert's, warps 4-11 epilogue (lane
-// quarter warp % 4, 64 columns each).  Few units and a long K: the CTAs of a
-// cluster share a unit, each a slice of K, and sum their registers through
-// distributed shared memory in rank order (no atomics, the same bits every
-// time).  Every wait is bounded.
+// the last expert's, warps 4-11 epilogue (lane quarter warp % 4, 64 columns
+// each).  Few units and a long K: the CTAs of a cluster share a unit, each a
+// slice of K, and sum their registers through distributed shared memory in rank
+// order (no atomics, the same bits every time).  Every wait is bounded.
 #include "fp8_common.cuh"
 
 namespace nvfp4 {
@@ -145,8 +144,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     // ------------------------------------------------------------ producer
     if (elect_one()) {
       uint32_t issued = 0;
-      // weights pass through once unless several token tiles share them
-      const uint64_t wpol = l2_policy_evict_first();
+      // Weights: out of L2 first, so that the activations stay (one tile of tokens
+      // per expert reads them once; 4096 x 4096 x 6144 97.6 us, 106.1 us kept like
+      // other lines), except where experts have several tiles of tokens that share
+      // them in passing (64 experts, 16384 routes, N 3000, K 4096: 298 and 267 us;
+      // the 65536-route prefill 2.04 and 1.88 ms).  Rows that start inside a
+      // 128-byte line go out first there too (K 4080: 334 and 385 us).
+      const bool shared_w = NT == 128 && a.offsets != nullptr && (a.K & 127) == 0;
+      const uint64_t wpol = shared_w ? l2_policy_evict_normal() : l2_policy_evict_first();
       const uint64_t apol = l2_policy_evict_last();
       auto load_w = [&](const Unit& un, int kb, int s) {
         mbar_arrive_expect_tx(full_bar(s), C::kStageBytes);

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
       if (r < 0) continue;
       if (r >= a.out_rows) { raise_status(a.status, NVFP4_ERR_DEVICE_CHECK); continue; }
     }
-    *reinterpret_cast<uint4*>(a.codes + r * a.cols + c) = q;
+    *reinterpret_cast<uint4*>(a.codes + r * a.ldq + c) = q;
     if (first) a.scales[kb * a.out_rows + r] = b.scale;
   }
 }

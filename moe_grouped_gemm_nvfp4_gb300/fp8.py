@@ -76,8 +76,18 @@ def transpose_weights(w, w_scale):
     return codes, w_scale.transpose(-1, -2).contiguous()
 
 
+def _refuse_grad(x):
+    """The products take no part in autograd; losing a gradient silently is worse
+    than an error."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("FP8 products are not differentiable by themselves: call them in an "
+                           "autograd.Function (the gradient is the product with "
+                           "transpose_weights) or under no_grad")
+
+
 def linear(x, w, w_scale, stream=None):
     """y = x . w^T: x [.., K] BF16 or FP16, w codes [N, K] -> [.., N] in x's type."""
+    _refuse_grad(x)
     if stream is not None:
         with on_stream(stream):
             return linear(x, w, w_scale)
@@ -95,6 +105,7 @@ def expert_linear(x, w, w_scale, expert_offsets, route_pos=None, R=None, silu_mu
     without, x is in expert order already.  silu_mul: x holds gate and up halves
     [.., 2K], the rows are SiLU(gate) * up.  Rows past expert_offsets[E] are
     zero."""
+    _refuse_grad(x)
     R = -1 if R is None else R
     if stream is not None:
         with on_stream(stream):

@@ -114,3 +114,21 @@ def test_python_refusals():
             fp8.expert_linear(x, codes, scales, bad_off)
     with pytest.raises(ValueError):
         fp8.quantize_rows(x, pos[:3])
+    leaf = x.clone().requires_grad_()
+    with pytest.raises(RuntimeError):                     # a gradient would be lost
+        fp8.linear(leaf, codes[0], scales[0])
+    with pytest.raises(RuntimeError):
+        fp8.expert_linear(leaf, codes, scales, off[:3])
+
+
+def test_workspace_bytes():
+    assert F.nvfp4_fp8_linear_workspace_bytes(5, 144) == 5 * (256 + 4 * 2)   # rows of 128 bytes
+    assert F.nvfp4_fp8_linear_workspace_bytes(0, 128) == 0
+    assert F.nvfp4_fp8_linear_workspace_bytes(-1, 128) == 0
+    lib = F.load()
+    for call, extra in ((lib.nvfp4_fp8_linear, ()), (lib.nvfp4_fp8_expert_linear, (0, None, 1))):
+        middle = (P, P) if call is lib.nvfp4_fp8_linear else (P, P, P, 4, 4)
+        args = (P, 4, 64, 0, *extra, *middle, 64, 64, P, 64, P)
+        assert call(*args, 4 * (128 + 4) - 1, None) == F.NVFP4_ERR_UNSUPPORTED   # too small
+    assert lib.nvfp4_fp8_linear(P, 4, 64, 0, P, P, 64, 64, P, 64, None, 1 << 20, None) == \
+        F.NVFP4_ERR_INVALID_ARG
