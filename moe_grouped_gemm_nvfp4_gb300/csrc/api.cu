@@ -287,6 +287,7 @@ nvfp4_status fp8_gemm_impl(DeviceState* d, const uint8_t* A, int64_t lda, const 
   a.out = out;
   a.ldc = ldc;
   a.out_type = dtype;
+  a.vec = aligned16(out) && (ldc * dtype_bytes(dtype)) % 16 == 0 ? 1 : 0;
   a.overlap = overlap ? 1 : 0;
   a.status = d->status;
   a.timeout_ns = g_timeout_ns.load();

@@ -64,6 +64,7 @@ struct Fp8GemmArgs {
   void* out;                       // [rows, ldc]
   int64_t ldc;
   int32_t out_type;                // nvfp4_dtype
+  int32_t vec;                     // every row of out is 16-byte aligned
   int32_t overlap;                 // start while the kernel before (the quantiser) still runs
   int* status;
   uint64_t timeout_ns;

@@ -206,43 +206,63 @@ __device__ __forceinline__ void load_units(const int32_t* offsets, int E, int ro
   __syncthreads();
 }
 
-// One warp turns the scales of a unit's K blocks [kb0, kb1) into factors in
+// One warp turns the scales of its units' K blocks [kb0, kb1) into factors in
 // shared memory, sa[row] * sw for ROWS tokens, one set per accumulator buffer;
 // `put(b, phase)` waits until the buffer is free, `done(b)` tells the epilogue.
-// kAhead K blocks' loads are on their way while the group before is written: an
-// L2 read takes longer than a K block.
+// kAhead K blocks' loads are on their way while the group before is written, the
+// next unit's first ones behind a unit's last: an L2 read takes longer than a K
+// block.
 constexpr int kAhead = 4;
 template <int ROWS, int BUFS, class Put, class Done>
-__device__ __forceinline__ bool factor_unit(const Fp8GemmArgs& a, const Unit& un, int kb0, int kb1,
-                                            uint32_t fac, int lane, int& buf, uint32_t& phase,
-                                            Put put, Done done) {
+__device__ __forceinline__ void factor_units(const Fp8GemmArgs& a, const UnitMap& um, int u,
+                                             int units, int ustep, int kb0, int kb1, uint32_t fac,
+                                             int lane, Put put, Done done) {
   constexpr int kPer = (ROWS + 31) / 32;
-  const float* sw = a.sw + (static_cast<int64_t>(un.e) * a.nnb + un.nt) * a.nkb;
-  const float* sa = a.sa + kb0 * a.lds + un.row + lane;
-  const int rows = un.cnt - lane;                // rows of this lane: 32 * i < rows
+  if (u >= units) return;
+  const float* sw = nullptr;
+  const float* sa = nullptr;
+  int rows = 0, kb = kb0;
+  auto open = [&] {
+    const Unit un = unit_at(um, u);
+    sw = a.sw + (static_cast<int64_t>(un.e) * a.nnb + un.nt) * a.nkb;
+    sa = a.sa + kb0 * a.lds + un.row + lane;
+    rows = un.cnt - lane;                        // rows of this lane: 32 * i < rows
+    kb = kb0;
+  };
   float na[kAhead][kPer], nw[kAhead];
-  auto fetch = [&](int kb) {
+  int nn = 0;                                    // K blocks of the fetched group
+  auto fetch = [&] {
+    nn = u < units ? min(kAhead, kb1 - kb) : 0;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const bool in = kb + j < kb1;
+      const bool in = j < nn;
       nw[j] = in ? __ldg(sw + kb + j) : 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) na[j][i] = in && 32 * i < rows ? __ldg(sa + 32 * i) : 0.f;
       sa += a.lds;
     }
+    kb += kAhead;
+    if (nn > 0 && kb >= kb1) {
+      u += ustep;
+      if (u < units) open();
+    }
   };
-  fetch(kb0);
-  for (int kb = kb0; kb < kb1; kb += kAhead) {
+  open();
+  fetch();
+  int buf = 0;
+  uint32_t phase = 0;
+  while (nn > 0) {
+    const int n = nn;
     float f[kAhead][kPer];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) f[j][i] = na[j][i] * nw[j];
-    fetch(kb + kAhead);
+    fetch();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (kb + j >= kb1) break;
-      if (!put(buf, phase)) return false;
+      if (j >= n) break;
+      if (!put(buf, phase)) return;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) st_shared_f32(fac + 4 * (buf * 128 + lane + 32 * i), f[j][i]);
       __syncwarp();
@@ -250,7 +270,6 @@ __device__ __forceinline__ bool factor_unit(const Fp8GemmArgs& a, const Unit& un
       if (++buf == BUFS) { buf = 0; phase ^= 1u; }
     }
   }
-  return true;
 }
 
 // n K blocks of one unit added into acc (COLS FP32 values, packed in pairs),
@@ -292,46 +311,90 @@ __device__ __forceinline__ bool add_unit(uint64_t (&acc)[COLS / 2], int n, uint3
   return true;
 }
 
-// COLS neighbouring outputs of one row (those before column N).
-template <int COLS>
-__device__ __forceinline__ void store_row(const Fp8GemmArgs& a, int row, int n0,
-                                          const uint64_t (&acc2)[COLS / 2]) {
+// A warp's 32 rows x COLS columns of outputs, row `lane` of them in each lane's
+// acc; rows from `rows` on and columns from N on are not stored.  VEC: every row
+// is 16-byte aligned and leaves by 16 bytes a lane.  Others (an odd row stride)
+// pass through `buf`, 32 rows of 16 words and one of padding, so that a store
+// covers 64 bytes of one row: by element from each lane's own row, 9995 routes of
+// 1329 columns (K 400) took 127 us, like this 36 us.  (Two kernels: with both ways
+// in one the accumulation loop came out 10% slower.)
+constexpr int kStoreWords = 32 * 17;
+template <int COLS, bool VEC>
+__device__ __forceinline__ void store_rows(const Fp8GemmArgs& a, int row0, int rows, int n0,
+                                           const uint64_t (&acc2)[COLS / 2], uint32_t buf,
+                                           int lane) {
   const int n = a.N - n0;
   if (n <= 0) return;
   float acc[COLS];
 #pragma unroll
   for (int i = 0; i < COLS / 2; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
-  const int64_t at = static_cast<int64_t>(row) * a.ldc + n0;
-  if (a.out_type == NVFP4_FP32) {
-    float* dst = static_cast<float*>(a.out) + at;
-    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+  const bool wide = a.out_type == NVFP4_FP32;
+  if constexpr (VEC) {
+    if (lane >= rows) return;
+    const int64_t at = static_cast<int64_t>(row0 + lane) * a.ldc + n0;
+    if (wide) {
+      float* dst = static_cast<float*>(a.out) + at;
 #pragma unroll
-    for (int i = 0; i < COLS; i += 4) {
-      if (vec && i + 4 <= n) {
-        *reinterpret_cast<float4*>(dst + i) =
-            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-      } else {
+      for (int i = 0; i < COLS; i += 4) {
+        if (i + 4 <= n) {
+          *reinterpret_cast<float4*>(dst + i) =
+              make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < n) dst[i + j] = acc[i + j];
+          for (int j = 0; j < 4; ++j)
+            if (i + j < n) dst[i + j] = acc[i + j];
+        }
+      }
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+      for (int i = 0; i < COLS; i += 8) {
+        uint16_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = f32_to_out16(acc[i + j], a.out_type);
+        if (i + 8 <= n) {
+          *reinterpret_cast<uint4*>(dst + i) =
+              make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                         h[6] | (h[7] << 16));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (i + j < n) dst[i + j] = h[j];
+        }
       }
     }
   } else {
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + at;
-    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+    const int live = min(rows, 32);
+    if (wide) {
+      float* out = static_cast<float*>(a.out) + static_cast<int64_t>(row0) * a.ldc + n0;
 #pragma unroll
-    for (int i = 0; i < COLS; i += 8) {
-      uint16_t h[8];
+      for (int c = 0; c < COLS; c += 16) {
+        __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = f32_to_out16(acc[i + j], a.out_type);
-      if (vec && i + 8 <= n) {
-        *reinterpret_cast<uint4*>(dst + i) =
-            make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
-                       h[6] | (h[7] << 16));
-      } else {
+        for (int i = 0; i < 16; ++i) st_shared_f32(buf + 4 * (lane * 17 + i), acc[c + i]);
+        __syncwarp();
+        const int col = c + (lane & 15);
+        for (int r = lane >> 4; r < live; r += 2) {
+          const float v = ld_shared_f32(buf + 4 * (r * 17 + (lane & 15)));
+          if (col < n) out[r * a.ldc + col] = v;
+        }
+      }
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(row0) * a.ldc + n0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i + j < n) dst[i + j] = h[j];
+      for (int c = 0; c < COLS; c += 32) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          st_shared_f32(buf + 4 * (lane * 17 + i),
+                        __uint_as_float(f32_to_out16(acc[c + 2 * i], a.out_type) |
+                                        (f32_to_out16(acc[c + 2 * i + 1], a.out_type) << 16)));
+        __syncwarp();
+        const int col = c + lane;
+        for (int r = 0; r < live; ++r) {
+          const uint32_t v = __float_as_uint(ld_shared_f32(buf + 4 * (r * 17 + (lane >> 1))));
+          if (col < n) out[r * a.ldc + col] = static_cast<uint16_t>(v >> (16 * (lane & 1)));
+        }
       }
     }
   }

@@ -44,7 +44,9 @@ struct Cfg {
   static constexpr int kThreads = 128 + 256;
   static constexpr int kUnitBytes = 2 * 4 * (kFp8MaxExperts + 1) + 8;
   static constexpr int kFacOffset = kStages * kStageBytes;
-  static constexpr int kUnitOffset = kFacOffset + kBufs * 128 * 4;
+  // rows on their way out, one buffer per epilogue warp
+  static constexpr int kStoreOffset = kFacOffset + kBufs * 128 * 4;
+  static constexpr int kUnitOffset = kStoreOffset + 2 * kQuarters * kStoreWords * 4;
   static constexpr int kBarOffset = (kUnitOffset + kUnitBytes + 7) / 8 * 8;
   // full[S], empty[S], acc_full[B], acc_empty[B], drain
   static constexpr int kBarBytes = 8 * (2 * kStages + 2 * kBufs + 1);
@@ -70,18 +72,43 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void store_out(const Fp8GemmArgs& a, int row, int n, float v) {
+// Four neighbouring outputs of one row (those before column N).
+__device__ __forceinline__ void store_four(const Fp8GemmArgs& a, int row, int n, const float4& v) {
   const int64_t at = static_cast<int64_t>(row) * a.ldc + n;
-  if (a.out_type == NVFP4_FP32) static_cast<float*>(a.out)[at] = v;
-  else static_cast<uint16_t*>(a.out)[at] = f32_to_out16(v, a.out_type);
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  if (a.out_type == NVFP4_FP32) {
+    float* dst = static_cast<float*>(a.out) + at;
+    if (a.vec && n + 4 <= a.N) {
+      *reinterpret_cast<float4*>(dst) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < a.N) dst[j] = f[j];
+    }
+  } else {
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + at;
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = f32_to_out16(f[j], a.out_type);
+    if (a.vec && n + 4 <= a.N) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < a.N) dst[j] = static_cast<uint16_t>(h[j]);
+    }
+  }
 }
 
-// SPLIT: one unit per cluster, K shared by its CTAs; otherwise persistent.
-template <int NT, bool SPLIT>
+// kSplit: one unit per cluster, K shared by its CTAs.  Persistent otherwise, with
+// outputs in rows of 16-byte chunks or in any.
+enum Mode : int { kChunkRows, kAnyRows, kSplit };
+template <int NT, int MODE>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tw,
                 const Fp8GemmArgs a) {
   using C = Cfg<NT>;
+  constexpr bool SPLIT = MODE == kSplit;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -234,19 +261,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   } else if (warp == 2) {
     // ------------------------------------------------------------- factors
     grid_dependency_wait();
-    int buf = 0;
-    uint32_t bphase = 0;
-    for (int u = u0; u < units; u += ustep) {
-      const Unit un = unit_at(um, u);
-      if (!factor_unit<NT, C::kBufs>(
-              a, un, kb0, kb1, fac, lane, buf, bphase,
-              [&](int b, uint32_t phase) {
-                return __all_sync(0xFFFFFFFFu,
-                                  wait_soon(acce_bar(b), phase ^ 1u, ctl, a.status)) != 0;
-              },
-              [&](int b) { mbar_arrive(accf_bar(b)); }))
-        break;
-    }
+    factor_units<NT, C::kBufs>(
+        a, um, u0, units, ustep, kb0, kb1, fac, lane,
+        [&](int b, uint32_t phase) {
+          return __all_sync(0xFFFFFFFFu, wait_soon(acce_bar(b), phase ^ 1u, ctl, a.status)) != 0;
+        },
+        [&](int b) { mbar_arrive(accf_bar(b)); });
   } else if (warp == 3) {
     // ------------------------------------------- rows of no expert are zero
     if (um.first) zero_rows_past(a, um.first[a.E], lane);
@@ -289,8 +309,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
             red[i] = v;
           }
         }
-      } else if (row < un.cnt) {
-        store_row<C::kCols>(a, un.row + row, un.nt * 128 + c0, acc);
+      } else {
+        const int q = warp & 3;
+        store_rows<C::kCols, MODE == kChunkRows>(
+            a, un.row + 32 * q, un.cnt - 32 * q, un.nt * 128 + c0, acc,
+            sbase + C::kStoreOffset + 4 * kStoreWords * (((warp - 4) >> 2) * C::kQuarters + q),
+            lane);
       }
     }
   }
@@ -327,10 +351,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
             o.x += v[i][j].x; o.y += v[i][j].y; o.z += v[i][j].z; o.w += v[i][j].w;
           }
           const int row = un.row + t0 + i * step, col = un.nt * 128 + n;
-          if (col < a.N) store_out(a, row, col, o.x);
-          if (col + 1 < a.N) store_out(a, row, col + 1, o.y);
-          if (col + 2 < a.N) store_out(a, row, col + 2, o.z);
-          if (col + 3 < a.N) store_out(a, row, col + 3, o.w);
+          store_four(a, row, col, o);
         }
       }
     }
@@ -346,10 +367,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   }
 }
 
-template <int NT, bool SPLIT>
+template <int NT, int MODE>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(fp8_gemm_kernel<NT, SPLIT>,
+  return cudaFuncSetAttribute(fp8_gemm_kernel<NT, MODE>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmemBytes);
+}
+
+template <int NT>
+cudaError_t set_attrs() {
+  cudaError_t e = set_attr<NT, kChunkRows>();
+  if (e == cudaSuccess) e = set_attr<NT, kAnyRows>();
+  return e == cudaSuccess ? set_attr<NT, kSplit>() : e;
 }
 
 template <int NT>
@@ -376,28 +404,24 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tw, const Fp8GemmAr
   }
   if (split == 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms), 1, 1);
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, false>, ta, tw, a);
+    return a.vec ? cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, kChunkRows>, ta, tw, a)
+                 : cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, kAnyRows>, ta, tw, a);
   }
   attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
   attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(split);
   attr[cfg.numAttrs].val.clusterDim.y = 1;
   attr[cfg.numAttrs++].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(units * split), 1, 1);
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, true>, ta, tw, a);
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NT, kSplit>, ta, tw, a);
 }
 
 }  // namespace
 
 cudaError_t init_fp8_gemm_attributes() {
-  cudaError_t e = set_attr<16, false>();
-  if (e == cudaSuccess) e = set_attr<32, false>();
-  if (e == cudaSuccess) e = set_attr<64, false>();
-  if (e == cudaSuccess) e = set_attr<128, false>();
-  if (e == cudaSuccess) e = set_attr<16, true>();
-  if (e == cudaSuccess) e = set_attr<32, true>();
-  if (e == cudaSuccess) e = set_attr<64, true>();
-  if (e == cudaSuccess) e = set_attr<128, true>();
-  return e;
+  cudaError_t e = set_attrs<16>();
+  if (e == cudaSuccess) e = set_attrs<32>();
+  if (e == cudaSuccess) e = set_attrs<64>();
+  return e == cudaSuccess ? set_attrs<128>() : e;
 }
 
 // Tokens per tile: the rows themselves for one matrix; for E experts 1.6

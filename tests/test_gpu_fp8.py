@@ -154,7 +154,7 @@ def weights(seed, E, N, K):
 DENSE = [(1, 128, 128), (1, 4096, 6144), (2, 1, 16), (2, 640, 1040), (3, 130, 272), (4, 4096, 6144),
          (4, 257, 8192), (7, 100, 48), (16, 256, 1024), (17, 130, 272),
          (32, 512, 4096), (33, 384, 144), (65, 1000, 528), (64, 128, 8192), (81, 257, 400),
-         (129, 640, 1552), (333, 2056, 1552), (1000, 384, 256), (300, 6000, 128)]
+         (129, 640, 1552), (333, 2056, 1552), (1000, 384, 256), (300, 6000, 128), (4000, 645, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -169,8 +169,9 @@ def test_linear(M, N, K, dtype):
     assert F.nvfp4_device_status() == F.NVFP4_OK
 
 
-def test_linear_output_types_strides_and_repeat():
-    M, N, K = 50, 300, 1040
+@pytest.mark.parametrize("M,N,K", [(50, 300, 1040), (3000, 333, 272), (2500, 1001, 128),
+                                   (20000, 64, 144)])
+def test_linear_output_types_strides_and_repeat(M, N, K):
     w, ws = weights(1, 1, N, K)
     x = normal(0, (M, K), torch.bfloat16)
     codes, scales = fp8.quantize_rows(x)
@@ -185,7 +186,7 @@ def test_linear_output_types_strides_and_repeat():
         first = c.clone()
         F.nvfp4_fp8_gemm(codes, scales, w[0], ws[0], c)
         assert torch.equal(first, c)
-    y3 = fp8.linear(x.view(5, 10, K), w[0], ws[0])
+    y3 = fp8.linear(x.view(5, M // 5, K), w[0], ws[0])
     assert torch.equal(y3.view(M, N), fp8.linear(x, w[0], ws[0]))
     assert fp8.linear(x[:0], w[0], ws[0]).shape == (0, N)
 
@@ -227,7 +228,8 @@ def check_experts(x, w, ws, pos, off, R, gather, y):
 # without a token; the sum over a cluster
 GROUPED = [(1, 1, 4, 128, 128), (1, 8, 8, 512, 2048), (5, 2, 16, 100, 144), (40, 4, 8, 257, 272),
            (64, 8, 16, 384, 256), (200, 2, 4, 130, 528), (300, 4, 8, 256, 400),
-           (256, 8, 128, 256, 512), (700, 3, 5, 640, 128)]
+           (256, 8, 128, 256, 512), (700, 3, 5, 640, 128), (900, 5, 8, 1329, 400),
+           (1500, 2, 4, 130, 144)]
 
 
 @pytest.mark.parametrize("T,topk,E,N,K", GROUPED)
