@@ -45,12 +45,6 @@ struct Pack {
       w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     }
   }
-  __device__ __forceinline__ void store(void* base, int64_t elem) const {
-    using Bits = typename Elem<DT>::Bits;
-    Bits* p = static_cast<Bits*>(base) + elem;
-    if constexpr (VEC == 1) *p = static_cast<Bits>(w[0]);
-    else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (elem_bytes<DT>() == 4) return __uint_as_float(w[i]);
     else if constexpr (VEC == 1) return elem_to_f32<DT>(w[0]);
