@@ -211,7 +211,8 @@ __device__ __forceinline__ void load_units(const int32_t* offsets, int E, int ro
 // `put(b, phase)` waits until the buffer is free, `done(b)` tells the epilogue.
 // kAhead K blocks' loads are on their way while the group before is written, the
 // next unit's first ones behind a unit's last: an L2 read takes longer than a K
-// block.
+// block.  (sa is read by ordinary loads: it may have been written while this
+// kernel already ran, which read-only loads rule out.)
 constexpr int kAhead = 4;
 template <int ROWS, int BUFS, class Put, class Done>
 __device__ __forceinline__ void factor_units(const Fp8GemmArgs& a, const UnitMap& um, int u,
@@ -238,7 +239,7 @@ __device__ __forceinline__ void factor_units(const Fp8GemmArgs& a, const UnitMap
       const bool in = j < nn;
       nw[j] = in ? __ldg(sw + kb + j) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) na[j][i] = in && 32 * i < rows ? __ldg(sa + 32 * i) : 0.f;
+      for (int i = 0; i < kPer; ++i) na[j][i] = in && 32 * i < rows ? sa[32 * i] : 0.f;
       sa += a.lds;
     }
     kb += kAhead;
