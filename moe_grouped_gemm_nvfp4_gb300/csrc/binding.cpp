@@ -120,7 +120,17 @@ void check(const char* name, int status) {
 
 PyObject* give(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 
-// dispatch(x, route_pos, expert_offsets | None, R | -1) -> [R, D]
+// Route-ordered rows for a kernel to write.  `zero`: rows that no route names are
+// zero; with expert_offsets the kernel zeroes them, without them nothing says
+// which rows those are, so all are.
+Tensor route_rows(const On& on, at::IntArrayRef shape, at::ScalarType type, const int32_t* off,
+                  bool zero) {
+  Tensor t = on.empty(shape, type);
+  if (zero && !off) t.zero_();
+  return t;
+}
+
+// dispatch(x, route_pos, expert_offsets | None, R | -1, zero) -> [R, D]
 PyObject* dispatch(PyObject* const* a) {
   Tensor x = tensor(a[0], "x: expected a tensor");
   const Tensor& pos = tensor(a[1], "route_pos: expected a tensor");
@@ -134,7 +144,7 @@ PyObject* dispatch(PyObject* const* a) {
   x = rows_of(x);
   int64_t R = integer(a[3]);
   if (R < 0) R = pos.numel();
-  Tensor out = on.empty({R, x.size(1)}, x.scalar_type());
+  Tensor out = route_rows(on, {R, x.size(1)}, x.scalar_type(), off, PyObject_IsTrue(a[4]) == 1);
   check("nvfp4_tokens_dispatch",
         nvfp4_tokens_dispatch(x.data_ptr(), row_stride(x), p, off, E, pos.size(0),
                               static_cast<int32_t>(pos.size(1)), R, x.size(1), type,
@@ -167,7 +177,7 @@ PyObject* combine(PyObject* const* a) {
   return give(std::move(out));
 }
 
-// combine_grad(dout, y, route_pos, weights, expert_offsets | None) -> (dy, dw)
+// combine_grad(dout, y, route_pos, weights, expert_offsets | None, zero) -> (dy, dw)
 PyObject* combine_grad(PyObject* const* a) {
   Tensor dout = tensor(a[0], "dout: expected a tensor");
   Tensor y = tensor(a[1], "y: expected a tensor");
@@ -188,7 +198,7 @@ PyObject* combine_grad(PyObject* const* a) {
   const int32_t* off = offsets(on, a[4], &E);
   dout = rows_of(dout);
   y = rows_of(y);
-  Tensor dy = on.empty(y.sizes(), y.scalar_type());
+  Tensor dy = route_rows(on, y.sizes(), y.scalar_type(), off, PyObject_IsTrue(a[5]) == 1);
   Tensor dw = on.empty(pos.sizes(), at::kFloat);
   check("nvfp4_tokens_combine_grad",
         nvfp4_tokens_combine_grad(dout.data_ptr(), row_stride(dout), y.data_ptr(), row_stride(y), p,
@@ -335,9 +345,9 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {
-    method<dispatch, 4>("dispatch"),
+    method<dispatch, 5>("dispatch"),
     method<combine, 3>("combine"),
-    method<combine_grad, 5>("combine_grad"),
+    method<combine_grad, 6>("combine_grad"),
     method<linear, 3>("linear"),
     method<expert_linear, 7>("expert_linear"),
     {"set_error", set_error, METH_O, nullptr},

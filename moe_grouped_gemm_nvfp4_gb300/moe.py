@@ -347,4 +347,4 @@ class Fp8MLP:
         offsets, pos = self.route(topk_ids)
         gate_up = fp8.expert_linear(x, *self.gate_up, offsets, pos)
         y = fp8.expert_linear(gate_up, *self.down, offsets, silu_mul=True)
-        return tokens.combine(y, pos, topk_weights)
+        return tokens.combine(y, pos, topk_weights, offsets)

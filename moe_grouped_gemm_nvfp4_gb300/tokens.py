@@ -37,7 +37,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, route_pos, expert_offsets, R):
         ctx.save_for_backward(route_pos)
-        return native().dispatch(x, route_pos, expert_offsets, R)
+        return native().dispatch(x, route_pos, expert_offsets, R, True)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -59,21 +59,23 @@ class _Combine(torch.autograd.Function):
         if weights is None:
             weights = torch.ones(route_pos.shape, dtype=torch.float32, device=y.device)
         dy, dw = native().combine_grad(dout, y, route_pos, weights,
-                                       offsets[0] if offsets else None)
+                                       offsets[0] if offsets else None, True)
         return dy, None, dw if ctx.needs_input_grad[2] else None, None
 
 
 def dispatch(x, route_pos, expert_offsets=None, R=None, stream=None):
     """x [T, D] -> rows in expert order [R, D] (R: T * topk unless given).  Rows
-    past expert_offsets[E] are zero; without expert_offsets, rows that no route
-    names are left unwritten."""
+    past expert_offsets[E] are zero.  Without expert_offsets, rows that no route
+    names are zero while torch records gradients (an expert's weight gradient
+    sums over every row, and zero times stale memory may be NaN), which costs a
+    fill of the buffer, and are left unwritten under no_grad."""
     R = -1 if R is None else R
     if stream is not None:
         with on_stream(stream):
             return dispatch(x, route_pos, expert_offsets, R)
     if x.requires_grad and torch.is_grad_enabled():
         return _Dispatch.apply(x, route_pos, expert_offsets, R)
-    return native().dispatch(x, route_pos, expert_offsets, R)
+    return native().dispatch(x, route_pos, expert_offsets, R, torch.is_grad_enabled())
 
 
 def dispatch_grad(dout, route_pos, stream=None):
@@ -87,8 +89,9 @@ def dispatch_grad(dout, route_pos, stream=None):
 
 def combine(y, route_pos, weights=None, expert_offsets=None, stream=None):
     """y [R, D] in expert order -> [T, D]: the sum of each token's routes, times
-    weights (FP32 [T, topk]) where given.  expert_offsets is used by the
-    backward pass alone: the gradient's rows past expert_offsets[E] are zero."""
+    weights (FP32 [T, topk]) where given.  The gradient's rows that no route names
+    are zero; expert_offsets, which only the backward pass uses, lets it zero the
+    rows past expert_offsets[E] instead of filling the whole buffer first."""
     if stream is not None:
         with on_stream(stream):
             return combine(y, route_pos, weights, expert_offsets)
@@ -104,5 +107,5 @@ def combine_grad(dout, y, route_pos, weights, expert_offsets=None, stream=None):
     names are left unwritten."""
     if stream is not None:
         with on_stream(stream):
-            return native().combine_grad(dout, y, route_pos, weights, expert_offsets)
-    return native().combine_grad(dout, y, route_pos, weights, expert_offsets)
+            return native().combine_grad(dout, y, route_pos, weights, expert_offsets, False)
+    return native().combine_grad(dout, y, route_pos, weights, expert_offsets, False)
