@@ -6,10 +6,13 @@
 // cost of the tensor-core path (a quantiser launch, tensor memory, the sum over a
 // cluster) is longer than moving them.  Here every block quantises the rows for
 // itself (the same codes as the quantiser's; K values, read from L2) and keeps
-// them in shared memory as FP32 products with their scales; each warp then
-// streams two weight rows, 16 bytes a lane and row, four steps on their way
-// ahead, expands the codes exactly (E4M3 -> FP16 -> FP32) and adds in FP32.  With
-// fewer weight rows than warps the warps of a block share the rows' K.
+// the codes' values in shared memory as FP32, their scales beside them; each warp
+// then streams two weight rows, 16 bytes a lane and row, four steps on their way
+// ahead, expands the codes exactly (E4M3 -> FP16 -> FP32) and adds 16 products in
+// FP32 before both scales, multiplied first, are applied: the sum of code products
+// stays below 16 * 448^2 and sa * sw in the range of the result, so that a row
+// near the type's largest values comes out as on the tensor cores.  With fewer
+// weight rows than warps the warps of a block share the rows' K.
 //
 // Grouped: one block column per route (blockIdx.y): the route's expert and, with
 // route_pos, its token are found by the block's threads side by side.
@@ -34,11 +37,13 @@ __device__ __forceinline__ void put(void* out, int64_t at, float v) {
 
 template <int DT, int M, bool GROUPED, bool SILU>
 __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const Fp8RowsArgs a, int ks) {
-  extern __shared__ float4 xs[];     // [M][steps][4][32]: conflict-free 16-byte reads
+  // code values [M][steps][4][32] (conflict-free 16-byte reads), scales [M][steps][4]
+  extern __shared__ float4 xs[];
   __shared__ float part[kWarps][kRows][M];
   __shared__ int route[2];           // expert, token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int steps = (a.K + 511) / 512;
+  float* xscale = reinterpret_cast<float*>(xs + M * steps * 128);
   const int per_block = kRows * (kWarps / ks);         // weight rows
   const int n0 = blockIdx.x * per_block + kRows * (warp / ks);
   const int kpart = warp % ks;
@@ -109,12 +114,11 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const Fp8RowsArgs a,
       }
       const BlockScale b(block_amax(v));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 q = e4m3x4_f32(e4m3x4(b.quotient(v[4 * j]), b.quotient(v[4 * j + 1]),
-                                           b.quotient(v[4 * j + 2]), b.quotient(v[4 * j + 3])));
+      for (int j = 0; j < 4; ++j)
         xs[((m * steps + s) * 4 + j) * 32 + lane] =
-            make_float4(q.x * b.scale, q.y * b.scale, q.z * b.scale, q.w * b.scale);
-      }
+            e4m3x4_f32(e4m3x4(b.quotient(v[4 * j]), b.quotient(v[4 * j + 1]),
+                              b.quotient(v[4 * j + 2]), b.quotient(v[4 * j + 3])));
+      if ((lane & 7) == 0) xscale[(m * steps + s) * 4 + (lane >> 3)] = b.scale;
     }
   }
   __syncthreads();
@@ -151,9 +155,11 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const Fp8RowsArgs a,
         }
       }
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
+      for (int m = 0; m < M; ++m) {
+        const float f = xscale[(m * steps + s) * 4 + (lane >> 3)] * cur.s[u];
 #pragma unroll
-        for (int m = 0; m < M; ++m) acc[i][m] = fmaf(sum[i][m], cur.s[u], acc[i][m]);
+        for (int i = 0; i < kRows; ++i) acc[i][m] = fmaf(sum[i][m], f, acc[i][m]);
+      }
     }
     cur = next;
   }
@@ -179,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const Fp8RowsArgs a,
 }
 
 constexpr size_t kMaxSmem = 160 * 1024;
+constexpr int64_t kStepBytes = 512 * 4 + 4 * 4;      // 512 code values and four scales
 
 template <int DT, int M, bool GROUPED, bool SILU>
 cudaError_t go(const Fp8RowsArgs& a, int sms, cudaStream_t s) {
@@ -189,7 +196,7 @@ cudaError_t go(const Fp8RowsArgs& a, int sms, cudaStream_t s) {
          (a.K + 511) / 512 >= 4 * ks)
     ks *= 2;
   const int per_block = kRows * (kWarps / ks);
-  const size_t smem = static_cast<size_t>(M) * ((a.K + 511) / 512) * 512 * 4;
+  const size_t smem = static_cast<size_t>(M * ((a.K + 511) / 512) * kStepBytes);
   const dim3 grid(static_cast<unsigned>((a.N + per_block - 1) / per_block),
                   static_cast<unsigned>(columns), 1);
   fp8_rows_kernel<DT, M, GROUPED, SILU><<<grid, kThreads, smem, s>>>(a, ks);
@@ -242,7 +249,7 @@ cudaError_t init_fp8_rows_attributes() {
 // up to 20 MB.
 bool fp8_few_rows(int64_t R, int64_t n_pos, int64_t N, int64_t K, bool grouped) {
   if (R > (grouped ? kFp8FewRoutes : kFp8FewRows) || n_pos > 4 * kFp8FewRoutes) return false;
-  if ((grouped ? 1 : R) * ((K + 511) / 512) * 2048 > static_cast<int64_t>(kMaxSmem)) return false;
+  if ((grouped ? 1 : R) * ((K + 511) / 512) * kStepBytes > static_cast<int64_t>(kMaxSmem)) return false;
   return R * N * K <= ((grouped ? 20LL : 32LL) << 20);
 }
 
