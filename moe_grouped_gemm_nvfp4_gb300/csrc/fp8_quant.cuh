@@ -42,7 +42,8 @@ __device__ __forceinline__ float4 e4m3x4_f32(uint32_t codes) {
 // representable exactly; an E4M3 rounding border has five significant bits, so it
 // is met exactly or missed by at least 2^-16 of its value, far more than the
 // step's error.  No overflow: p and a' stay below the largest float, q0 below
-// 448 (1 + 2^-22).
+// 448 (1 + 2^-22).  That is quotient(); the gate's product, formed in FP32 with
+// rounding errors of its own, takes it too.
 struct BlockScale {
   float unit, inv, scale;
   __device__ __forceinline__ explicit BlockScale(float amax) {
@@ -55,6 +56,36 @@ struct BlockScale {
     const float p = x * 0.875f;
     const float q = p * inv;
     return fmaf(fmaf(-q, unit, p), inv, q);
+  }
+};
+
+// The quotient for FP32 x, where 0.875 x is a sum of two floats, p + pl, and may
+// miss a border by 2^-29 of its value only.  The residual step with pl included
+// returns the nearest float, which lies on the border or on the quotient's side of
+// it; then the sign of what is left, (p - q a') + pl with the first term exact,
+// moves a q of even mantissa (a border's is) one step towards the quotient.  Blocks
+// below 2^-40 are scaled up (exactly) so that the residuals do not underflow.
+// (Without all that one normal weight in two million got the neighbouring code.)
+struct BlockScale32 {
+  float up, unit, inv, scale;
+  __device__ __forceinline__ explicit BlockScale32(float amax) {
+    const BlockScale b(amax);
+    const bool low = b.unit < 1.7763568394002505e-15f;     // 2^-49
+    up = low ? 1.152921504606847e18f : 1.f;                // 2^60
+    unit = b.unit * up;
+    inv = low ? __frcp_rn(unit) : b.inv;
+    scale = b.scale;
+  }
+  __device__ __forceinline__ float quotient(float x) const {
+    const float xu = x * up;
+    const float p = xu * 0.875f;
+    const float pl = fmaf(xu, 0.875f, -p);
+    float q = p * inv;
+    q = fmaf(fmaf(-q, unit, p) + pl, inv, q);
+    const float left = fmaf(-q, unit, p) + pl;
+    const uint32_t bits = __float_as_uint(q);
+    const bool away = ((bits ^ __float_as_uint(left)) >> 31) == 0;   // from zero
+    return left != 0.f && (bits & 1u) == 0 ? __uint_as_float(bits + (away ? 1u : ~0u)) : q;
   }
 };
 

@@ -10,6 +10,8 @@
 // HBM (2 bytes read + fanout * (1 + 4/128) written per element): 8192 x 8192 37 us,
 // 8192 x 6144 to eight positions each 97 us, 0.8 of the copy rate; the scales,
 // written four bytes at a time into their K-block-major matrix, are what it lacks.
+#include <type_traits>
+
 #include "fp8.h"
 #include "fp8_quant.cuh"
 
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_weights_kernel(
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) amax = fmaxf(amax, part[i]);
-  const BlockScale b(amax);
+  const std::conditional_t<DT == NVFP4_FP32, BlockScale32, BlockScale> b(amax);
   if (on)
     for (int r = half; r < n_rows; r += 2) {
       Pack<DT, 1> v;
