@@ -7,7 +7,8 @@ Weights are codes [N, K] (or [E, N, K]) and scales [ceil(N/128), ceil(K/128)]
 Activations are BF16 or FP16 rows, quantised inside `linear` and
 `expert_linear`.  The gradient of the activations is the same product with the
 weights transposed (`transpose_weights`, prepared once); the weights themselves
-are frozen.
+are frozen.  The quantisers round and have no derivative; the products refuse
+tensors that would lose one.
 
 Work goes to the current stream, or to `stream` (a torch stream or a raw
 handle), where outputs and workspace are then allocated too.
@@ -18,7 +19,7 @@ import torch
 
 from . import nvfp4 as F
 from .nvfp4 import native
-from .tokens import on_stream
+from .tokens import on_stream, refuse_tangents
 
 BLOCK = 128
 
@@ -76,18 +77,21 @@ def transpose_weights(w, w_scale):
     return codes, w_scale.transpose(-1, -2).contiguous()
 
 
-def _refuse_grad(x):
+def _refuse_grad(*tensors):
     """The products take no part in autograd; losing a gradient silently is worse
-    than an error."""
-    if x.requires_grad and torch.is_grad_enabled():
+    than an error.  (torch.nn.Parameter requires a gradient unless told not to,
+    scales and codes too.)"""
+    if torch.is_grad_enabled() and any(
+            getattr(t, "requires_grad", False) for t in tensors):
         raise RuntimeError("FP8 products are not differentiable by themselves: call them in an "
                            "autograd.Function (the gradient is the product with "
-                           "transpose_weights) or under no_grad")
+                           "transpose_weights; the weights are frozen) or under no_grad")
+    refuse_tangents(*tensors)
 
 
 def linear(x, w, w_scale, stream=None):
     """y = x . w^T: x [.., K] BF16 or FP16, w codes [N, K] -> [.., N] in x's type."""
-    _refuse_grad(x)
+    _refuse_grad(x, w, w_scale)
     if stream is not None:
         with on_stream(stream):
             return linear(x, w, w_scale)
@@ -105,7 +109,7 @@ def expert_linear(x, w, w_scale, expert_offsets, route_pos=None, R=None, silu_mu
     without, x is in expert order already.  silu_mul: x holds gate and up halves
     [.., 2K], the rows are SiLU(gate) * up.  Rows past expert_offsets[E] are
     zero."""
-    _refuse_grad(x)
+    _refuse_grad(x, w, w_scale)
     R = -1 if R is None else R
     if stream is not None:
         with on_stream(stream):

@@ -8,11 +8,12 @@ negative for a dropped route, and expert_offsets int32 [E + 1].  Rows are BF16,
 FP16 or FP32 of any width; rows whose elements are not neighbours are copied
 first, any other row stride is used as it is.
 
-`dispatch_grad` and `combine_grad` are the gradients as plain calls; they
-enqueue kernels only, so that a step made of them can be captured into a CUDA
-graph.  (A captured step should not run autograd's backward over leaves that an
-eager graph still holds: torch binds a leaf's accumulation to the stream of its
-first use.)
+`dispatch_grad` and `combine_grad` are the gradients as plain calls, which take no
+part in autograd; they enqueue kernels only, so that a step made of them can be
+captured into a CUDA graph.  (A captured step should not run autograd's backward
+over leaves that an eager graph still holds: torch binds a leaf's accumulation to
+the stream of its first use.)  There is no forward-mode derivative: tensors that
+carry a tangent are refused.
 
 Work goes to the current stream, or to `stream` (a torch stream or a raw
 handle), where the outputs are then allocated too.  The arithmetic runs in the
@@ -21,6 +22,7 @@ CUDA kernels; sums are FP32 in a fixed order.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from .nvfp4 import native
 
@@ -31,6 +33,15 @@ def on_stream(stream):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
+
+
+def refuse_tangents(*tensors):
+    """Forward-mode tangents would be lost (the derivative zero) without an error;
+    `requires_grad` does not show them.  (No level is open outside dual_level().)"""
+    if forward_ad._current_level >= 0 and any(
+            isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
+            for t in tensors):
+        raise RuntimeError("no forward-mode derivative: a tensor carries a tangent")
 
 
 class _Dispatch(torch.autograd.Function):
@@ -69,6 +80,7 @@ def dispatch(x, route_pos, expert_offsets=None, R=None, stream=None):
     names are zero while torch records gradients (an expert's weight gradient
     sums over every row, and zero times stale memory may be NaN), which costs a
     fill of the buffer, and are left unwritten under no_grad."""
+    refuse_tangents(x)
     R = -1 if R is None else R
     if stream is not None:
         with on_stream(stream):
@@ -81,6 +93,7 @@ def dispatch(x, route_pos, expert_offsets=None, R=None, stream=None):
 def dispatch_grad(dout, route_pos, stream=None):
     """Gradient of `dispatch`: dout [R, D] -> [T, D], the sum over each token's
     routes."""
+    refuse_tangents(dout)
     if stream is not None:
         with on_stream(stream):
             return native().combine(dout, route_pos, None)
@@ -92,6 +105,7 @@ def combine(y, route_pos, weights=None, expert_offsets=None, stream=None):
     weights (FP32 [T, topk]) where given.  The gradient's rows that no route names
     are zero; expert_offsets, which only the backward pass uses, lets it zero the
     rows past expert_offsets[E] instead of filling the whole buffer first."""
+    refuse_tangents(y, weights)
     if stream is not None:
         with on_stream(stream):
             return combine(y, route_pos, weights, expert_offsets)
@@ -105,6 +119,7 @@ def combine_grad(dout, y, route_pos, weights, expert_offsets=None, stream=None):
     """Gradient of `combine`: (dy [R, D], dweights FP32 [T, topk]).  Rows of dy
     past expert_offsets[E] are zero; without expert_offsets, rows that no route
     names are left unwritten."""
+    refuse_tangents(dout, y, weights)
     if stream is not None:
         with on_stream(stream):
             return native().combine_grad(dout, y, route_pos, weights, expert_offsets, False)
