@@ -10,8 +10,9 @@ weights transposed (`transpose_weights`, prepared once); the weights themselves
 are frozen.  The quantisers round and have no derivative; the products refuse
 tensors that would lose one.
 
-Work goes to the current stream, or to `stream` (a torch stream or a raw
-handle), where outputs and workspace are then allocated too.
+Work goes to the current stream of the tensors' device, whichever device is
+current, or to `stream` (a torch stream of that device or a raw handle), where
+outputs and workspace are then allocated too.
 """
 from __future__ import annotations
 
@@ -34,7 +35,7 @@ def quantize_rows(x, route_pos=None, R=None, silu_mul: bool = False, stream=None
     route_pos, row t goes to the rows route_pos[t, :] (R: their number unless
     given); rows that no route names are left unwritten."""
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, x.device):
             return quantize_rows(x, route_pos, R, silu_mul)
     if x.dim() != 2 or x.shape[1] == 0 or (silu_mul and x.shape[1] % 2):
         raise ValueError(f"x: expected rows, got shape {tuple(x.shape)}")
@@ -45,6 +46,8 @@ def quantize_rows(x, route_pos=None, R=None, silu_mul: bool = False, stream=None
         if route_pos.dim() != 2 or route_pos.dtype != torch.int32 \
                 or not route_pos.is_contiguous() or route_pos.shape[0] != T:
             raise ValueError("route_pos: expected contiguous int32 [T, topk]")
+        if route_pos.device != x.device:
+            raise ValueError("tensors on different devices")
         R = route_pos.numel() if R is None else R
     if x.stride(1) != 1 or (T > 1 and (x.stride(0) < width or x.stride(0) % 8)) \
             or x.data_ptr() % 16:
@@ -52,20 +55,22 @@ def quantize_rows(x, route_pos=None, R=None, silu_mul: bool = False, stream=None
     K = width // 2 if silu_mul else width
     codes = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty((_blocks(K), R), dtype=torch.float32, device=x.device)
-    F.nvfp4_fp8_quantize(x, codes, scales, F.NVFP4_FP8_SILU_MUL if silu_mul else 0, route_pos)
+    with torch.cuda.device_of(x):
+        F.nvfp4_fp8_quantize(x, codes, scales, F.NVFP4_FP8_SILU_MUL if silu_mul else 0, route_pos)
     return codes, scales
 
 
 def quantize_weights(w, stream=None):
     """[N, K] or [E, N, K] -> (codes, scales), one scale per 128 x 128 block."""
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, w.device):
             return quantize_weights(w)
     w3 = (w if w.dim() == 3 else w[None]).contiguous()
     E, N, K = w3.shape
     codes = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=w.device)
     scales = torch.empty((E, _blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
-    F.nvfp4_fp8_quantize_weights(w3, codes, scales)
+    with torch.cuda.device_of(w3):
+        F.nvfp4_fp8_quantize_weights(w3, codes, scales)
     return (codes, scales) if w.dim() == 3 else (codes[0], scales[0])
 
 
@@ -93,7 +98,7 @@ def linear(x, w, w_scale, stream=None):
     """y = x . w^T: x [.., K] BF16 or FP16, w codes [N, K] -> [.., N] in x's type."""
     _refuse_grad(x, w, w_scale)
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, x.device):
             return linear(x, w, w_scale)
     if x.dim() == 2:
         return native().linear(x, w, w_scale)
@@ -112,6 +117,6 @@ def expert_linear(x, w, w_scale, expert_offsets, route_pos=None, R=None, silu_mu
     _refuse_grad(x, w, w_scale)
     R = -1 if R is None else R
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, x.device):
             return native().expert_linear(x, w, w_scale, expert_offsets, route_pos, R, silu_mul)
     return native().expert_linear(x, w, w_scale, expert_offsets, route_pos, R, silu_mul)

@@ -335,14 +335,18 @@ class Fp8MLP:
 
     def route(self, topk_ids, stream=None):
         """topk_ids int32 [T, k] -> (expert_offsets [E + 1], route_pos [T, k])."""
-        offsets, _, _, pos = F.moe_route(topk_ids, self.gate_up[0].shape[0], stream)
+        if stream is not None:
+            with tokens.on_stream(stream, topk_ids.device):
+                return self.route(topk_ids)
+        with torch.cuda.device_of(topk_ids):
+            offsets, _, _, pos = F.moe_route(topk_ids, self.gate_up[0].shape[0])
         return offsets, pos.view(topk_ids.shape)
 
     def step(self, x, topk_ids, topk_weights, stream=None):
         """x [T, K] BF16 or FP16, topk_ids int32 [T, k], topk_weights FP32 [T, k]
         -> [T, N] in x's type."""
         if stream is not None:
-            with tokens.on_stream(stream):
+            with tokens.on_stream(stream, x.device):
                 return self.step(x, topk_ids, topk_weights)
         offsets, pos = self.route(topk_ids)
         gate_up = fp8.expert_linear(x, *self.gate_up, offsets, pos)

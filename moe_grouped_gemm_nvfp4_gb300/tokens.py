@@ -15,8 +15,9 @@ over leaves that an eager graph still holds: torch binds a leaf's accumulation t
 the stream of its first use.)  There is no forward-mode derivative: tensors that
 carry a tangent are refused.
 
-Work goes to the current stream, or to `stream` (a torch stream or a raw
-handle), where the outputs are then allocated too.  The arithmetic runs in the
+Work goes to the current stream of the tensors' device, whichever device is
+current, or to `stream` (a torch stream of that device or a raw handle), where the
+outputs are then allocated too.  The arithmetic runs in the
 CUDA kernels; sums are FP32 in a fixed order.
 """
 from __future__ import annotations
@@ -27,11 +28,16 @@ from torch.autograd import forward_ad
 from .nvfp4 import native
 
 
-def on_stream(stream):
-    """Context that makes `stream` (a torch stream or a raw handle) current, so
-    that memory freed on return is reused in that stream's order."""
+def on_stream(stream, device):
+    """Context that makes `stream` (a torch stream or a raw handle) of the tensors'
+    `device` current there, so that the calls find it and memory freed on return is
+    reused in that stream's order."""
+    if device.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(stream)
 
 
@@ -83,7 +89,7 @@ def dispatch(x, route_pos, expert_offsets=None, R=None, stream=None):
     refuse_tangents(x)
     R = -1 if R is None else R
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, x.device):
             return dispatch(x, route_pos, expert_offsets, R)
     if x.requires_grad and torch.is_grad_enabled():
         return _Dispatch.apply(x, route_pos, expert_offsets, R)
@@ -95,7 +101,7 @@ def dispatch_grad(dout, route_pos, stream=None):
     routes."""
     refuse_tangents(dout)
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, dout.device):
             return native().combine(dout, route_pos, None)
     return native().combine(dout, route_pos, None)
 
@@ -107,7 +113,7 @@ def combine(y, route_pos, weights=None, expert_offsets=None, stream=None):
     rows past expert_offsets[E] instead of filling the whole buffer first."""
     refuse_tangents(y, weights)
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, y.device):
             return combine(y, route_pos, weights, expert_offsets)
     if (y.requires_grad or (weights is not None and weights.requires_grad)) \
             and torch.is_grad_enabled():
@@ -121,6 +127,6 @@ def combine_grad(dout, y, route_pos, weights, expert_offsets=None, stream=None):
     names are left unwritten."""
     refuse_tangents(dout, y, weights)
     if stream is not None:
-        with on_stream(stream):
+        with on_stream(stream, y.device):
             return native().combine_grad(dout, y, route_pos, weights, expert_offsets, False)
     return native().combine_grad(dout, y, route_pos, weights, expert_offsets, False)
