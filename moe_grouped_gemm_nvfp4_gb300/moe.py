@@ -338,6 +338,8 @@ class Fp8MLP:
         if stream is not None:
             with tokens.on_stream(stream, topk_ids.device):
                 return self.route(topk_ids)
+        if topk_ids.dim() != 2 or topk_ids.dtype != torch.int32 or not topk_ids.is_contiguous():
+            raise ValueError("topk_ids: expected contiguous int32 [T, k]")
         with torch.cuda.device_of(topk_ids):
             offsets, _, _, pos = F.moe_route(topk_ids, self.gate_up[0].shape[0])
         return offsets, pos.view(topk_ids.shape)
