@@ -86,17 +86,30 @@ def _build_binding(verbose: bool) -> None:
     os.replace(tmp, BINDING_PATH)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles the library and the binding if needed; returns the library's path."""
-    lib, binding = force or _stale(), force or _binding_stale()
-    if lib or binding:
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compiles the library if needed; returns its path."""
+    if force or _stale():
         os.makedirs(OUT_DIR, exist_ok=True)
+        _build_library(verbose)
+    return LIB_PATH
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compiles the binding if needed; returns its path.  It alone needs g++ and the
+    headers of Python and torch."""
+    if force or _binding_stale():
+        os.makedirs(OUT_DIR, exist_ok=True)
+        _build_binding(verbose)
+    return BINDING_PATH
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compiles the library and, beside it, the binding if needed; returns the
+    library's path."""
     with ThreadPoolExecutor(max_workers=1) as ex:
-        job = ex.submit(_build_binding, verbose) if binding else None
-        if lib:
-            _build_library(verbose)
-        if job is not None:
-            job.result()
+        job = ex.submit(build_binding, force, verbose)
+        build_library(force, verbose)
+        job.result()
     return LIB_PATH
 
 

@@ -120,7 +120,7 @@ def load() -> ctypes.CDLL:
     """Loads the in-tree library (building it first if sources are newer)."""
     global _lib
     if _lib is None:
-        path = _build.build()
+        path = _build.build_library()
         if not os.path.exists(path):
             raise RuntimeError(f"NVFP4 CUDA library missing: {path}")
         # global symbols: the native binding's C entry points are these
@@ -136,13 +136,13 @@ def load() -> ctypes.CDLL:
 def native():
     """The native binding (csrc/binding.cpp): checks, output allocation and the C
     call of the hot entry points in one native function each, on the current
-    stream."""
+    stream.  Built on first use if its source is newer: nothing else needs it."""
     global _native
     if _native is None:
         load()
-        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.BINDING_PATH)
-        spec = importlib.util.spec_from_file_location("_binding", _build.BINDING_PATH,
-                                                      loader=loader)
+        path = _build.build_binding()
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+        spec = importlib.util.spec_from_file_location("_binding", path, loader=loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         module.set_error(NVFP4Error)
