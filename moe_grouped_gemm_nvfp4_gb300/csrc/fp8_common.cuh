@@ -176,13 +176,17 @@ __device__ __forceinline__ Unit unit_at(const UnitMap& m, int u) {
 
 // Fills first/tiles from the device offsets (whole block; one warp scans).
 // An expert whose offsets are not monotone inside [0, rows] counts as empty
-// and the error is recorded.
+// and the error is recorded.  Offsets that go back and forth would count the same
+// rows many times and run over the 32-bit units, so the tiles end where those of
+// disjoint experts must (the bound the launcher checks); each stays in its rows.
 __device__ __forceinline__ void load_units(const int32_t* offsets, int E, int rows, int width,
                                            int* first, int* tiles, int* status) {
   for (int i = threadIdx.x; i <= E; i += blockDim.x) first[i] = __ldg(offsets + i);
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
+    const int some = min(rows, E);
+    const int limit = some + (rows - some) / width;
     int base = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
@@ -198,8 +202,8 @@ __device__ __forceinline__ void load_units(const int32_t* offsets, int E, int ro
         const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (e < E) tiles[e] = base + incl - n;
-      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (e < E) tiles[e] = min(base + incl - n, limit);
+      base = min(base + __shfl_sync(0xFFFFFFFFu, incl, 31), limit);
     }
     if (lane == 0) tiles[E] = base;
   }
