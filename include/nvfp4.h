@@ -622,7 +622,7 @@ nvfp4_status nvfp4_tokens_combine_grad(const void* dout, int64_t ld, const void*
  * [rows, 2 * cols], gate half first, the product formed in FP32).  route_pos
  * (int32 [rows, fanout], or NULL): row i is written to the rows route_pos[i, :]
  * of codes and scales (out_rows rows), negative positions are skipped; NULL:
- * fanout must be 1 and out_rows == rows.  A block that holds an infinity or
+ * fanout must be 1 and out_rows == rows (unless rows is 0).  A block that holds an infinity or
  * NaN quantises to values that make its row's products NaN. */
 nvfp4_status nvfp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld,
                                 int32_t dtype, uint32_t flags, const int32_t* route_pos,

@@ -221,7 +221,8 @@ nvfp4_status check_quantize(const void* x, int64_t rows, int64_t cols, int64_t l
   if (rows < 0 || cols <= 0 || ld < width || fanout <= 0 || out_rows < 0 || !is_dtype(dtype) ||
       (flags & ~NVFP4_FP8_SILU_MUL))
     return NVFP4_ERR_INVALID_ARG;
-  if (!route_pos && (fanout != 1 || out_rows != rows)) return NVFP4_ERR_INVALID_ARG;
+  // (an empty tensor of positions has no address)
+  if (!route_pos && rows > 0 && (fanout != 1 || out_rows != rows)) return NVFP4_ERR_INVALID_ARG;
   if ((rows > 0 && !x) || (out_rows > 0 && (!codes || !scales))) return NVFP4_ERR_INVALID_ARG;
   if (dtype == NVFP4_FP32 || cols % 16 != 0 || ld % 8 != 0 || out_rows > 0x7FFFFFFFLL ||
       cols > (1LL << 30) || !aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4) ||
