@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -228,11 +229,24 @@ void check_product(const Tensor& x, int64_t K, const Tensor& w, const Tensor& sc
        "x: expected BF16 or FP16");
 }
 
+// The products take no part in autograd; losing a gradient silently is worse than an
+// error.  (torch.nn.Parameter requires a gradient unless told not to, scales and
+// codes too.)
+void no_gradient(const Tensor& x, const Tensor& w, const Tensor& scale) {
+  if (c10::GradMode::is_enabled() &&
+      (x.requires_grad() || w.requires_grad() || scale.requires_grad()))
+    throw std::runtime_error(
+        "FP8 products are not differentiable by themselves: call them in an autograd.Function "
+        "(the gradient is the product with transpose_weights; the weights are frozen) or under "
+        "no_grad");
+}
+
 // linear(x, w, w_scale) -> [M, N]; x [M, K]
 PyObject* linear(PyObject* const* a) {
   Tensor x = tensor(a[0], "x: expected a tensor");
   const Tensor& w = tensor(a[1], "w: expected a tensor");
   const Tensor& scale = tensor(a[2], "w_scale: expected a tensor");
+  no_gradient(x, w, scale);
   need(x.dim() == 2, "x: expected rows [M, K]");
   check_product(x, x.size(1), w, scale, 2);
   const On on(x);
@@ -256,6 +270,7 @@ PyObject* expert_linear(PyObject* const* a) {
   Tensor x = tensor(a[0], "x: expected a tensor");
   const Tensor& w = tensor(a[1], "w: expected a tensor");
   const Tensor& scale = tensor(a[2], "w_scale: expected a tensor");
+  no_gradient(x, w, scale);
   const int silu = PyObject_IsTrue(a[6]);
   need(x.dim() == 2, "x: expected rows");
   const int64_t K = silu ? x.size(1) / 2 : x.size(1);

@@ -17,6 +17,7 @@ outputs and workspace are then allocated too.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import nvfp4 as F
 from .nvfp4 import native
@@ -82,21 +83,10 @@ def transpose_weights(w, w_scale):
     return codes, w_scale.transpose(-1, -2).contiguous()
 
 
-def _refuse_grad(*tensors):
-    """The products take no part in autograd; losing a gradient silently is worse
-    than an error.  (torch.nn.Parameter requires a gradient unless told not to,
-    scales and codes too.)"""
-    if torch.is_grad_enabled() and any(
-            getattr(t, "requires_grad", False) for t in tensors):
-        raise RuntimeError("FP8 products are not differentiable by themselves: call them in an "
-                           "autograd.Function (the gradient is the product with "
-                           "transpose_weights; the weights are frozen) or under no_grad")
-    refuse_tangents(*tensors)
-
-
 def linear(x, w, w_scale, stream=None):
     """y = x . w^T: x [.., K] BF16 or FP16, w codes [N, K] -> [.., N] in x's type."""
-    _refuse_grad(x, w, w_scale)
+    if forward_ad._current_level >= 0:
+        refuse_tangents(x, w, w_scale)
     if stream is not None:
         with on_stream(stream, x.device):
             return linear(x, w, w_scale)
@@ -114,7 +104,8 @@ def expert_linear(x, w, w_scale, expert_offsets, route_pos=None, R=None, silu_mu
     without, x is in expert order already.  silu_mul: x holds gate and up halves
     [.., 2K], the rows are SiLU(gate) * up.  Rows past expert_offsets[E] are
     zero."""
-    _refuse_grad(x, w, w_scale)
+    if forward_ad._current_level >= 0:
+        refuse_tangents(x, w, w_scale)
     R = -1 if R is None else R
     if stream is not None:
         with on_stream(stream, x.device):
