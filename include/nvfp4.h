@@ -569,7 +569,8 @@ nvfp4_status nvfp4_decode_attention(const void* q, const uint8_t* k_packed,
  * route_pos int32 [T, topk] is the position of each route's row in the
  * route-ordered buffer of R rows (as nvfp4_moe_route writes it); a negative
  * position is a route that was dropped and is neither read nor written.  The
- * live positions are distinct.  A position >= R is skipped and recorded as
+ * live positions are distinct and, where expert_offsets is given, those below
+ * expert_offsets[E].  A position >= R is skipped and recorded as
  * NVFP4_ERR_DEVICE_CHECK.  expert_offsets, where given, is nvfp4_moe_route's
  * [E + 1]: the rows from expert_offsets[E] on belong to no route and are set
  * to zero; NULL leaves rows without a route unwritten.  1 <= D <= 2^28 and any

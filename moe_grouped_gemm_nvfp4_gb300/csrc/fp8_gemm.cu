@@ -26,9 +26,9 @@
 // slice of K, and sum their registers through distributed shared memory in rank
 // order (no atomics, the same bits every time).  Every wait is bounded.
 //
-// Measured with the quantiser: 128 experts' gate_up at 16 tokens each 461 us (the
-// 3.2 GB of weights at the copy rate), down at 64 tokens 262 us (0.98), 8192^3 467
-// us (2.35 PFLOP/s, 0.63 of twice the BF16 rate), 4096 x 4096 x 6144 97 us, the
+// Measured with the quantiser: 128 experts' gate_up at 16 tokens each 461 us (3.2
+// GB of weights at 7.0 TB/s; a copy moves 6.8), down at 64 tokens 262 us (6.7 TB/s),
+// 8192^3 467 us (2.35 PFLOP/s, 0.63 of twice the BF16 rate), 4096 x 4096 x 6144 97 us, the
 // skewed 65536-route prefill 1.82 ms.  Many tokens are bound by two things at once,
 // both per K block: the way through MMA warp, accumulator, epilogue and back
 // (about 430 cycles with the ring full; 355 without loads, reads and additions)
