@@ -43,8 +43,8 @@ def on_stream(stream, device):
 
 def refuse_tangents(*tensors):
     """Forward-mode tangents would be lost (the derivative zero) without an error;
-    `requires_grad` does not show them.  Called where a dual level is open
-    (forward_ad._current_level >= 0) and no other: a call of one token takes 5 us."""
+    `requires_grad` does not show them.  The calls come here only while a dual level
+    is open (forward_ad._current_level >= 0): a whole call of one token takes 5 us."""
     if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
            for t in tensors):
         raise RuntimeError("no forward-mode derivative: a tensor carries a tangent")

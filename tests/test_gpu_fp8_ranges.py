@@ -61,3 +61,18 @@ def test_gated_halves_of_large_activations(R):
     codes, scales = fp8.quantize_rows(gu, silu_mul=True)
     ref, mag = product(codes, scales, w[0], ws[0])
     check(y, ref, mag, K)
+
+
+@pytest.mark.parametrize("M", [2, 4])
+@pytest.mark.parametrize("N,K", [(256, 512), (130, 2064)])
+def test_few_rows_with_nan_or_infinity_stay_alone(M, N, K):
+    w, ws = weights(1, 1, N, K, 0.02)
+    x = normal(0, (M, K), torch.bfloat16)
+    want = fp8.linear(x, w[0], ws[0])
+    for bad in (float("inf"), float("nan")):
+        z = x.clone()
+        z[1, K - 1] = bad
+        y = fp8.linear(z, w[0], ws[0])
+        assert torch.isnan(y[1]).all()
+        keep = [m for m in range(M) if m != 1]
+        assert torch.equal(y[keep], want[keep])
