@@ -672,6 +672,109 @@ nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, in
                                      int64_t N, int64_t K, void* y, int64_t ldy, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows (BF16, FP16, FP32), with the residual's
+ * addition and the gradient.
+ *
+ *   h = x + residual            rounded to the rows' type (without a residual: x)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ * FP32 arithmetic on the stored h, one rounding.  x and residual [T, D] with any
+ * row stride >= D; h and y dense; weight [D] of weight_dtype: the rows' type or
+ * FP32.  1 <= D <= 16384, eps >= 0.  Rows whose bases, strides and width are
+ * multiples of 16 bytes move fastest.  h may be residual and y may be x (the
+ * same rows, in place).
+ * ------------------------------------------------------------------------ */
+
+/* residual NULL: h is not written. */
+nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld, const void* residual, int64_t ld_residual,
+                            int64_t T, int64_t D, int32_t dtype, const void* weight,
+                            int32_t weight_dtype, float eps, void* h, void* y, void* stream);
+
+/* y as E4M3 codes [T, D] with FP32 scales [ceil(D/128), T], as nvfp4_fp8_quantize
+ * makes them, taken from the unrounded y.  BF16 or FP16 rows; D % 16 == 0, row
+ * strides % 8 == 0, x, residual, weight, h and codes 16-byte aligned. */
+nvfp4_status nvfp4_rms_norm_fp8(const void* x, int64_t ld, const void* residual,
+                                int64_t ld_residual, int64_t T, int64_t D, int32_t dtype,
+                                const void* weight, int32_t weight_dtype, float eps, void* h,
+                                uint8_t* codes, float* scales, void* stream);
+
+/* Gradient of y (dy) and of h as an output of its own (dh, or NULL) -> dx [T, D],
+ * the gradient of x and of the residual alike, and dweight [D] of weight_dtype:
+ *   g = dy * weight,  r = 1 / sqrt(mean(h^2) + eps)
+ *   dx = r * (g - h * r^2 * mean(g * h)) + dh,   dweight = sum_t dy * h * r
+ * Sums in a fixed order: results repeat bit for bit.  workspace: 4-byte aligned,
+ * nvfp4_rms_norm_grad_workspace_bytes(T, D) bytes, overwritten. */
+size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t T, int64_t D);
+
+nvfp4_status nvfp4_rms_norm_grad(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
+                                 const void* dh, int64_t ld_dh, int64_t T, int64_t D,
+                                 int32_t dtype, const void* weight, int32_t weight_dtype,
+                                 float eps, void* dx, void* dweight, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Top-k gate of an MoE layer.  Logits [T, E] (BF16, FP16, FP32; row stride ld
+ * >= E): scores s = softmax(logits) or, with NVFP4_GATE_SIGMOID, 1 / (1 +
+ * exp(-logits)).  Chosen are the topk largest logits, or, with a bias (FP32
+ * [E]), the topk largest s + bias; best first, the lower number first among
+ * equals, a NaN as the largest value.  The order is that of the real sums
+ * (neighbours nearer than FP32 rounding are compared in FP64).  The weight of a
+ * chosen expert is s (without the bias), with NVFP4_GATE_RENORMALIZE over the sum
+ * of the chosen scores, times `scale`.  A row of -infinities has softmax scores
+ * 0, and a sum of 0 gives weights 0.  1 <= E <= 1024, topk <= min(E, 32).
+ * ------------------------------------------------------------------------ */
+#define NVFP4_GATE_SIGMOID 1u
+#define NVFP4_GATE_RENORMALIZE 2u
+
+nvfp4_status nvfp4_topk_gate(const void* logits, int64_t ld, int64_t T, int32_t E, int32_t dtype,
+                             int32_t topk, const float* bias, uint32_t flags, float scale,
+                             int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* Gradient of the weights (dweights, FP32 [T, topk]) -> dlogits, dense [T, E] of
+ * the logits' type.  topk_ids: the gate's choice; an expert outside [0, E) is
+ * skipped and recorded as NVFP4_ERR_DEVICE_CHECK. */
+nvfp4_status nvfp4_topk_gate_grad(const float* dweights, const void* logits, int64_t ld, int64_t T,
+                                  int32_t E, int32_t dtype, int32_t topk, const int32_t* topk_ids,
+                                  uint32_t flags, float scale, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A whole MoE layer for a few tokens, in one launch: router, gate, FP8 experts,
+ * weighted sum.
+ *
+ *   logits = x . router^T (FP32);  ids and weights by the gate (above)
+ *   h = SiLU(xq . gate_e^T) * (xq . up_e^T),   out = sum_k weight_k * hq_k . down_e^T
+ *
+ * with xq and hq the rows of x and of the FP32 h quantised as by
+ * nvfp4_fp8_quantize, FP32 sums in a fixed order and one rounding at the end.
+ *   x        [T, K] BF16 or FP16, row stride ld (% 8 == 0), 16-byte aligned
+ *   router   [E, K] dense, of x's type or FP32 (router_dtype), 16-byte aligned; or
+ *            NULL: topk_ids and topk_weights are inputs.  An id outside [0, E)
+ *            contributes nothing and is recorded as NVFP4_ERR_DEVICE_CHECK; an
+ *            expert that a token names twice counts with both weights.
+ *   bias, flags, scale: the gate's; without a router NULL, 0 and any
+ *   W1, s1   gate_up codes [E, 2 I, K] (gate half first), scales [E, ceil(2 I / 128),
+ *            ceil(K / 128)];  W2, s2: down codes [E, N, I], scales likewise
+ *   topk_ids, topk_weights  int32 and FP32 [T, topk]; outputs with a router
+ *   out      [T, N] of x's type, row stride ldo
+ * K % 16 == 0, I % 16 == 0.  T <= 16, T * topk <= 256, topk <= min(E, 32), E <= 1024,
+ * and the activations of the tokens have to fit shared memory beside the weights
+ * on their way: nvfp4_fp8_moe_layer_workspace_bytes is 0 for sizes that this call
+ * refuses as NVFP4_ERR_UNSUPPORTED.  workspace: 16-byte aligned, of that many
+ * bytes, overwritten; calls that may overlap need one each.  A cooperative launch
+ * (its blocks meet at barriers): it waits until every SM has room for a block.
+ * ------------------------------------------------------------------------ */
+size_t nvfp4_fp8_moe_layer_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I,
+                                           int64_t N);
+
+nvfp4_status nvfp4_fp8_moe_layer(const void* x, int64_t ld, int64_t T, int32_t dtype,
+                                 const void* router, int32_t router_dtype, const float* bias,
+                                 uint32_t flags, float scale, const uint8_t* W1, const float* s1,
+                                 const uint8_t* W2, const float* s2, int32_t E, int32_t topk,
+                                 int64_t K, int64_t I, int64_t N, int32_t* topk_ids,
+                                 float* topk_weights, void* out, int64_t ldo, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -25,11 +25,12 @@ SOURCES = ["api.cu", "quantize.cu", "route.cu", "gemm.cu", "gemm_pair.cu", "gemm
            "sparse.cu",
            "attention.cu", "attention_tc.cu", "attention_tc_wide.cu",
            "tokens.cu", "fp8_quantize.cu", "fp8_gemm.cu",
-           "fp8_rows.cu"]
+           "fp8_rows.cu", "norm.cu", "gate.cu", "fp8_moe.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "format.cuh", "attention.h",
                                                 "attention_tc_common.cuh",
                                                 "rows.cuh", "tokens.h", "fp8.h",
-                                                "fp8_common.cuh", "fp8_quant.cuh")] + [
+                                                "fp8_common.cuh", "fp8_quant.cuh", "norm.h",
+                                                "gate.h", "gate.cuh", "fp8_moe.h")] + [
     os.path.join(ROOT, "include", "nvfp4.h")]
 
 NVCC_FLAGS = [

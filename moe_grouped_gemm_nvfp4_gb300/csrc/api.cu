@@ -14,6 +14,9 @@
 #include "attention.h"
 #include "fp8.h"
 #include "tokens.h"
+#include "norm.h"
+#include "gate.h"
+#include "fp8_moe.h"
 
 namespace {
 
@@ -68,6 +71,7 @@ nvfp4_status device_state(DeviceState** out) {
       if (nvfp4::init_route_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_fp8_gemm_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_fp8_rows_attributes() != cudaSuccess) return cuda_fail();
+      if (nvfp4::init_fp8_moe_attributes() != cudaSuccess) return cuda_fail();
     }
     if (!g_encode) {
       void* fn = nullptr;
@@ -356,6 +360,71 @@ nvfp4_status fp8_linear_impl(const void* x, int64_t rows, int64_t ld, int32_t dt
   return fp8_gemm_impl(d, codes, ldq, scales, W, sW, offsets, E, R, N, K, y, ldy, dtype, rows > 0,
                        stream);
 }
+
+nvfp4_status launched(cudaError_t e) {
+  if (e == cudaErrorInvalidConfiguration) {
+    cudaGetLastError();
+    return NVFP4_ERR_UNSUPPORTED;
+  }
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail();
+}
+
+// Rows, weight and eps of a norm and of its gradient.
+nvfp4_status check_norm(int64_t T, int64_t D, int32_t dtype, const void* weight,
+                        int32_t weight_dtype, float eps) {
+  if (T < 0 || D <= 0 || !is_dtype(dtype) || !is_dtype(weight_dtype) || !weight || !(eps >= 0.f))
+    return NVFP4_ERR_INVALID_ARG;
+  if (D > nvfp4::kNormMaxWidth || (weight_dtype != dtype && weight_dtype != NVFP4_FP32) ||
+      !aligned_to(weight, dtype_bytes(weight_dtype)))
+    return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+nvfp4_status check_norm_rows(const void* x, int64_t ld, const void* r, int64_t ld_r, int64_t T,
+                             int64_t D, int32_t dtype, const void* h) {
+  if (ld < D || (r && ld_r < D) || (T > 0 && (!x || (r && !h)))) return NVFP4_ERR_INVALID_ARG;
+  const unsigned es = dtype_bytes(dtype);
+  if (!aligned_to(x, es) || !aligned_to(r, es) || !aligned_to(h, es)) return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+nvfp4_status check_gate(const void* logits, int64_t ld, int64_t T, int32_t E, int32_t dtype,
+                        int32_t topk, uint32_t flags) {
+  if (T < 0 || E <= 0 || topk <= 0 || topk > E || ld < E || !is_dtype(dtype) ||
+      (flags & ~(NVFP4_GATE_SIGMOID | NVFP4_GATE_RENORMALIZE)) || (T > 0 && !logits))
+    return NVFP4_ERR_INVALID_ARG;
+  if (E > nvfp4::kGateMaxExperts || topk > nvfp4::kGateMaxTopk ||
+      !aligned_to(logits, dtype_bytes(dtype)))
+    return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+nvfp4::GateRule gate_rule(int32_t E, int32_t topk, const float* bias, uint32_t flags, float scale) {
+  nvfp4::GateRule r{};
+  r.bias = bias;
+  r.E = E;
+  r.topk = topk;
+  r.sigmoid = (flags & NVFP4_GATE_SIGMOID) ? 1 : 0;
+  r.renormalize = (flags & NVFP4_GATE_RENORMALIZE) ? 1 : 0;
+  r.scale = scale;
+  return r;
+}
+
+// The MoE layer's workspace: logits, h, route rows of the output, arrival counters.
+struct MoeWorkspace {
+  size_t h, part, arrived, bytes;
+};
+MoeWorkspace moe_workspace(int64_t T, int32_t topk, int32_t E, int64_t I, int64_t N) {
+  auto up = [](int64_t n) { return static_cast<size_t>((n + 15) / 16 * 16); };
+  MoeWorkspace w{};
+  const int64_t R = T * topk;
+  w.h = up(T * E * 4);
+  w.part = w.h + up(R * I * 4);
+  w.arrived = w.part + up(R * N * 4);
+  w.bytes = w.arrived + up((N + 15) / 16 * 4);
+  return w;
+}
+constexpr int kMoeFewestSms = 128;   // sizes that fit with these fit on every sm_103 part
 
 nvfp4_status fp8_gemm_checked(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
                               const int32_t* offsets, int32_t E, int64_t rows, int64_t N,
@@ -1401,6 +1470,220 @@ nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, in
   if (!expert_offsets) return NVFP4_ERR_INVALID_ARG;
   return fp8_linear_impl(x, rows, ld, dtype, flags, route_pos, fanout, W, sW, expert_offsets, E, R,
                          N, K, y, ldy, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------- norm, gate, MoE layer
+
+nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld, const void* residual, int64_t ld_residual,
+                            int64_t T, int64_t D, int32_t dtype, const void* weight,
+                            int32_t weight_dtype, float eps, void* h, void* y, void* stream) {
+  nvfp4_status st = check_norm(T, D, dtype, weight, weight_dtype, eps);
+  if (st == NVFP4_OK) st = check_norm_rows(x, ld, residual, ld_residual, T, D, dtype, h);
+  if (st != NVFP4_OK) return st;
+  if (T > 0 && !y) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned_to(y, dtype_bytes(dtype))) return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::NormArgs a{};
+  a.x = x;
+  a.ld = ld;
+  a.r = residual;
+  a.ld_r = ld_residual;
+  a.w = weight;
+  a.w_type = weight_dtype;
+  a.D = static_cast<int32_t>(D);
+  a.T = T;
+  a.eps = eps;
+  a.h = residual ? h : nullptr;
+  a.y = y;
+  return launched(nvfp4::launch_rms_norm(a, dtype, false, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_rms_norm_fp8(const void* x, int64_t ld, const void* residual,
+                                int64_t ld_residual, int64_t T, int64_t D, int32_t dtype,
+                                const void* weight, int32_t weight_dtype, float eps, void* h,
+                                uint8_t* codes, float* scales, void* stream) {
+  nvfp4_status st = check_norm(T, D, dtype, weight, weight_dtype, eps);
+  if (st == NVFP4_OK) st = check_norm_rows(x, ld, residual, ld_residual, T, D, dtype, h);
+  if (st != NVFP4_OK) return st;
+  if (T > 0 && (!codes || !scales)) return NVFP4_ERR_INVALID_ARG;
+  if (dtype == NVFP4_FP32 || D % 16 != 0 || (T > 1 && (ld % 8 != 0 || (residual && ld_residual % 8 != 0))) ||
+      !aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) ||
+      !aligned16(codes) || !aligned_to(scales, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::NormArgs a{};
+  a.x = x;
+  a.ld = ld;
+  a.r = residual;
+  a.ld_r = ld_residual;
+  a.w = weight;
+  a.w_type = weight_dtype;
+  a.D = static_cast<int32_t>(D);
+  a.T = T;
+  a.eps = eps;
+  a.h = residual ? h : nullptr;
+  a.codes = codes;
+  a.scales = scales;
+  return launched(nvfp4::launch_rms_norm(a, dtype, true, static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t T, int64_t D) {
+  if (T <= 0 || D <= 0 || D > nvfp4::kNormMaxWidth) return 0;
+  return static_cast<size_t>(nvfp4::norm_grad_parts(T, D)) * static_cast<size_t>(D) * sizeof(float);
+}
+
+nvfp4_status nvfp4_rms_norm_grad(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
+                                 const void* dh, int64_t ld_dh, int64_t T, int64_t D,
+                                 int32_t dtype, const void* weight, int32_t weight_dtype,
+                                 float eps, void* dx, void* dweight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  nvfp4_status st = check_norm(T, D, dtype, weight, weight_dtype, eps);
+  if (st == NVFP4_OK) st = check_norm_rows(h, ld_h, dh, ld_dh, T, D, dtype, dx);
+  if (st != NVFP4_OK) return st;
+  if (ld_dy < D || !dweight || (T > 0 && (!dy || !dx || !workspace))) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned_to(dy, dtype_bytes(dtype)) || !aligned_to(dweight, dtype_bytes(weight_dtype)) ||
+      !aligned_to(workspace, 4) || workspace_bytes < nvfp4_rms_norm_grad_workspace_bytes(T, D))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  nvfp4::NormArgs a{};
+  a.x = h;
+  a.ld = ld_h;
+  a.r = dh;
+  a.ld_r = ld_dh;
+  a.dy = dy;
+  a.ld_dy = ld_dy;
+  a.w = weight;
+  a.w_type = weight_dtype;
+  a.D = static_cast<int32_t>(D);
+  a.T = T;
+  a.eps = eps;
+  a.y = dx;
+  a.part = static_cast<float*>(workspace);
+  a.dw = dweight;
+  return launched(nvfp4::launch_rms_norm_grad(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_topk_gate(const void* logits, int64_t ld, int64_t T, int32_t E, int32_t dtype,
+                             int32_t topk, const float* bias, uint32_t flags, float scale,
+                             int32_t* topk_ids, float* topk_weights, void* stream) {
+  nvfp4_status st = check_gate(logits, ld, T, E, dtype, topk, flags);
+  if (st != NVFP4_OK) return st;
+  if (T > 0 && (!topk_ids || !topk_weights)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned_to(bias, 4) || !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::GateArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.rule = gate_rule(E, topk, bias, flags, scale);
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.status = d->status;
+  return launched(nvfp4::launch_topk_gate(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_topk_gate_grad(const float* dweights, const void* logits, int64_t ld, int64_t T,
+                                  int32_t E, int32_t dtype, int32_t topk, const int32_t* topk_ids,
+                                  uint32_t flags, float scale, void* dlogits, void* stream) {
+  nvfp4_status st = check_gate(logits, ld, T, E, dtype, topk, flags);
+  if (st != NVFP4_OK) return st;
+  if (T > 0 && (!dweights || !topk_ids || !dlogits)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned_to(dweights, 4) || !aligned_to(topk_ids, 4) || !aligned_to(dlogits, dtype_bytes(dtype)))
+    return NVFP4_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::GateArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.rule = gate_rule(E, topk, nullptr, flags, scale);
+  a.dweights = dweights;
+  a.chosen = topk_ids;
+  a.dlogits = dlogits;
+  a.status = d->status;
+  return launched(nvfp4::launch_topk_gate_grad(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_fp8_moe_layer_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I,
+                                           int64_t N) {
+  nvfp4::Fp8MoePlan p{};
+  if (T <= 0 || T > nvfp4::kMoeMaxTokens || topk <= 0 || E <= 0 || topk > E || K <= 0 || I <= 0 ||
+      N <= 0 || K % 16 != 0 || I % 16 != 0 ||
+      !nvfp4::fp8_moe_plan(static_cast<int>(T), topk, E, K, I, N, kMoeFewestSms, &p))
+    return 0;
+  return moe_workspace(T, topk, E, I, N).bytes;
+}
+
+nvfp4_status nvfp4_fp8_moe_layer(const void* x, int64_t ld, int64_t T, int32_t dtype,
+                                 const void* router, int32_t router_dtype, const float* bias,
+                                 uint32_t flags, float scale, const uint8_t* W1, const float* s1,
+                                 const uint8_t* W2, const float* s2, int32_t E, int32_t topk,
+                                 int64_t K, int64_t I, int64_t N, int32_t* topk_ids,
+                                 float* topk_weights, void* out, int64_t ldo, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (T < 0 || !is_dtype(dtype) || E <= 0 || topk <= 0 || topk > E || K <= 0 || I <= 0 || N <= 0 ||
+      ld < K || ldo < N || (flags & ~(NVFP4_GATE_SIGMOID | NVFP4_GATE_RENORMALIZE)) || !W1 || !s1 ||
+      !W2 || !s2 || (router && !is_dtype(router_dtype)) || (!router && (bias || flags)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!x || !topk_ids || !topk_weights || !out || !workspace))
+    return NVFP4_ERR_INVALID_ARG;
+  if (dtype == NVFP4_FP32 || (router && router_dtype != dtype && router_dtype != NVFP4_FP32) ||
+      !aligned16(x) || !aligned16(router) || !aligned16(W1) || !aligned16(W2) ||
+      !aligned_to(s1, 4) || !aligned_to(s2, 4) || !aligned_to(bias, 4) ||
+      !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4) || !aligned_to(out, 2) ||
+      !aligned16(workspace) || (T > 1 && ld % 8 != 0))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (T > 0) {
+    const size_t want = nvfp4_fp8_moe_layer_workspace_bytes(T, topk, E, K, I, N);
+    if (want == 0 || workspace_bytes < want) return NVFP4_ERR_UNSUPPORTED;
+  }
+  DeviceState* d = nullptr;
+  const nvfp4_status st = device_state(&d);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::Fp8MoePlan p{};
+  if (!nvfp4::fp8_moe_plan(static_cast<int>(T), topk, E, K, I, N, d->sms, &p))
+    return NVFP4_ERR_UNSUPPORTED;
+  const MoeWorkspace w = moe_workspace(T, topk, E, I, N);
+  char* ws = static_cast<char*>(workspace);
+  nvfp4::Fp8MoeArgs a{};
+  a.x = x;
+  a.ld = ld;
+  a.router = router;
+  a.router_type = router_dtype;
+  a.rule = gate_rule(E, topk, bias, flags, scale);
+  a.T = static_cast<int32_t>(T);
+  a.K = static_cast<int32_t>(K);
+  a.I = static_cast<int32_t>(I);
+  a.N = static_cast<int32_t>(N);
+  a.w1 = W1;
+  a.s1 = s1;
+  a.w2 = W2;
+  a.s2 = s2;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.out = out;
+  a.ldo = ldo;
+  a.logits = reinterpret_cast<float*>(ws);
+  a.h = reinterpret_cast<float*>(ws + w.h);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.arrived = reinterpret_cast<uint32_t*>(ws + w.arrived);
+  a.status = d->status;
+  return launched(nvfp4::launch_fp8_moe(a, p, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
-// Native binding of the calls whose host time matters (token movement and FP8
-// products, called many times per step on small batches): argument checks,
+// Native binding of the calls whose host time matters (token movement, FP8
+// products, norms, gates and the MoE layer for a few tokens, called many times per
+// step on small batches): argument checks,
 // output allocation and the C call without interpreter work in between.  The
 // ctypes binding of the same C entry points takes 5 to 10 us more per call.
 //
@@ -12,6 +13,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <initializer_list>
 #include <stdexcept>
 #include <string>
 
@@ -45,6 +47,15 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) {
     PyErr_Clear();
     throw BadArg("expected an integer");
+  }
+  return v;
+}
+
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw BadArg("expected a number");
   }
   return v;
 }
@@ -215,7 +226,7 @@ PyObject* combine_grad(PyObject* const* a) {
 
 int64_t blocks(int64_t n) { return (n + 127) / 128; }
 
-void check_product(const Tensor& x, int64_t K, const Tensor& w, const Tensor& scale, int dim) {
+void check_weights(int64_t K, const Tensor& w, const Tensor& scale, int dim) {
   need(w.dim() == dim && w.scalar_type() == at::kFloat8_e4m3fn && w.is_contiguous(),
        dim == 2 ? "w: expected contiguous float8_e4m3fn codes [N, K]"
                 : "w: expected contiguous float8_e4m3fn codes [E, N, K]");
@@ -225,6 +236,9 @@ void check_product(const Tensor& x, int64_t K, const Tensor& w, const Tensor& sc
            (dim == 2 || scale.size(0) == w.size(0)),
        "w_scale: expected contiguous FP32, one value per 128 x 128 block of w");
   need(K == w.size(dim - 1), "x: its columns are not the weights'");
+}
+void check_product(const Tensor& x, int64_t K, const Tensor& w, const Tensor& scale, int dim) {
+  check_weights(K, w, scale, dim);
   need(x.scalar_type() == at::kBFloat16 || x.scalar_type() == at::kHalf,
        "x: expected BF16 or FP16");
 }
@@ -313,6 +327,284 @@ PyObject* expert_linear(PyObject* const* a) {
   return give(std::move(y));
 }
 
+// linear_codes(codes, scales, w, w_scale, nvfp4_dtype) -> [M, N]
+PyObject* linear_codes(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "codes: expected a tensor");
+  const Tensor& sq = tensor(a[1], "scales: expected a tensor");
+  const Tensor& w = tensor(a[2], "w: expected a tensor");
+  const Tensor& scale = tensor(a[3], "w_scale: expected a tensor");
+  const int64_t type = integer(a[4]);
+  no_gradient(sq, w, scale);
+  need(q.dim() == 2 && q.scalar_type() == at::kFloat8_e4m3fn && q.is_contiguous() && q.size(1) > 0,
+       "codes: expected contiguous float8_e4m3fn [M, K]");
+  const int64_t M = q.size(0), K = q.size(1);
+  need(sq.dim() == 2 && sq.scalar_type() == at::kFloat && sq.is_contiguous() &&
+           sq.size(0) == blocks(K) && sq.size(1) == M,
+       "scales: expected contiguous FP32 [ceil(K / 128), M]");
+  check_weights(K, w, scale, 2);
+  const On on(q);
+  on.same(sq);
+  on.same(w);
+  on.same(scale);
+  const int64_t N = w.size(0);
+  Tensor y = on.empty({M, N}, type == NVFP4_FP32   ? at::kFloat
+                              : type == NVFP4_FP16 ? at::kHalf
+                                                   : at::kBFloat16);
+  check("nvfp4_fp8_gemm",
+        nvfp4_fp8_gemm(static_cast<const uint8_t*>(q.data_ptr()),
+                       static_cast<const float*>(sq.data_ptr()),
+                       static_cast<const uint8_t*>(w.data_ptr()),
+                       static_cast<const float*>(scale.data_ptr()), y.data_ptr(), M, N, K, N,
+                       static_cast<int32_t>(type), on.stream()));
+  return give(std::move(y));
+}
+
+PyObject* give(std::initializer_list<Tensor> ts) {
+  PyObject* all = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+  if (!all) return nullptr;
+  Py_ssize_t i = 0;
+  for (const Tensor& t : ts) PyTuple_SET_ITEM(all, i++, give(t));
+  return all;
+}
+
+// Weight of a norm over rows of width D.
+Tensor norm_weight(const On& on, PyObject* o, const Tensor& x) {
+  Tensor w = tensor(o, "weight: expected a tensor");
+  need(w.dim() == 1 && w.size(0) == x.size(1) &&
+           (w.scalar_type() == x.scalar_type() || w.scalar_type() == at::kFloat),
+       "weight: expected [D] of the rows' type or FP32");
+  on.same(w);
+  return w.contiguous();
+}
+
+// A second operand of x's shape and type, or None.
+Tensor like_rows(const On& on, PyObject* o, const Tensor& x, const char* what) {
+  if (o == Py_None) return {};
+  const Tensor& t = tensor(o, what);
+  need(t.sizes() == x.sizes() && t.scalar_type() == x.scalar_type(), what);
+  on.same(t);
+  return rows_of(t);
+}
+Tensor aligned_rows(const Tensor& t) { return t.defined() ? rows16_of(t) : t; }
+const void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+int64_t stride_or_0(const Tensor& t) { return t.defined() ? row_stride(t) : 0; }
+
+float epsilon(PyObject* o) {
+  const float eps = static_cast<float>(real(o));
+  need(eps >= 0.f, "eps: expected a number >= 0");
+  return eps;
+}
+
+// rms_norm(x, weight, residual | None, eps, fp8) -> (y, h) or (codes, scales, h);
+// without a residual no h
+PyObject* rms_norm(PyObject* const* a) {
+  Tensor x = tensor(a[0], "x: expected a tensor");
+  need(x.dim() == 2 && x.size(1) > 0, "x: expected rows [T, D]");
+  const int type = dtype_of(x);
+  const float eps = epsilon(a[3]);
+  const bool fp8 = PyObject_IsTrue(a[4]) == 1;
+  const On on(x);
+  Tensor w = norm_weight(on, a[1], x);
+  Tensor r = like_rows(on, a[2], x, "residual: expected rows of x's shape and type");
+  x = rows_of(x);
+  const int64_t T = x.size(0), D = x.size(1);
+  Tensor h;
+  if (r.defined()) h = on.empty({T, D}, x.scalar_type());
+  if (fp8) {
+    need(type != NVFP4_FP32 && D % 16 == 0,
+         "x: expected BF16 or FP16 rows whose width is a multiple of 16");
+    x = rows16_of(x);
+    r = aligned_rows(r);
+    if (reinterpret_cast<uintptr_t>(w.data_ptr()) & 15u) w = w.clone();
+    Tensor codes = on.empty({T, D}, at::kFloat8_e4m3fn);
+    Tensor scales = on.empty({blocks(D), T}, at::kFloat);
+    check("nvfp4_rms_norm_fp8",
+          nvfp4_rms_norm_fp8(x.data_ptr(), row_stride(x), ptr(r), stride_or_0(r), T, D, type,
+                             w.data_ptr(), dtype_of(w), eps, h.defined() ? h.data_ptr() : nullptr,
+                             static_cast<uint8_t*>(codes.data_ptr()),
+                             static_cast<float*>(scales.data_ptr()), on.stream()));
+    return h.defined() ? give({codes, scales, h}) : give({codes, scales});
+  }
+  Tensor y = on.empty({T, D}, x.scalar_type());
+  check("nvfp4_rms_norm",
+        nvfp4_rms_norm(x.data_ptr(), row_stride(x), ptr(r), stride_or_0(r), T, D, type,
+                       w.data_ptr(), dtype_of(w), eps, h.defined() ? h.data_ptr() : nullptr,
+                       y.data_ptr(), on.stream()));
+  return h.defined() ? give({y, h}) : give({y});
+}
+
+// rms_norm_grad(dy, h, weight, dh | None, eps) -> (dx, dweight)
+PyObject* rms_norm_grad(PyObject* const* a) {
+  Tensor h = tensor(a[1], "h: expected a tensor");
+  need(h.dim() == 2 && h.size(1) > 0, "h: expected rows [T, D]");
+  const int type = dtype_of(h);
+  const float eps = epsilon(a[4]);
+  const On on(h);
+  need(a[0] != Py_None, "dy: expected rows of h's shape and type");
+  Tensor dy = like_rows(on, a[0], h, "dy: expected rows of h's shape and type");
+  Tensor w = norm_weight(on, a[2], h);
+  Tensor dh = like_rows(on, a[3], h, "dh: expected rows of h's shape and type");
+  h = rows_of(h);
+  const int64_t T = h.size(0), D = h.size(1);
+  Tensor dx = on.empty({T, D}, h.scalar_type());
+  Tensor dw = on.empty({D}, w.scalar_type());
+  const size_t bytes = nvfp4_rms_norm_grad_workspace_bytes(T, D);
+  Tensor ws = on.empty({static_cast<int64_t>(bytes)}, at::kByte);
+  check("nvfp4_rms_norm_grad",
+        nvfp4_rms_norm_grad(dy.data_ptr(), row_stride(dy), h.data_ptr(), row_stride(h), ptr(dh),
+                            stride_or_0(dh), T, D, type, w.data_ptr(), dtype_of(w), eps,
+                            dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), bytes, on.stream()));
+  return give({dx, dw});
+}
+
+// flags from (sigmoid, renormalize)
+uint32_t gate_flags(PyObject* sigmoid, PyObject* renormalize) {
+  return (PyObject_IsTrue(sigmoid) == 1 ? NVFP4_GATE_SIGMOID : 0u) |
+         (PyObject_IsTrue(renormalize) == 1 ? NVFP4_GATE_RENORMALIZE : 0u);
+}
+
+Tensor gate_bias(const On& on, PyObject* o, int64_t E) {
+  if (o == Py_None) return {};
+  const Tensor& b = tensor(o, "bias: expected a tensor");
+  need(b.dim() == 1 && b.size(0) == E && b.scalar_type() == at::kFloat, "bias: expected FP32 [E]");
+  on.same(b);
+  return b.contiguous();
+}
+
+int32_t gate_topk(PyObject* o, int64_t E) {
+  const int64_t k = integer(o);
+  need(k > 0 && k <= E, "topk: expected 1 to E experts");
+  return static_cast<int32_t>(k < 1 << 20 ? k : 1 << 20);
+}
+
+// topk_gate(logits, topk, bias | None, sigmoid, renormalize, scale) -> (ids, weights)
+PyObject* topk_gate(PyObject* const* a) {
+  Tensor l = tensor(a[0], "logits: expected a tensor");
+  need(l.dim() == 2 && l.size(1) > 0, "logits: expected [T, E]");
+  const int type = dtype_of(l);
+  const int64_t T = l.size(0), E = l.size(1);
+  const int32_t k = gate_topk(a[1], E);
+  const On on(l);
+  const Tensor bias = gate_bias(on, a[2], E);
+  l = rows_of(l);
+  Tensor ids = on.empty({T, k}, at::kInt), w = on.empty({T, k}, at::kFloat);
+  check("nvfp4_topk_gate",
+        nvfp4_topk_gate(l.data_ptr(), row_stride(l), T, static_cast<int32_t>(E < 1 << 30 ? E : 1 << 30),
+                        type, k, static_cast<const float*>(ptr(bias)), gate_flags(a[3], a[4]),
+                        static_cast<float>(real(a[5])), static_cast<int32_t*>(ids.data_ptr()),
+                        static_cast<float*>(w.data_ptr()), on.stream()));
+  return give({ids, w});
+}
+
+const Tensor& chosen(const On& on, PyObject* o, int64_t T) {
+  const Tensor& ids = tensor(o, "topk_ids: expected a tensor");
+  need(ids.dim() == 2 && ids.size(0) == T && ids.size(1) > 0 && ids.scalar_type() == at::kInt &&
+           ids.is_contiguous(),
+       "topk_ids: expected contiguous int32 [T, topk]");
+  on.same(ids);
+  return ids;
+}
+
+// topk_gate_grad(dweights, logits, ids, sigmoid, renormalize, scale) -> dlogits
+PyObject* topk_gate_grad(PyObject* const* a) {
+  Tensor l = tensor(a[1], "logits: expected a tensor");
+  need(l.dim() == 2 && l.size(1) > 0, "logits: expected [T, E]");
+  const int type = dtype_of(l);
+  const int64_t T = l.size(0), E = l.size(1);
+  const On on(l);
+  const Tensor& ids = chosen(on, a[2], T);
+  Tensor dw = tensor(a[0], "dweights: expected a tensor");
+  need(dw.sizes() == ids.sizes() && dw.scalar_type() == at::kFloat,
+       "dweights: expected FP32 of topk_ids' shape");
+  on.same(dw);
+  dw = dw.contiguous();
+  l = rows_of(l);
+  Tensor dl = on.empty({T, E}, l.scalar_type());
+  check("nvfp4_topk_gate_grad",
+        nvfp4_topk_gate_grad(static_cast<const float*>(dw.data_ptr()), l.data_ptr(), row_stride(l),
+                             T, static_cast<int32_t>(E < 1 << 30 ? E : 1 << 30), type,
+                             static_cast<int32_t>(ids.size(1)),
+                             static_cast<const int32_t*>(ids.data_ptr()), gate_flags(a[3], a[4]),
+                             static_cast<float>(real(a[5])), dl.data_ptr(), on.stream()));
+  return give(std::move(dl));
+}
+
+// moe_layer(x, router | None, gate_up, gate_up_scale, down, down_scale, topk, bias | None,
+//           sigmoid, renormalize, scale, ids | None, weights | None)
+//   -> (out, ids, weights), or None for sizes that the call does not take
+PyObject* moe_layer(PyObject* const* a) {
+  Tensor x = tensor(a[0], "x: expected a tensor");
+  const Tensor& w1 = tensor(a[2], "gate_up: expected a tensor");
+  const Tensor& s1 = tensor(a[3], "gate_up scales: expected a tensor");
+  const Tensor& w2 = tensor(a[4], "down: expected a tensor");
+  const Tensor& s2 = tensor(a[5], "down scales: expected a tensor");
+  no_gradient(x, w1, s1);
+  no_gradient(x, w2, s2);
+  need(x.dim() == 2, "x: expected rows [T, K]");
+  check_product(x, x.size(1), w1, s1, 3);
+  need(w1.size(1) % 2 == 0, "gate_up: gate and up halves of one width");
+  const int64_t T = x.size(0), K = x.size(1), E = w1.size(0), I = w1.size(1) / 2;
+  check_weights(I, w2, s2, 3);
+  need(w2.size(0) == E, "down: expected as many experts as gate_up");
+  const int64_t N = w2.size(1);
+  const On on(x);
+  on.same(w1);
+  on.same(s1);
+  on.same(w2);
+  on.same(s2);
+  Tensor router, bias, ids, weights;
+  int32_t k;
+  uint32_t flags = 0;
+  float scale = 1.f;
+  if (a[1] != Py_None) {
+    router = tensor(a[1], "router: expected a tensor");
+    need(router.dim() == 2 && router.size(0) == E && router.size(1) == K &&
+             (router.scalar_type() == x.scalar_type() || router.scalar_type() == at::kFloat),
+         "router: expected [E, K] of x's type or FP32");
+    no_gradient(router, w1, s1);
+    on.same(router);
+    k = gate_topk(a[6], E);
+    bias = gate_bias(on, a[7], E);
+    flags = gate_flags(a[8], a[9]);
+    scale = static_cast<float>(real(a[10]));
+  } else {
+    ids = chosen(on, a[11], T);
+    weights = tensor(a[12], "topk_weights: expected a tensor");
+    need(weights.sizes() == ids.sizes() && weights.scalar_type() == at::kFloat,
+         "topk_weights: expected FP32 of topk_ids' shape");
+    no_gradient(weights, w1, s1);
+    on.same(weights);
+    weights = weights.contiguous();
+    need(ids.size(1) <= 1 << 20, "topk_ids: too many routes");
+    k = static_cast<int32_t>(ids.size(1));
+  }
+  const size_t bytes = T == 0 ? 0
+                              : nvfp4_fp8_moe_layer_workspace_bytes(T, k, static_cast<int32_t>(E), K,
+                                                                    I, N);
+  if (bytes == 0) Py_RETURN_NONE;
+  x = rows16_of(x);
+  if (router.defined()) {
+    router = router.contiguous();
+    if (reinterpret_cast<uintptr_t>(router.data_ptr()) & 15u) router = router.clone();
+    ids = on.empty({T, k}, at::kInt);
+    weights = on.empty({T, k}, at::kFloat);
+  }
+  Tensor out = on.empty({T, N}, x.scalar_type());
+  Tensor ws = on.empty({static_cast<int64_t>(bytes)}, at::kByte);
+  check("nvfp4_fp8_moe_layer",
+        nvfp4_fp8_moe_layer(x.data_ptr(), row_stride(x), T, dtype_of(x), ptr(router),
+                            router.defined() ? dtype_of(router) : dtype_of(x),
+                            static_cast<const float*>(ptr(bias)), flags, scale,
+                            static_cast<const uint8_t*>(w1.data_ptr()),
+                            static_cast<const float*>(s1.data_ptr()),
+                            static_cast<const uint8_t*>(w2.data_ptr()),
+                            static_cast<const float*>(s2.data_ptr()), static_cast<int32_t>(E), k, K,
+                            I, N, static_cast<int32_t*>(ids.data_ptr()),
+                            static_cast<float*>(weights.data_ptr()), out.data_ptr(), N,
+                            ws.data_ptr(), bytes, on.stream()));
+  return give({out, ids, weights});
+}
+
 // No C++ exception leaves a Python entry.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -365,6 +657,12 @@ PyMethodDef g_methods[] = {
     method<combine_grad, 6>("combine_grad"),
     method<linear, 3>("linear"),
     method<expert_linear, 7>("expert_linear"),
+    method<linear_codes, 5>("linear_codes"),
+    method<rms_norm, 5>("rms_norm"),
+    method<rms_norm_grad, 5>("rms_norm_grad"),
+    method<topk_gate, 6>("topk_gate"),
+    method<topk_gate_grad, 6>("topk_gate_grad"),
+    method<moe_layer, 13>("moe_layer"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

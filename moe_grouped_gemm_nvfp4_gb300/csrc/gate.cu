@@ -1,0 +1,143 @@
+// Top-k gate of an MoE layer and its gradient: a warp per token (gate.cuh).
+//
+// Gradient: with dp the gradient of the chosen scores (dw * scale, through the
+// division by their sum S where they are renormalised: (g - sum_j g_j w_j) / S),
+//
+//   softmax  dl = p (dp - sum_j dp_j p_j),   sigmoid  dl = dp s (1 - s)
+//
+// The sum vanishes for renormalised softmax weights: like the sigmoid's, that
+// gradient is zero outside the chosen experts and needs no other logits, so only the
+// chosen ones are read.  Bound: latency up to some thousand tokens, then HBM (the
+// logits once, the gradient's rows once).
+#include <cuda_fp16.h>
+
+#include "gate.h"
+#include "rows.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int L>
+__global__ void __launch_bounds__(kThreads) topk_gate_kernel(const GateArgs a, int type) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  float l[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = e < a.rule.E ? gate_logit(a.logits, t * a.ld + e, type) : -INFINITY;
+  }
+  int id;
+  float w;
+  gate_choose<L>(a.rule, l, &id, &w);
+  if (lane < a.rule.topk) {
+    a.ids[t * a.rule.topk + lane] = id;
+    a.weights[t * a.rule.topk + lane] = w;
+  }
+}
+
+template <int DT, int L>
+__global__ void __launch_bounds__(kThreads) topk_gate_grad_kernel(const GateArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const GateRule& r = a.rule;
+  const bool on = lane < r.topk;
+  int e = on ? __ldg(a.chosen + t * r.topk + lane) : -1;
+  float g = on ? __ldg(a.dweights + t * r.topk + lane) * r.scale : 0.f;
+  if (e >= r.E || (on && e < 0)) {
+    raise_status(a.status, NVFP4_ERR_DEVICE_CHECK);
+    e = -1;
+  }
+  const bool ok = e >= 0;
+  if (!ok) g = 0.f;
+  float l[L];
+  GateScores sc{0.f, 1.f, r.sigmoid};
+  float p;                                         // the chosen expert's score
+  const bool whole = !r.sigmoid && !r.renormalize;
+  const float chosen = ok ? gate_logit(a.logits, t * a.ld + e, DT) : -INFINITY;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int c = lane + 32 * i;
+      l[i] = c < r.E ? gate_logit(a.logits, t * a.ld + c, DT) : -INFINITY;
+    }
+    sc = gate_scores<L>(l, r.E, 0);
+  } else if (!r.sigmoid) {
+    sc.max = warp_max(chosen);
+  }
+  p = ok ? sc.of(chosen) : 0.f;
+  float dp = g, back = 0.f;
+  if (r.renormalize) {
+    const float sum = warp_sum(p);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float mean = warp_sum(g * (p * inv));
+    dp = ok ? (g - mean) * inv : 0.f;
+  }
+  if (whole) back = warp_sum(dp * p);
+  // what the chosen experts get, then the place of each in its lane's experts
+  float d = dp * p;
+  if (r.sigmoid && ok) {                           // s (1 - s) without the difference
+    const float q = expf(-fabsf(chosen));
+    d = dp * (q / ((1.f + q) * (1.f + q)));
+  }
+  float add[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) add[i] = 0.f;
+  for (int j = 0; j < r.topk; ++j) {
+    const int ej = __shfl_sync(kFullWarp, e, j);
+    const float dj = __shfl_sync(kFullWarp, d, j);
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (lane + 32 * i == ej) add[i] += dj;
+  }
+  using Bits = typename Elem<DT>::Bits;
+  Bits* out = static_cast<Bits*>(a.dlogits) + t * r.E;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int c = lane + 32 * i;
+    if (c < r.E) {
+      const float v = whole ? add[i] - sc.of(l[i]) * back : add[i];
+      out[c] = static_cast<Bits>(f32_to_elem<DT>(v));
+    }
+  }
+}
+
+template <int DT>
+cudaError_t grad(const GateArgs& a, unsigned g, cudaStream_t s) {
+  const int E = a.rule.E;
+  if (E <= 64) topk_gate_grad_kernel<DT, 2><<<g, kThreads, 0, s>>>(a);
+  else if (E <= 128) topk_gate_grad_kernel<DT, 4><<<g, kThreads, 0, s>>>(a);
+  else if (E <= 256) topk_gate_grad_kernel<DT, 8><<<g, kThreads, 0, s>>>(a);
+  else topk_gate_grad_kernel<DT, 32><<<g, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_topk_gate(const GateArgs& a, int dtype, cudaStream_t s) {
+  const int64_t blocks = (a.T + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const unsigned g = static_cast<unsigned>(blocks);
+  const int E = a.rule.E;
+  if (E <= 64) topk_gate_kernel<2><<<g, kThreads, 0, s>>>(a, dtype);
+  else if (E <= 128) topk_gate_kernel<4><<<g, kThreads, 0, s>>>(a, dtype);
+  else if (E <= 256) topk_gate_kernel<8><<<g, kThreads, 0, s>>>(a, dtype);
+  else topk_gate_kernel<32><<<g, kThreads, 0, s>>>(a, dtype);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_topk_gate_grad(const GateArgs& a, int dtype, cudaStream_t s) {
+  const int64_t blocks = (a.T + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const unsigned g = static_cast<unsigned>(blocks);
+  if (dtype == NVFP4_BF16) return grad<NVFP4_BF16>(a, g, s);
+  if (dtype == NVFP4_FP16) return grad<NVFP4_FP16>(a, g, s);
+  return grad<NVFP4_FP32>(a, g, s);
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,221 @@
+// The top-k gate of one token by one warp: scores, choice and weights.
+//
+//   s = softmax(l) or 1 / (1 + exp(-l));  chosen: the topk largest l, or, with a bias,
+//   s + bias, best first, the lower number first among equals;  w = s of the chosen
+//   [/ their sum] * scale
+//
+// Lane i of the warp holds the experts i, i + 32, ...: a choice is a maximum of
+// order-preserving integers over the lane's own, then over the lanes (two integer
+// reductions: the key, then the lowest number that has it).  A NaN counts as the
+// largest value.  With a bias the chosen order hangs on sums whose 32-bit rounding
+// can swap neighbours; where two neighbours of the order (the first one left out
+// among them) are nearer than that rounding, the token is chosen again on 64-bit
+// keys.  That is about one token in a thousand at 128 sigmoid scores; 64-bit
+// exponentials for all would take longer than everything else here.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace nvfp4 {
+
+constexpr int kGateMaxExperts = 1024;
+constexpr int kGateMaxTopk = 32;             // one lane each
+
+struct GateRule {
+  const float* bias;                         // [E], or NULL
+  int32_t E, topk;
+  int32_t sigmoid, renormalize;
+  float scale;
+};
+
+namespace {
+
+constexpr uint32_t kFullWarp = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float gate_logit(const void* l, int64_t at, int type) {
+  if (type == NVFP4_FP32) return __ldg(static_cast<const float*>(l) + at);
+  const unsigned short b = __ldg(static_cast<const unsigned short*>(l) + at);
+  return type == NVFP4_BF16 ? bf16_bits_to_f32(b) : __half2float(__ushort_as_half(b));
+}
+
+// Larger floats have larger keys, -0 and 0 the same, NaN the largest; 0 is no float's.
+__device__ __forceinline__ uint32_t gate_key(float f) {
+  if (f != f) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(f + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long gate_key64(double f) {
+  if (f != f) return ~0ull;
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(f + 0.0));
+  return b >> 63 ? ~b : b | (1ull << 63);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullWarp, v, o);
+  return v;
+}
+
+// Scores of a row of logits; max and total are its softmax's (a row of -infinities
+// has no total: all its scores are 0).
+struct GateScores {
+  float max, inv;
+  int sigmoid;
+  __device__ __forceinline__ float of(float l) const {
+    if (sigmoid) return 1.f / (1.f + expf(-l));
+    return max == -INFINITY && l == max ? 0.f : expf(l - max) * inv;
+  }
+};
+template <int L>
+__device__ __forceinline__ GateScores gate_scores(const float (&l)[L], int E, int sigmoid) {
+  GateScores g{-INFINITY, 1.f, sigmoid};
+  if (sigmoid) return g;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < L; ++i) g.max = fmaxf(g.max, l[i]);     // -inf past E
+  g.max = warp_max(g.max);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < L; ++i)
+    if (lane + 32 * i < E) sum += g.of(l[i]);
+  sum = warp_sum(sum);
+  g.inv = sum == 0.f ? 0.f : 1.f / sum;
+  return g;
+}
+
+// The choice on 64-bit keys (with a bias): lane j < topk gets the j-th expert.
+template <int L>
+__device__ __noinline__ int gate_choose64(const GateRule& r, const float (&l)[L], float max) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long key[L];
+  double inv = 1.0;
+  if (!r.sigmoid) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (lane + 32 * i < r.E && max != -INFINITY)
+        sum += exp(static_cast<double>(l[i]) - static_cast<double>(max));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
+    inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+  }
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 0;
+    if (e < r.E) {
+      const double x = static_cast<double>(l[i]);
+      double s;
+      if (r.sigmoid) s = 1.0 / (1.0 + exp(-x));
+      else s = max == -INFINITY && l[i] == max ? 0.0 : exp(x - static_cast<double>(max)) * inv;
+      key[i] = gate_key64(s + static_cast<double>(__ldg(r.bias + e)));
+    }
+  }
+  int mine = 0;
+  for (int j = 0; j < r.topk; ++j) {
+    unsigned long long best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (key[i] > best) { best = key[i]; at = i; }
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+    const uint32_t top = __reduce_max_sync(kFullWarp, hi);
+    const uint32_t low = __reduce_max_sync(kFullWarp, hi == top ? lo : 0u);
+    const int e = static_cast<int>(__reduce_min_sync(
+        kFullWarp, hi == top && lo == low ? static_cast<uint32_t>(lane + 32 * at) : ~0u));
+    if (j == lane) mine = e;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (lane + 32 * i == e) key[i] = 0;
+  }
+  return mine;
+}
+
+// l[i]: logit of expert lane + 32 i, -infinity past E.  Lane j < topk gets the j-th
+// expert and its weight.
+template <int L>
+__device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[L], int* id,
+                                            float* weight) {
+  const int lane = threadIdx.x & 31;
+  // renormalised softmax weights need no total, nor does the choice without a bias
+  const bool total = r.sigmoid || r.bias || !r.renormalize;
+  GateScores g{0.f, 1.f, r.sigmoid};
+  if (total) {
+    g = gate_scores<L>(l, r.E, r.sigmoid);
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < L; ++i) m = fmaxf(m, l[i]);
+    g.max = warp_max(m);
+  }
+  float s[L];
+  uint32_t key[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    s[i] = r.bias && e < r.E ? g.of(l[i]) : l[i];
+    key[i] = e < r.E ? gate_key(r.bias ? s[i] + __ldg(r.bias + e) : s[i]) : 0u;
+  }
+  // one more than wanted where neighbours are compared
+  const int picks = r.bias && r.topk < r.E ? r.topk + 1 : r.topk;
+  int mine = 0;
+  float chosen = 0.f, last_s = 0.f, last = 0.f;                   // last: the pick before
+  bool near = false;
+  for (int j = 0; j < picks; ++j) {
+    uint32_t best = 0;
+    int at = 0;
+    float val = 0.f;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (key[i] > best) { best = key[i]; at = i; val = s[i]; }
+    const uint32_t top = __reduce_max_sync(kFullWarp, best);
+    const int e = static_cast<int>(
+        __reduce_min_sync(kFullWarp, best == top ? static_cast<uint32_t>(lane + 32 * at) : ~0u));
+    const float v = __shfl_sync(kFullWarp, val, e & 31);
+    if (r.bias) {
+      const float k = top == 0xFFFFFFFFu ? NAN
+                      : __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+      // a score's relative error is below 1e-6, the sum's half a step of the key
+      if (j > 0)
+        near |= !(last - k > 2e-6f * (fabsf(last_s) + fabsf(v)) + 2.4e-7f * (fabsf(last) + fabsf(k)));
+      last_s = v;
+      last = k;
+    }
+    if (j == lane && j < r.topk) { mine = e; chosen = v; }
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (lane + 32 * i == e) key[i] = 0;
+  }
+  if (near) {                                       // the same in every lane
+    mine = gate_choose64<L>(r, l, g.max);
+    // the score again, from the expert's lane
+    for (int j = 0; j < r.topk; ++j) {
+      const int e = __shfl_sync(kFullWarp, mine, j);
+      float val = 0.f;
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (lane + 32 * i == e) val = s[i];
+      val = __shfl_sync(kFullWarp, val, e & 31);
+      if (j == lane) chosen = val;
+    }
+  }
+  const bool on = lane < r.topk;
+  float w = !on ? 0.f : r.bias ? chosen : g.of(chosen);
+  if (r.renormalize) {
+    const float sum = warp_sum(w);
+    w = sum == 0.f ? 0.f : w / sum;
+  }
+  *id = mine;
+  *weight = w * r.scale;
+}
+
+}  // namespace
+}  // namespace nvfp4

@@ -96,6 +96,20 @@ def linear(x, w, w_scale, stream=None):
     return y.view(*x.shape[:-1], y.shape[1])
 
 
+def linear_codes(codes, scales, w, w_scale, dtype=torch.bfloat16, stream=None):
+    """y = x . w^T for rows that are quantised already (quantize_rows,
+    norm.rms_norm_fp8): codes float8_e4m3fn [M, K], scales FP32 [ceil(K / 128), M], w
+    codes [N, K] -> [M, N] of `dtype` (BF16, FP16 or FP32)."""
+    if forward_ad._current_level >= 0:
+        refuse_tangents(scales, w_scale)
+    if dtype not in F._DTYPES:
+        raise ValueError(f"dtype: expected BF16, FP16 or FP32, got {dtype}")
+    if stream is not None:
+        with on_stream(stream, codes.device):
+            return native().linear_codes(codes, scales, w, w_scale, F._DTYPES[dtype])
+    return native().linear_codes(codes, scales, w, w_scale, F._DTYPES[dtype])
+
+
 def expert_linear(x, w, w_scale, expert_offsets, route_pos=None, R=None, silu_mul: bool = False,
                   stream=None):
     """Each route's row times its expert's weights: w codes [E, N, K] -> [R, N]

@@ -16,8 +16,9 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 
-from . import fp8, tokens
+from . import fp8, gating, tokens
 from . import nvfp4 as F
 
 
@@ -354,3 +355,67 @@ class Fp8MLP:
         gate_up = fp8.expert_linear(x, *self.gate_up, offsets, pos)
         y = fp8.expert_linear(gate_up, *self.down, offsets, silu_mul=True)
         return tokens.combine(y, pos, topk_weights, offsets)
+
+    def step_few(self, x, topk_ids, topk_weights, stream=None):
+        """step() of a few tokens in one launch: at most 16, whose activations fit
+        shared memory (ValueError for more).  gate_up's product and the experts' rows
+        stay FP32 here, where step() rounds them to x's type.  An expert that a token
+        names twice counts with both weights."""
+        if forward_ad._current_level >= 0:
+            tokens.refuse_tangents(x, topk_weights, *self.gate_up, *self.down)
+        if stream is not None:
+            with tokens.on_stream(stream, x.device):
+                return self.step_few(x, topk_ids, topk_weights)
+        done = F.native().moe_layer(x, None, *self.gate_up, *self.down, 0, None, False, False, 1.0,
+                                    topk_ids, topk_weights)
+        if done is not None:
+            return done[0]
+        if x.shape[0] == 0:
+            return x.new_empty((0, self.down[0].shape[1]))
+        raise ValueError("more tokens or wider rows than one launch takes: use step()")
+
+
+class Fp8MoE:
+    """An MoE layer over FP8 experts: the router's product, the top-k gate and the
+    experts (weights as in Fp8MLP).  router [E, K] has the tokens' type or is FP32;
+    bias, score, renormalize and scale are the gate's (gating.topk_gate).
+
+    step() of a few tokens (up to 16 whose activations fit shared memory,
+    nvfp4.nvfp4_fp8_moe_layer_workspace_bytes) runs in one launch.  More go through
+    the router's product with FP32 logits, gating.topk_gate and Fp8MLP.step, whose
+    gate_up product and expert rows are rounded to the tokens' type; the router's
+    sums also have another order, which can change the choice between nearly equal
+    logits.  Both enqueue kernels only and keep no buffers; the experts are frozen
+    and neither takes part in autograd."""
+
+    def __init__(self, router, gate_up, down, topk: int, bias=None, score: str = "softmax",
+                 renormalize: bool = True, scale: float = 1.0):
+        self.mlp = Fp8MLP(gate_up, down)
+        self.router, self.topk, self.bias = router, topk, bias
+        self.sigmoid = gating.is_sigmoid(score)
+        self.score, self.renormalize, self.scale = score, renormalize, scale
+
+    def step(self, x, stream=None):
+        """x [T, K] BF16 or FP16 -> [T, N] in x's type."""
+        return self.step_routed(x, stream)[0]
+
+    def step_routed(self, x, stream=None):
+        """The same with the choice: (out [T, N], ids int32 [T, topk], weights FP32)."""
+        if forward_ad._current_level >= 0:
+            tokens.refuse_tangents(x, self.router, *self.mlp.gate_up, *self.mlp.down)
+        if stream is not None:
+            with tokens.on_stream(stream, x.device):
+                return self.step_routed(x)
+        done = F.native().moe_layer(x, self.router, *self.mlp.gate_up, *self.mlp.down, self.topk,
+                                    self.bias, self.sigmoid, self.renormalize, self.scale, None,
+                                    None)
+        if done is not None:
+            return done
+        router = self.router
+        if router.dtype == x.dtype:
+            logits = torch.mm(x, router.t(), out_dtype=torch.float32)
+        else:
+            logits = torch.mm(x.float(), router.t())
+        ids, weights = gating.topk_gate(logits, self.topk, self.bias, self.score,
+                                        self.renormalize, self.scale)
+        return self.mlp.step(x, ids, weights), ids, weights

@@ -35,12 +35,15 @@ NVFP4_BF16 = 0
 NVFP4_FP16 = 1
 NVFP4_FP32 = 2
 NVFP4_FP8_SILU_MUL = 1
+NVFP4_GATE_SIGMOID = 1
+NVFP4_GATE_RENORMALIZE = 2
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _U32 = ctypes.c_uint32
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 
 _SIGS = {
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -101,6 +104,21 @@ _SIGS = {
                                         _SZ, _P]),
     "nvfp4_fp8_expert_linear": (ctypes.c_int, [_P, _I64, _I64, _I32, _U32, _P, _I32, _P, _P, _P,
                                                _I32, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P]),
+    "nvfp4_rms_norm": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _P,
+                                      _P]),
+    "nvfp4_rms_norm_fp8": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P,
+                                          _P, _P, _P]),
+    "nvfp4_rms_norm_grad_workspace_bytes": (_SZ, [_I64, _I64]),
+    "nvfp4_rms_norm_grad": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32,
+                                           _F32, _P, _P, _P, _SZ, _P]),
+    "nvfp4_topk_gate": (ctypes.c_int, [_P, _I64, _I64, _I32, _I32, _I32, _P, _U32, _F32, _P, _P,
+                                       _P]),
+    "nvfp4_topk_gate_grad": (ctypes.c_int, [_P, _P, _I64, _I64, _I32, _I32, _I32, _P, _U32, _F32,
+                                            _P, _P]),
+    "nvfp4_fp8_moe_layer_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I64, _I64, _I64]),
+    "nvfp4_fp8_moe_layer": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _I32, _P, _U32, _F32, _P, _P,
+                                           _P, _P, _I32, _I32, _I64, _I64, _I64, _P, _P, _P, _I64,
+                                           _P, _SZ, _P]),
     "nvfp4_grouped_gemm_combine_noalloc": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I32,
                                                           _I64, _I64, _P, _P, _P, _P, _P]),
 }
@@ -489,6 +507,75 @@ def nvfp4_fp8_expert_linear(x, W, sW, expert_offsets, y, workspace, flags: int =
         _ptr(x), x.shape[0], _row_stride(x), _dtype(x), flags, _ptr(route_pos), fanout, _ptr(W),
         _ptr(sW), _ptr(expert_offsets), E, y.shape[0], N, K, _ptr(y), _row_stride(y),
         _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def nvfp4_rms_norm(x, residual, weight, eps: float, h, y, stream=None) -> None:
+    """h = x + residual (None: h is not written), y = h / sqrt(mean(h^2) + eps) * weight."""
+    T, D = x.shape
+    _check("nvfp4_rms_norm", load().nvfp4_rms_norm(
+        _ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
+        T, D, _dtype(x), _ptr(weight), _dtype(weight), float(eps), _ptr(h), _ptr(y),
+        _stream(stream)))
+
+
+def nvfp4_rms_norm_fp8(x, residual, weight, eps: float, h, codes, scales, stream=None) -> None:
+    """The norm's rows as E4M3 codes [T, D] and scales [ceil(D / 128), T]."""
+    T, D = x.shape
+    _check("nvfp4_rms_norm_fp8", load().nvfp4_rms_norm_fp8(
+        _ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
+        T, D, _dtype(x), _ptr(weight), _dtype(weight), float(eps), _ptr(h), _ptr(codes),
+        _ptr(scales), _stream(stream)))
+
+
+def nvfp4_rms_norm_grad_workspace_bytes(T: int, D: int) -> int:
+    return load().nvfp4_rms_norm_grad_workspace_bytes(T, D)
+
+
+def nvfp4_rms_norm_grad(dy, h, dh, weight, eps: float, dx, dweight, workspace, stream=None) -> None:
+    """dx [T, D] and dweight [D] of the norm; dh: gradient of h itself, or None."""
+    T, D = h.shape
+    _check("nvfp4_rms_norm_grad", load().nvfp4_rms_norm_grad(
+        _ptr(dy), _row_stride(dy), _ptr(h), _row_stride(h), _ptr(dh),
+        0 if dh is None else _row_stride(dh), T, D, _dtype(h), _ptr(weight), _dtype(weight),
+        float(eps), _ptr(dx), _ptr(dweight), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+
+
+def nvfp4_topk_gate(logits, bias, topk_ids, topk_weights, flags: int = 0, scale: float = 1.0,
+                    stream=None) -> None:
+    """Logits [T, E] -> the chosen experts int32 [T, topk] and their weights FP32 [T, topk]."""
+    T, E = logits.shape
+    _check("nvfp4_topk_gate", load().nvfp4_topk_gate(
+        _ptr(logits), _row_stride(logits), T, E, _dtype(logits), topk_ids.shape[1], _ptr(bias),
+        flags, float(scale), _ptr(topk_ids), _ptr(topk_weights), _stream(stream)))
+
+
+def nvfp4_topk_gate_grad(dweights, logits, topk_ids, dlogits, flags: int = 0, scale: float = 1.0,
+                         stream=None) -> None:
+    """Gradient of the gate's weights -> dlogits [T, E] of the logits' type."""
+    T, E = logits.shape
+    _check("nvfp4_topk_gate_grad", load().nvfp4_topk_gate_grad(
+        _ptr(dweights), _ptr(logits), _row_stride(logits), T, E, _dtype(logits),
+        topk_ids.shape[1], _ptr(topk_ids), flags, float(scale), _ptr(dlogits), _stream(stream)))
+
+
+def nvfp4_fp8_moe_layer_workspace_bytes(T: int, topk: int, E: int, K: int, I: int, N: int) -> int:
+    """0: sizes that nvfp4_fp8_moe_layer refuses."""
+    return load().nvfp4_fp8_moe_layer_workspace_bytes(T, topk, E, K, I, N)
+
+
+def nvfp4_fp8_moe_layer(x, router, bias, W1, s1, W2, s2, topk_ids, topk_weights, out, workspace,
+                        flags: int = 0, scale: float = 1.0, stream=None) -> None:
+    """A whole MoE layer for a few tokens; router None: topk_ids and topk_weights are
+    inputs, else outputs."""
+    T, K = x.shape
+    E, N, I = W2.shape
+    _check("nvfp4_fp8_moe_layer", load().nvfp4_fp8_moe_layer(
+        _ptr(x), _row_stride(x), T, _dtype(x), _ptr(router),
+        _dtype(x if router is None else router), _ptr(bias), flags, float(scale), _ptr(W1),
+        _ptr(s1), _ptr(W2), _ptr(s2), E, topk_ids.shape[1], K, I, N, _ptr(topk_ids),
+        _ptr(topk_weights), _ptr(out), _row_stride(out), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
 
 
 # ------------------------------------------- allocating conveniences (torch)
