@@ -410,22 +410,6 @@ nvfp4::GateRule gate_rule(int32_t E, int32_t topk, const float* bias, uint32_t f
   return r;
 }
 
-// The MoE layer's workspace: logits, h, route rows of the output, arrival counters.
-struct MoeWorkspace {
-  size_t h, part, arrived, bytes;
-};
-MoeWorkspace moe_workspace(int64_t T, int32_t topk, int32_t E, int64_t I, int64_t N) {
-  auto up = [](int64_t n) { return static_cast<size_t>((n + 15) / 16 * 16); };
-  MoeWorkspace w{};
-  const int64_t R = T * topk;
-  w.h = up(T * E * 4);
-  w.part = w.h + up(R * I * 4);
-  w.arrived = w.part + up(R * N * 4);
-  w.bytes = w.arrived + up((N + 15) / 16 * 4);
-  return w;
-}
-constexpr int kMoeFewestSms = 128;   // sizes that fit with these fit on every sm_103 part
-
 nvfp4_status fp8_gemm_checked(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW,
                               const int32_t* offsets, int32_t E, int64_t rows, int64_t N,
                               int64_t K, void* out, int64_t ldc, int32_t dtype, void* stream) {
@@ -1620,12 +1604,8 @@ nvfp4_status nvfp4_topk_gate_grad(const float* dweights, const void* logits, int
 
 size_t nvfp4_fp8_moe_layer_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I,
                                            int64_t N) {
-  nvfp4::Fp8MoePlan p{};
-  if (T <= 0 || T > nvfp4::kMoeMaxTokens || topk <= 0 || E <= 0 || topk > E || K <= 0 || I <= 0 ||
-      N <= 0 || K % 16 != 0 || I % 16 != 0 ||
-      !nvfp4::fp8_moe_plan(static_cast<int>(T), topk, E, K, I, N, kMoeFewestSms, &p))
-    return 0;
-  return moe_workspace(T, topk, E, I, N).bytes;
+  nvfp4::MoeLayout m{};
+  return nvfp4::fp8_moe_layout(T, topk, E, K, I, N, &m) ? m.bytes : 0;
 }
 
 nvfp4_status nvfp4_fp8_moe_layer(const void* x, int64_t ld, int64_t T, int32_t dtype,
@@ -1647,22 +1627,18 @@ nvfp4_status nvfp4_fp8_moe_layer(const void* x, int64_t ld, int64_t T, int32_t d
       !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4) || !aligned_to(out, 2) ||
       !aligned16(workspace) || (T > 1 && ld % 8 != 0))
     return NVFP4_ERR_UNSUPPORTED;
-  if (T > 0) {
-    const size_t want = nvfp4_fp8_moe_layer_workspace_bytes(T, topk, E, K, I, N);
-    if (want == 0 || workspace_bytes < want) return NVFP4_ERR_UNSUPPORTED;
-  }
+  nvfp4::MoeLayout m{};
+  if (T > 0 && (!nvfp4::fp8_moe_layout(T, topk, E, K, I, N, &m) || workspace_bytes < m.bytes))
+    return NVFP4_ERR_UNSUPPORTED;
   DeviceState* d = nullptr;
   const nvfp4_status st = device_state(&d);
   if (st != NVFP4_OK) return st;
   if (T == 0) return NVFP4_OK;
-  nvfp4::Fp8MoePlan p{};
-  if (!nvfp4::fp8_moe_plan(static_cast<int>(T), topk, E, K, I, N, d->sms, &p))
-    return NVFP4_ERR_UNSUPPORTED;
-  const MoeWorkspace w = moe_workspace(T, topk, E, I, N);
-  char* ws = static_cast<char*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   nvfp4::Fp8MoeArgs a{};
   a.x = x;
   a.ld = ld;
+  a.type = dtype;
   a.router = router;
   a.router_type = router_dtype;
   a.rule = gate_rule(E, topk, bias, flags, scale);
@@ -1670,20 +1646,34 @@ nvfp4_status nvfp4_fp8_moe_layer(const void* x, int64_t ld, int64_t T, int32_t d
   a.K = static_cast<int32_t>(K);
   a.I = static_cast<int32_t>(I);
   a.N = static_cast<int32_t>(N);
-  a.w1 = W1;
   a.s1 = s1;
-  a.w2 = W2;
   a.s2 = s2;
   a.ids = topk_ids;
   a.weights = topk_weights;
   a.out = out;
   a.ldo = ldo;
   a.logits = reinterpret_cast<float*>(ws);
-  a.h = reinterpret_cast<float*>(ws + w.h);
-  a.part = reinterpret_cast<float*>(ws + w.part);
-  a.arrived = reinterpret_cast<uint32_t*>(ws + w.arrived);
+  a.xq = ws + m.xq;
+  a.ld_xq = m.ld_xq;
+  a.xs = reinterpret_cast<float*>(ws + m.xs);
+  a.hq = ws + m.hq;
+  a.ld_hq = m.ld_hq;
+  a.hs = reinterpret_cast<float*>(ws + m.hs);
+  a.part = reinterpret_cast<float*>(ws + m.part);
+  a.arrived = reinterpret_cast<uint32_t*>(ws + m.arrived);
+  a.items1 = static_cast<int32_t>(m.experts * ((I + 127) / 128));
   a.status = d->status;
-  return launched(nvfp4::launch_fp8_moe(a, p, dtype, static_cast<cudaStream_t>(stream)));
+  a.timeout_ns = g_timeout_ns.load();
+  CUtensorMap t1, t2, tx, th;
+  const uint32_t box = static_cast<uint32_t>(nvfp4::fp8_moe_box_rows(m.columns));
+  if (make_fp8_map(&t1, W1, K, K, I, 2 * static_cast<uint64_t>(E), 128, 3) != NVFP4_OK ||
+      make_fp8_map(&t2, W2, I, I, N, E, 128, 3) != NVFP4_OK ||
+      make_fp8_map(&tx, a.xq, K, m.ld_xq, m.columns, 1, box, 2) != NVFP4_OK ||
+      make_fp8_map(&th, a.hq, I, m.ld_hq, static_cast<uint64_t>(m.experts) * m.columns, 1, box,
+                   2) != NVFP4_OK)
+    return NVFP4_ERR_UNSUPPORTED;
+  return launched(nvfp4::launch_fp8_moe(t1, t2, tx, th, a, m.columns, d->sms,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,4 +1,4 @@
-// A whole MoE layer for a few tokens (up to 16) over FP8 experts, in one launch:
+// A whole MoE layer for a few tokens (up to 32) over FP8 experts, in one launch:
 //
 //   l = x . router^T;  experts e_tk and weights w_tk by the top-k gate (gate.cuh)
 //   h_tk = SiLU(xq . gate_e^T) * (xq . up_e^T),   out_t = sum_k w_tk hq_tk . down_e^T
@@ -8,29 +8,32 @@
 //
 // Bound: the chosen experts' bytes (HBM).  The design serves that stream:
 //
-// * One block per SM (a cooperative launch: the blocks meet at two grid barriers, after
-//   the router and after h), eight warps, each with a shared-memory ring of its own that
-//   it fills by 16-byte asynchronous copies several stages ahead: no barrier inside the
-//   stream, and about 100 KB on the way per SM.  At the end of gate_up a warp starts its
-//   down copies before it waits for the other blocks, so HBM does not idle there.
-// * Work is items of 16 weight rows (8 gate rows and the 8 up rows of the same columns,
-//   so that a thread holds both factors of its h; or 16 down rows), expert by expert.  A
-//   block takes a contiguous run of items and cuts its K blocks (128 codes of each of the
-//   16 rows, 2 KB) into eight equal runs, one a warp.  An item that lies across warps is
-//   joined through shared memory in warp order.
-// * The tokens are the MMA's 8 columns: m16n8k32 with E4M3 operands, FP32 accumulators
-//   cleared every K block and added with both scales.  The matrix pipe idles nearly
-//   always (a warp's 2 KB take four instructions), so that the tensor memory path's
-//   128-row tiles and set-up would buy nothing here: what counts is that a token's
-//   experts divide into two thousand small items instead of hundreds of large ones.
-//   Within a K block the order of k is free as long as weights and activations share it:
-//   a lane takes 16 consecutive bytes of a row for two MMAs, one 16-byte read each.
-// * The down products go out as FP32 rows per route; the last block to finish 16 columns
-//   (an arrival counter) adds the routes of each token in order with their weights.
+// * One block per SM (a cooperative launch).  The blocks meet at two grid barriers: when
+//   the logits and the codes of x are written, and when the codes of h are.
+// * Weights are the MMA's 128 rows (tcgen05, M 128), the tokens its 16 or 32 columns: all
+//   tokens, so that nothing is gathered; an expert's columns of other tokens are dropped.
+//   A tile is 256 weight rows x 128 K (32 KB, two TMA boxes): the gate and up rows of 128
+//   columns of h, so that one thread holds both factors of its h, or 256 down rows.
+//   Rows past a matrix read as zeros.
+// * The tiles of a phase stand in one line (gate_up: expert, 128 columns, K block; down:
+//   256 columns, expert, K block) that is cut into equal runs, one a block, wherever that
+//   falls: a token's eight experts have some thousands of tiles, and every SM streams the
+//   same bytes.  An item (128 columns of one expert's h; 256 output columns over all
+//   experts) whose tiles lie in several blocks is joined by the last of them to finish,
+//   which adds the parts in block order.
+// * Six stages are on their way (192 KB an SM).  When a block has asked for all its gate_up
+//   tiles, its producer goes on with the weights of its first down tiles, before the grid
+//   barrier that the codes of h wait for: HBM does not idle there.
+// * Both scales differ by K block, so every K block has accumulators of its own in tensor
+//   memory, which four warps read and add as FP32 times the factor (weight scale * token
+//   scale, for down also * routing weight) that a warp of its own lays out.
+//
+// (A first form with mma.sync, eight warps with rings of their own: it spent 280
+// instructions on 2 KB of weights, converting codes, and reached 4.3 TB/s: one token
+// through 128 experts of 6144 x 2048, eight of them chosen, in 96 us.)
 #include <cooperative_groups.h>
-#include <cuda_fp16.h>
 
-#include "fp8.h"
+#include "fp8_common.cuh"
 #include "fp8_moe.h"
 #include "fp8_quant.cuh"
 
@@ -42,372 +45,499 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kItemRows = 16;
-constexpr int kStageBytes = kItemRows * 128;
-constexpr size_t kMoeSmemMost = (227 - 13) * 1024;     // beside the static arrays
+constexpr int kGroupBytes = 128 * 128;      // 128 weight rows of a K block
+constexpr int kAccBufs = 8;                 // of 2 x 16 or 2 x 32 columns
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
-  const int n = in ? 16 : 0;                            // the rest of the 16 bytes: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
-// c += A (16 x 32, rows) . B (32 x 8): a0, a2 row g, a1, a3 row g + 8.
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// TB: token columns (8, 16 or 32).
+template <int TB>
+struct Shape {
+  static constexpr int kCols = TB < 16 ? 16 : TB;           // of the MMA
+  static constexpr int kStages = TB == 32 ? 5 : 6;
+  static constexpr int kTokOffset = 2 * kGroupBytes;
+  static constexpr int kStageBytes = kTokOffset + kCols * 128;
+  static constexpr int kFacOffset = kStages * kStageBytes;  // [bufs][3][TB] floats
+  static constexpr int kRedOffset = kFacOffset + kAccBufs * 3 * TB * 4;   // [4][TB] maxima
+  static constexpr int kBarOffset = kRedOffset + 4 * TB * 4;
+  static constexpr int kCtlOffset = kBarOffset + 8 * (2 * kStages + 2 * kAccBufs + 2);
+  static constexpr int kSmemBytes = kCtlOffset + 32 + 1024;
+  static constexpr uint32_t kTmemCols = kAccBufs * 2 * kCols;             // 256 or 512
+};
 
 // The distinct experts in order of first appearance, and each one's routes.
 struct Routes {
+  float weight[kMoeMaxRoutes];              // of each route
+  uint32_t tokens[kMoeMaxRoutes];           // of each live expert, one bit each
   int16_t expert[kMoeMaxRoutes];            // of each route, -1: none
-  float weight[kMoeMaxRoutes];
   int16_t live[kMoeMaxRoutes];              // experts' numbers
-  int16_t start[kMoeMaxRoutes + 1];         // first of each live expert's entries in `route`
+  int16_t start[kMoeMaxRoutes];             // first of each live expert's entries in `route`
   int16_t route[kMoeMaxRoutes];
-  int16_t at[kMoeMaxRoutes];                // start of a leading route's expert
   int n_live;
 };
 
-// One phase's matrix and the block's part of its items.
-struct Phase {
-  const uint8_t* w;
-  const float* s;
-  int K, nkb, nnb;                          // bytes of a row; blocks of K and of rows
-  int units;                                // items of an expert
-  int rows;                                 // rows of an expert's matrix
-  int half;                                 // gate_up: I; down: 0
-  int first, count;                         // the block's items
-};
-
-__device__ __forceinline__ int share(int64_t n, int part, int parts) {
-  return static_cast<int>(n * part / parts);
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
-// Where a warp stands in its run of K blocks.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// Uses of r stay behind the wait for its load (volatile statements keep their order).
+__device__ __forceinline__ void keep_after(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                    "+r"(r[6]), "+r"(r[7]));
+}
+
+// One phase's line of tiles and the block's run of it.
+struct Phase {
+  int down;
+  int nkb;                                  // K blocks of an item's expert
+  int units;                                // gate_up: ceil(I / 128); down: ceil(N / 256)
+  int experts;
+  int per_item;                             // tiles of an item
+  int grain, grains;                        // runs begin at multiples of `grain` tiles
+  int parts;                                // blocks that have tiles
+  int first, count;                         // the block's run
+
+  __device__ __forceinline__ int begin(int block) const {
+    return grain * static_cast<int>(static_cast<int64_t>(grains) * block / parts);
+  }
+  // The block whose run holds a tile.
+  __device__ __forceinline__ int owner(int tile) const {
+    return static_cast<int>(((static_cast<int64_t>(tile / grain) + 1) * parts - 1) / grains);
+  }
+  // Runs of whole items need no join, which takes about 4 us behind the last tile; runs of
+  // single tiles are all equally long.  A tile takes 0.76 us while all SMs draw on HBM and
+  // at least 0.53 us (62 GB/s is all that one SM draws); a join 5 tiles' time.  At most about
+  // eight blocks share an item: the last one reads all parts.
+  __device__ __forceinline__ void set(int is_down, int k_blocks, int n_units, int n_experts) {
+    const int blocks = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+    down = is_down;
+    nkb = k_blocks;
+    units = n_units;
+    experts = n_experts;
+    per_item = max(down ? nkb * experts : nkb, 1);
+    const int items = down ? units * min(experts, 1) : units * experts;
+    const int rest = items % blocks;
+    const int64_t rounds = 100 * (items / blocks) + (rest ? max(70, 100 * rest / blocks) : 0);
+    const bool whole = rounds * per_item <= 100 * static_cast<int64_t>(items) * per_item / blocks + 500;
+    grain = whole ? per_item : 1;
+    grains = whole ? items : items * per_item;
+    parts = min(blocks, min(grains, 8 * items));
+    first = b < parts ? begin(b) : 0;
+    count = b < parts ? begin(b + 1) - first : 0;
+  }
+};
+
+// A tile of the line: live expert, unit, K block.
 struct Cursor {
-  int left;                                 // K blocks to go
   int x, unit, kb;
-  __device__ __forceinline__ void start(const Phase& p, int warp) {
-    const int64_t n = static_cast<int64_t>(p.count) * p.nkb;
-    const int a = share(n, warp, kWarps), b = share(n, warp + 1, kWarps);
-    left = b - a;
-    const int item = p.first + a / p.nkb;
-    kb = a % p.nkb;
-    x = item / p.units;
-    unit = item - x * p.units;
+  __device__ __forceinline__ void at(const Phase& p, int tile) {
+    kb = tile % p.nkb;
+    const int rest = tile / p.nkb;
+    if (p.down) {
+      x = rest % max(p.experts, 1);
+      unit = rest / max(p.experts, 1);
+    } else {
+      unit = rest % p.units;
+      x = rest / p.units;
+    }
   }
   __device__ __forceinline__ void next(const Phase& p) {
-    --left;
-    if (++kb == p.nkb) {
-      kb = 0;
+    if (++kb < p.nkb) return;
+    kb = 0;
+    if (p.down) {
+      if (++x == p.experts) { x = 0; ++unit; }
+    } else {
       if (++unit == p.units) { unit = 0; ++x; }
     }
   }
 };
 
-// Copies of one K block of 16 rows into a stage: instruction i takes rows 4 i to 4 i + 3,
-// eight lanes a row.  In shared memory the 16-byte chunks of odd rows lie 64 bytes on
-// (modulo 128), so that two rows' reads of four chunks fall into different banks.
-__device__ __forceinline__ void fetch(const Phase& p, const Routes& rt, const Cursor& c,
-                                      uint32_t stage, uint32_t scales) {
+// Shared memory of a block.
+template <int TB>
+struct Block {
+  using S = Shape<TB>;
+  uint32_t base;
+  uint8_t* smem;
+  CtaCtl* ctl;
+  int* status;
+  uint32_t tmem;
+  __device__ __forceinline__ uint32_t stage(int s) const { return base + s * S::kStageBytes; }
+  __device__ __forceinline__ uint32_t bar(int i) const { return base + S::kBarOffset + 8u * i; }
+  __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bar(S::kStages + s); }
+  __device__ __forceinline__ uint32_t accf(int b) const { return bar(2 * S::kStages + b); }
+  __device__ __forceinline__ uint32_t acce(int b) const {
+    return bar(2 * S::kStages + kAccBufs + b);
+  }
+  __device__ __forceinline__ uint32_t drain() const { return bar(2 * S::kStages + 2 * kAccBufs); }
+  __device__ __forceinline__ uint32_t meet() const {
+    return bar(2 * S::kStages + 2 * kAccBufs + 1);
+  }
+  __device__ __forceinline__ float* fac(int b) const {
+    return reinterpret_cast<float*>(smem + S::kFacOffset) + b * 3 * TB;
+  }
+  __device__ __forceinline__ float* red() const {
+    return reinterpret_cast<float*>(smem + S::kRedOffset);
+  }
+};
+
+// Counts a role's passes over a ring of n slots.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) { slot = 0; phase ^= 1u; }
+  }
+};
+
+// ------------------------------------------------------------------ producer
+
+template <int TB>
+struct Producer {
+  const Block<TB>& b;
+  const Routes& rt;
+  const CUtensorMap* w;
+  const CUtensorMap* tok;
+  uint64_t wpol, tpol;
+
+  __device__ __forceinline__ void weights(const Phase& p, const Cursor& c, int s) const {
+    using S = Shape<TB>;
+    const int e = rt.live[c.x];
+    mbar_arrive_expect_tx(b.full(s), S::kStageBytes);
+    if (p.down) {
+      tma_load_3d(b.stage(s), w, b.full(s), c.kb * 128, c.unit * 256, e, wpol);
+      tma_load_3d(b.stage(s) + kGroupBytes, w, b.full(s), c.kb * 128, c.unit * 256 + 128, e, wpol);
+    } else {
+      tma_load_3d(b.stage(s), w, b.full(s), c.kb * 128, c.unit * 128, 2 * e, wpol);
+      tma_load_3d(b.stage(s) + kGroupBytes, w, b.full(s), c.kb * 128, c.unit * 128, 2 * e + 1,
+                  wpol);
+    }
+  }
+  __device__ __forceinline__ void tokens(const Phase& p, const Cursor& c, int s) const {
+    tma_load_2d(b.stage(s) + Shape<TB>::kTokOffset, tok, b.full(s), c.kb * 128,
+                p.down ? c.x * TB : 0, tpol);
+  }
+};
+
+// ------------------------------------------------------------------- factors
+
+// One warp: for each tile the products of the weight scales (gate or first 128 rows; up
+// or second 128 rows, whose scale can change within the 128 rows where I is no multiple
+// of 128) and of each token's scale (times its routing weight in the down phase).
+template <int TB>
+__device__ __forceinline__ void factors(const Block<TB>& b, const Fp8MoeArgs& a, const Routes& rt,
+                                        const Phase& p, Ring& acc) {
   const int lane = threadIdx.x & 31;
-  const int e = rt.live[c.x];
-  const int chunk = lane & 7;
-  const int k = c.kb * 128 + chunk * 16;
-  const bool in = k < p.K;
-  const int r0 = lane >> 3;
-  // rows of the unit: 8 of each half (gate, up), or 16 of the matrix
-  const int base = p.half ? c.unit * 8 : c.unit * 16;
-  const int64_t first = static_cast<int64_t>(e) * p.rows;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * i + r0;
-    int row = base + r;
-    if (p.half) row = i < 2 ? row : p.half + row - 8;
-    else row = min(row, p.rows - 1);
-    const uint8_t* src = p.w + (first + row) * p.K + (in ? k : 0);
-    cp16(stage + r * 128 + ((chunk ^ ((r & 1) << 2)) << 4), src, in);
-  }
-  if (lane < 2) {
-    const int row = lane && p.half ? p.half + base : base;
-    cp4(scales + lane * 4,
-        p.s + (static_cast<int64_t>(e) * p.nnb + row / kFp8Block) * p.nkb + c.kb);
+  Cursor c;
+  c.at(p, p.first);
+  const float* ws = p.down ? a.s2 : a.s1;
+  const int nnb = p.down ? (a.N + 127) / 128 : (2 * a.I + 127) / 128;
+  int x = -1;
+  float weight = 1.f;
+  struct Raw {
+    float tok, w0, w1, w2;
+  };
+  auto load = [&](const Cursor& at) {
+    Raw r;
+    const int e = rt.live[at.x];
+    const int r0 = p.down ? 2 * at.unit : at.unit;
+    const int up = a.I + at.unit * 128;
+    const int r1 = p.down ? min(r0 + 1, nnb - 1) : up / 128;
+    const int r2 = p.down ? r1 : min(r1 + 1, nnb - 1);
+    const float* row = ws + static_cast<int64_t>(e) * nnb * p.nkb + at.kb;
+    r.w0 = __ldg(row + static_cast<int64_t>(r0) * p.nkb);
+    r.w1 = __ldg(row + static_cast<int64_t>(r1) * p.nkb);
+    r.w2 = __ldg(row + static_cast<int64_t>(r2) * p.nkb);
+    const float* ts = p.down ? a.hs + (static_cast<int64_t>(at.x) * p.nkb + at.kb) * TB
+                             : a.xs + at.kb * TB;
+    r.tok = lane < TB && lane < a.T ? __ldcg(ts + lane) : 0.f;
+    return r;
+  };
+  Raw next{};
+  if (p.count > 0) next = load(c);
+  for (int i = 0; i < p.count; ++i) {
+    const Raw r = next;
+    if (p.down && c.x != x) {
+      x = c.x;
+      const uint32_t tokens = rt.tokens[x];
+      const int j = rt.start[x] + __popc(tokens & ((1u << lane) - 1u));
+      weight = tokens >> lane & 1u ? rt.weight[rt.route[j]] : 0.f;
+    }
+    c.next(p);
+    if (i + 1 < p.count) next = load(c);
+    if (!__all_sync(kFullWarp, wait_soon(b.acce(acc.slot), acc.phase ^ 1u, b.ctl, b.status))) return;
+    if (lane < TB) {
+      float* f = b.fac(acc.slot);
+      // the weight's scale first: the product with the token's stays in the result's range
+      f[lane] = r.w0 * r.tok * weight;
+      f[TB + lane] = r.w1 * r.tok * weight;
+      f[2 * TB + lane] = r.w2 * r.tok * weight;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b.accf(acc.slot));
+    acc.next(kAccBufs);
   }
 }
 
-// Rows of activations as E4M3 codes in shared memory: row r at r * stride, chunks of 16
-// in order; the scales of its K blocks.
-struct Acts {
-  uint32_t codes;
-  int stride;
-  float* scale;                             // [rows][nkb]
-  int nkb;
-};
+// ------------------------------------------------------------------ epilogue
 
-template <class Scale>
-__device__ __forceinline__ void put_codes(const Acts& s, int row, int k, const float (&v)[16]) {
-  const Scale b(block_amax(v));
-  if (k >= s.nkb * 128) return;
-  uint32_t q[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    q[j] = e4m3x4(b.quotient(v[4 * j]), b.quotient(v[4 * j + 1]), b.quotient(v[4 * j + 2]),
-                  b.quotient(v[4 * j + 3]));
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(s.codes + row * s.stride + k),
-               "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]) : "memory");
-  if ((threadIdx.x & 7) == 0) s.scale[row * s.nkb + k / kFp8Block] = b.scale;
-}
-
-// An item that a warp's run of K blocks begins and does not end.
-struct Tail {
-  int x, unit;                              // x < 0: none
-};
-
-template <int DT, int NT, int S>
-struct Layer {
+// Four warps: thread r holds rows r and r + 128 of the tile (gate and up row of column
+// r of the unit, or two output columns) for all tokens.
+template <int TB>
+struct Epilogue {
+  const Block<TB>& b;
   const Fp8MoeArgs& a;
   const Routes& rt;
-  float (*head)[32][NT * 4];                // sums of items that an earlier warp began
-  uint32_t ring, ring_scale;                // of this warp
-  int warp, lane;
+  int r;                                    // 0 .. 127
+  uint32_t meets = 0;
 
-  __device__ __forceinline__ uint32_t stage(int i) const { return ring + i * kStageBytes; }
-  __device__ __forceinline__ uint32_t scales(int i) const { return ring_scale + i * 8; }
+  // All four warps (bounded: a warp may have given up).
+  __device__ __forceinline__ bool meet() {
+    mbar_arrive(b.meet());
+    const bool ok = wait_soon(b.meet(), meets & 1u, b.ctl, b.status);
+    ++meets;
+    return __all_sync(kFullWarp, ok);
+  }
 
-  // The first S - 1 stages on their way.
-  __device__ __forceinline__ void prime(const Phase& p, Cursor& in) const {
-    __syncwarp();
-    in.start(p, warp);
-#pragma unroll 1
-    for (int i = 0; i < S - 1; ++i) {
-      if (in.left > 0) {
-        fetch(p, rt, in, stage(i), scales(i));
-        in.next(p);
+  // h of the unit's column r for the expert's tokens, quantised over the unit's columns.
+  __device__ __forceinline__ bool finish_h(int x, int unit, const float (&g)[TB],
+                                           const float (&u)[TB]) {
+    const int col = unit * 128 + r, warp = r >> 5, lane = r & 31;
+    const uint32_t tokens = rt.tokens[x];
+    const int nkb = (a.I + 127) / 128;
+    float h[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      h[t] = 0.f;
+      if (tokens >> t & 1u) {
+        if (col < a.I) h[t] = g[t] / (1.f + __expf(-g[t])) * u[t];
+        // magnitudes order as integers; a NaN counts as nothing
+        const float m = fmaxf(fabsf(h[t]), 0.f);
+        const uint32_t top = __reduce_max_sync(kFullWarp, __float_as_uint(m));
+        if (lane == 0) b.red()[warp * TB + t] = __uint_as_float(top);
       }
-      cp_commit();
+    }
+    if (!meet()) return false;
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      if (tokens >> t & 1u) {
+        const float* m = b.red() + t;
+        const BlockScale32 s(fmaxf(fmaxf(m[0], m[TB]), fmaxf(m[2 * TB], m[3 * TB])));
+        if (col < a.I)
+          a.hq[(static_cast<int64_t>(x) * TB + t) * a.ld_hq + col] =
+              static_cast<uint8_t>(e4m3x4(s.quotient(h[t]), 0.f, 0.f, 0.f));
+        if (r == 0) __stcg(a.hs + (static_cast<int64_t>(x) * nkb + unit) * TB + t, s.scale);
+      }
+    }
+    return meet();                          // the maxima have been read
+  }
+
+  __device__ __forceinline__ void finish_out(int unit, const float (&v)[TB], const float (&w)[TB]) {
+    const int c = unit * 256 + r;
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      if (t < a.T) {
+        if (c < a.N) out[t * a.ldo + c] = f32_to_out16(v[t], a.type);
+        if (c + 128 < a.N) out[t * a.ldo + c + 128] = f32_to_out16(w[t], a.type);
+      }
     }
   }
 
-  // A finished item: h of the expert's routes, or their rows of the output.
-  template <bool DOWN>
-  __device__ __forceinline__ void finish(int x, int unit, const float (&acc)[NT][4]) const {
-    const int first = rt.start[x], n = rt.start[x + 1] - first;
-    const int g = lane >> 2, t = lane & 3;
+  // The block's tiles of an item are added up: the item is finished here, or by the last
+  // block to come with its part.
+  __device__ __forceinline__ bool finish(const Phase& p, int item, bool whole, float (&v)[TB],
+                                         float (&w)[TB]) {
+    const int x = p.down ? 0 : item / p.units;
+    const int unit = p.down ? item : item % p.units;
+    if (!whole) {
+      const int c0 = p.owner(item * p.per_item), c1 = p.owner((item + 1) * p.per_item - 1);
+      // A block's first item is its part 0, its last one (if another) its part 1: of an
+      // item's blocks only the first can have begun with another.
+      const int other = p.begin(c0) / p.per_item == item ? 0 : 1;
+      auto part = [&](int block) {
+        return a.part + (2 * block + (block == c0 ? other : 0)) * (2 * TB * 128) + r;
+      };
+      float* mine = part(static_cast<int>(blockIdx.x));
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = nt * 8 + 2 * t + i;
-        if (j >= n) continue;
-        const int64_t r = rt.route[first + j];
-        if constexpr (DOWN) {
-          const int c = unit * 16 + g;
-          if (c < a.N) __stcg(a.part + r * a.N + c, acc[nt][i]);
-          if (c + 8 < a.N) __stcg(a.part + r * a.N + c + 8, acc[nt][2 + i]);
-        } else {
-          const float gate = acc[nt][i], up = acc[nt][2 + i];
-          __stcg(a.h + r * a.I + unit * 8 + g, gate / (1.f + __expf(-gate)) * up);
+      for (int t = 0; t < TB; ++t) {
+        if (t < a.T) {
+          __stcg(mine + t * 128, v[t]);
+          __stcg(mine + (TB + t) * 128, w[t]);
         }
       }
-    if constexpr (DOWN) {
       __threadfence();
-      __syncwarp();
+      const uint32_t all = static_cast<uint32_t>(c1 - c0 + 1);
       uint32_t before = 0;
-      if (lane == 0) before = atomicAdd(a.arrived + unit, 1u);
-      before = __shfl_sync(kFullWarp, before, 0);
-      if (before + 1 != static_cast<uint32_t>(rt.n_live)) return;
+      if (p.down) {
+        // output columns stand alone: the last of each warp's 64
+        __syncwarp();
+        if ((r & 31) == 0) before = atomicAdd(a.arrived + a.items1 + 4 * item + (r >> 5), 1u);
+        before = __shfl_sync(kFullWarp, before, 0);
+      } else {
+        // a block of h is quantised together
+        if (!meet()) return false;
+        uint32_t* said = reinterpret_cast<uint32_t*>(b.red());
+        if (r == 0) *said = atomicAdd(a.arrived + item, 1u);
+        if (!meet()) return false;
+        before = *said;
+        if (!meet()) return false;          // it has been read
+      }
+      if (before + 1u != all) return true;
       __threadfence();
-      for (int i = lane; i < a.T * 16; i += 32) {
-        const int tok = i >> 4, c = unit * 16 + (i & 15);
-        if (c >= a.N) continue;
-        float v = 0.f;
-        for (int k = 0; k < a.rule.topk; ++k) {
-          const int r = tok * a.rule.topk + k;
-          if (rt.expert[r] >= 0)
-            v = fmaf(rt.weight[r], __ldcg(a.part + static_cast<int64_t>(r) * a.N + c), v);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) v[t] = w[t] = 0.f;
+      // the parts in block order, 64 reads on their way (a read takes about 0.7 us)
+      constexpr int kTogether = 32 / TB;
+#pragma unroll 1
+      for (int c = c0; c <= c1; c += kTogether) {
+        float pv[kTogether][TB], pw[kTogether][TB];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const float* q = part(min(c + i, c1));
+#pragma unroll
+          for (int t = 0; t < TB; ++t) {
+            pv[i][t] = t < a.T ? __ldcg(q + t * 128) : 0.f;
+            pw[i][t] = t < a.T ? __ldcg(q + (TB + t) * 128) : 0.f;
+          }
         }
-        static_cast<uint16_t*>(a.out)[tok * a.ldo + c] = static_cast<uint16_t>(f32_to_elem<DT>(v));
-      }
-    }
-  }
-
-  // The warp's run of K blocks, primed before.  Row of the activations of an entry:
-  // its token (gate_up), or its place among the block's entries from entry0 on (down).
-  template <bool DOWN>
-  __device__ __forceinline__ Tail stream(const Phase& p, const Acts& act, int entry0, Cursor& in,
-                                         float (&acc)[NT][4]) const {
-    auto act_row = [&](int entry) {
-      return DOWN ? entry - entry0 : rt.route[entry] / a.rule.topk;
-    };
-    Cursor c;
-    c.start(p, warp);
-    const int g = lane >> 2, t = lane & 3;
-    bool is_head = c.left > 0 && c.kb != 0;             // begun by an earlier warp
-    uint32_t row[NT];
-    int col[NT][2];
-    int x = -1, tiles = 0, slot = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      row[nt] = 0;
-      col[nt][0] = col[nt][1] = 0;
+        for (int i = 0; i < kTogether; ++i) {
+          if (c + i <= c1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-    }
-    while (c.left > 0) {
-      cp_wait<S - 2>();
-      __syncwarp();                      // the stage is there for every lane, and the one
-      if (in.left > 0) {                 // before it has been read by every lane
-        const int s = slot == 0 ? S - 1 : slot - 1;
-        fetch(p, rt, in, stage(s), scales(s));
-        in.next(p);
-      }
-      cp_commit();
-      if (c.x != x) {
-        x = c.x;
-        const int first = rt.start[x], n = rt.start[x + 1] - first;
-        tiles = (n + 7) >> 3;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // columns past the expert's routes repeat its last one; nobody reads them
-          row[nt] = act.codes + act.stride * act_row(first + min(nt * 8 + g, n - 1));
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            col[nt][i] = act_row(first + min(nt * 8 + 2 * t + i, n - 1)) * act.nkb;
-        }
-      }
-      const uint32_t st = stage(slot);
-      float sum[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[nt][i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int chunk = (t + 4 * j) ^ ((g & 1) << 2);
-        const uint4 lo = lds128(st + g * 128 + chunk * 16);
-        const uint4 hi = lds128(st + (g + 8) * 128 + chunk * 16);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (nt < tiles) {
-            const uint4 b = lds128(row[nt] + c.kb * 128 + (t + 4 * j) * 16);
-            mma_e4m3(sum[nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-            mma_e4m3(sum[nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+            for (int t = 0; t < TB; ++t) { v[t] += pv[i][t]; w[t] += pw[i][t]; }
           }
         }
       }
-      float s_lo, s_hi;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s_lo), "=f"(s_hi) : "r"(scales(slot))
-                   : "memory");
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt < tiles) {
-          const float a0 = act.scale[col[nt][0] + c.kb], a1 = act.scale[col[nt][1] + c.kb];
-          acc[nt][0] = fmaf(sum[nt][0], a0 * s_lo, acc[nt][0]);
-          acc[nt][1] = fmaf(sum[nt][1], a1 * s_lo, acc[nt][1]);
-          acc[nt][2] = fmaf(sum[nt][2], a0 * s_hi, acc[nt][2]);
-          acc[nt][3] = fmaf(sum[nt][3], a1 * s_hi, acc[nt][3]);
-        }
-      }
-      slot = slot + 1 == S ? 0 : slot + 1;
-      const int unit = c.unit;
-      const bool ends = c.kb == p.nkb - 1;
-      c.next(p);
-      if (ends || c.left == 0) {
-        if (is_head) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) head[warp][lane][nt * 4 + i] = acc[nt][i];
-          is_head = false;
-        } else if (ends) {
-          finish<DOWN>(x, unit, acc);
-        } else {
-          return Tail{x, unit};
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-      }
     }
-    return Tail{-1, 0};
+    if (p.down) {
+      finish_out(unit, v, w);
+      return true;
+    }
+    return finish_h(x, unit, v, w);
   }
 
-  // After a block barrier: the later warps' sums of the item that this warp began.
-  template <bool DOWN>
-  __device__ __forceinline__ void join(const Phase& p, const Tail& tail, float (&acc)[NT][4]) const {
-    if (tail.x < 0) return;
-    const int64_t n = static_cast<int64_t>(p.count) * p.nkb;
-    const int end = (tail.x * p.units + tail.unit - p.first + 1) * p.nkb;
-    for (int w = warp + 1; w < kWarps; ++w) {
-      const int from = share(n, w, kWarps);
-      if (from >= end) break;
-      if (from == share(n, w + 1, kWarps)) continue;    // no K block of its own
+  __device__ __forceinline__ bool run(const Phase& p, Ring& acc) {
+    using S = Shape<TB>;
+    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(r >> 5) << 21);
+    Cursor c;
+    c.at(p, p.first);
+    int item = p.first / p.per_item, inner = p.first - item * p.per_item;
+    bool from_start = inner == 0;
+    float v[TB], w[TB];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int t = 0; t < TB; ++t) v[t] = w[t] = 0.f;
+    for (int i = 0; i < p.count; ++i) {
+      const bool ok = wait_soon(b.accf(acc.slot), acc.phase, b.ctl, b.status);
+      if (!__all_sync(kFullWarp, ok)) return false;
+      tc_fence_after();
+      // which of the two scales of the second group: rows past a multiple of 128
+      const int second =
+          !p.down && (a.I + c.unit * 128 + r) / 128 != (a.I + c.unit * 128) / 128 ? 2 : 1;
+      const uint32_t tokens = p.down ? rt.tokens[c.x] : ~0u;
+      const float* f0 = b.fac(acc.slot);
+      const float* f1 = f0 + second * TB;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][i] += head[w][lane][nt * 4 + i];
+      for (int t0 = 0; t0 < TB; t0 += 8) {
+        uint32_t d[8], e[8];
+        tmem_ld8(lanes + acc.slot * 2 * S::kCols + t0, d);
+        tmem_ld8(lanes + acc.slot * 2 * S::kCols + S::kCols + t0, e);
+        tmem_ld_wait();
+        keep_after(d);
+        keep_after(e);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          // a token that the expert does not have brings codes of no meaning
+          if (tokens >> (t0 + t) & 1u) {
+            v[t0 + t] = fmaf(__uint_as_float(d[t]), f0[t0 + t], v[t0 + t]);
+            w[t0 + t] = fmaf(__uint_as_float(e[t]), f1[t0 + t], w[t0 + t]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(b.acce(acc.slot));
+      acc.next(kAccBufs);
+      c.next(p);
+      if (++inner == p.per_item || i + 1 == p.count) {
+        if (!finish(p, item, from_start && inner == p.per_item, v, w)) return false;
+        if (inner == p.per_item) {
+          inner = 0;
+          ++item;
+          from_start = true;
+        }
+#pragma unroll
+        for (int t = 0; t < TB; ++t) v[t] = w[t] = 0.f;
+      }
     }
-    finish<DOWN>(tail.x, tail.unit, acc);
+    return true;
   }
 };
 
-// Logits of the block's experts: the warps share K, every one for all tokens.
-template <int DT, int RT, int MT>
-__device__ __noinline__ void router_logits(const Fp8MoeArgs& a, float (*part)[MT]) {
+// Logits of the block's experts: the threads share K, the weights' loads are issued
+// together and a token's ahead of the one before it.
+template <int DT, int RT, int TB>
+__device__ __forceinline__ void router_logits(const Fp8MoeArgs& a, float (*part)[TB]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int N = elems_per_16b<DT>();
+  constexpr int kChunks = 4, kPass = kThreads * 8 * kChunks;
+  const int k0 = threadIdx.x * 8;
   for (int e = blockIdx.x; e < a.rule.E; e += gridDim.x) {
-    float acc[MT];
+    for (int from = 0; from < a.K; from += kPass) {
+      Pack<DT, 8> x[kChunks];
+      float w[kChunks][8];
+      auto load = [&](int t) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = 0.f;
-    for (int k = (warp * 32 + lane) * N; k < a.K; k += kThreads * N) {
-      float w[N];
-      if constexpr (RT == NVFP4_FP32) {
-        Pack<NVFP4_FP32, 4> lo, hi;
-        lo.load(a.router, static_cast<int64_t>(e) * a.K + k);
-        hi.load(a.router, static_cast<int64_t>(e) * a.K + k + 4);
+        for (int c = 0; c < kChunks; ++c) {
+          const int k = from + k0 + c * kThreads * 8;
+          x[c].zero();
+          if (k < a.K && t < a.T) x[c].load(a.x, t * a.ld + k);
+        }
+      };
+      load(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { w[i] = lo.get(i); w[4 + i] = hi.get(i); }
-      } else {
-        Pack<RT, N> v;
-        v.load(a.router, static_cast<int64_t>(e) * a.K + k);
+      for (int c = 0; c < kChunks; ++c) {
+        const int k = from + k0 + c * kThreads * 8;
+        const int64_t at = static_cast<int64_t>(e) * a.K + k;
+        if constexpr (RT == NVFP4_FP32) {
+          Pack<NVFP4_FP32, 4> lo, hi;
+          lo.zero();
+          hi.zero();
+          if (k < a.K) { lo.load(a.router, at); hi.load(a.router, at + 4); }
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = v.get(i);
-      }
+          for (int i = 0; i < 4; ++i) { w[c][i] = lo.get(i); w[c][4 + i] = hi.get(i); }
+        } else {
+          Pack<RT, 8> v;
+          v.zero();
+          if (k < a.K) v.load(a.router, at);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        if (t < a.T) {
-          Pack<DT, N> v;
-          v.load(a.x, t * a.ld + k);
-#pragma unroll
-          for (int i = 0; i < N; ++i) acc[t] = fmaf(v.get(i), w[i], acc[t]);
+          for (int i = 0; i < 8; ++i) w[c][i] = v.get(i);
         }
       }
-    }
+#pragma unroll 1
+      for (int t = 0; t < a.T; ++t) {
+        float sum[kChunks];
+        Pack<DT, 8> now[kChunks];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      acc[t] = warp_sum(acc[t]);
-      if (lane == 0) part[warp][t] = acc[t];
+        for (int c = 0; c < kChunks; ++c) now[c] = x[c];
+        load(t + 1);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          sum[c] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[c] = fmaf(now[c].get(i), w[c][i], sum[c]);
+        }
+        const float v = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (lane == 0) part[warp][t] = from == 0 ? v : part[warp][t] + v;
+      }
     }
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < a.T) {
@@ -421,7 +551,7 @@ __device__ __noinline__ void router_logits(const Fp8MoeArgs& a, float (*part)[MT
 }
 
 template <int L>
-__device__ __noinline__ void gate_token(const Fp8MoeArgs& a, Routes& rt, int t) {
+__device__ __forceinline__ void gate_token(const Fp8MoeArgs& a, Routes& rt, int t) {
   const int lane = threadIdx.x & 31;
   float l[L];
 #pragma unroll
@@ -443,35 +573,35 @@ __device__ __noinline__ void gate_token(const Fp8MoeArgs& a, Routes& rt, int t) 
   }
 }
 
-// The routes by expert, the same in every block.
-__device__ __noinline__ void list_experts(const Fp8MoeArgs& a, Routes& rt, int2* scan) {
-  const int R = a.T * a.rule.topk;
+// The routes by expert, the same in every block: an expert's tokens are the bits of a
+// word, a route's place among the expert's the bits below its own.
+__device__ __forceinline__ void list_experts(const Fp8MoeArgs& a, Routes& rt, uint32_t* bits,
+                                             int2* scan) {
+  const int topk = a.rule.topk, R = a.T * topk;
   const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
+  for (int i = r; i < a.rule.E; i += kThreads) bits[i] = 0;
   if (!a.router && r < a.T) {
     // an expert that a token names twice: once, with both weights
-    for (int k = 1; k < a.rule.topk; ++k)
-      for (int j = 0; j < k; ++j) {
-        const int i = r * a.rule.topk;
+    const int i = r * topk;
+#pragma unroll 1
+    for (int k = 1; k < topk; ++k)
+#pragma unroll 1
+      for (int j = 0; j < k; ++j)
         if (rt.expert[i + k] >= 0 && rt.expert[i + k] == rt.expert[i + j]) {
           rt.weight[i + j] += rt.weight[i + k];
           rt.expert[i + k] = -1;
         }
-      }
   }
   __syncthreads();
   const int e = r < R ? rt.expert[r] : -1;
-  int first = r, place = 0, count = 0;
-  if (e >= 0) {
-    for (int i = 0; i < R; ++i)
-      if (rt.expert[i] == e) {
-        first = min(first, i);
-        place += i < r;
-        ++count;
-      }
-  }
-  const bool lead = e >= 0 && first == r;
+  const int t = r / topk;
+  if (e >= 0) atomicOr(bits + e, 1u << t);
+  __syncthreads();
+  const uint32_t tokens = e >= 0 ? bits[e] : 0u;
+  const uint32_t below = e >= 0 ? tokens & ((1u << t) - 1u) : 0u;
+  const bool lead = e >= 0 && below == 0;
   // exclusive sums over the leading routes: experts (x) and entries (y)
-  int2 v = make_int2(lead ? 1 : 0, lead ? count : 0);
+  int2 v = make_int2(lead ? 1 : 0, lead ? __popc(tokens) : 0);
   const int2 own = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -481,63 +611,115 @@ __device__ __noinline__ void list_experts(const Fp8MoeArgs& a, Routes& rt, int2*
   if (lane == 31) scan[warp] = v;
   __syncthreads();
   int2 base = make_int2(v.x - own.x, v.y - own.y);
+#pragma unroll 1
   for (int w = 0; w < warp; ++w) { base.x += scan[w].x; base.y += scan[w].y; }
   if (lead) {
     rt.live[base.x] = static_cast<int16_t>(e);
     rt.start[base.x] = static_cast<int16_t>(base.y);
-    rt.at[r] = static_cast<int16_t>(base.y);
+    rt.tokens[base.x] = tokens;
+    bits[e] = base.y;                       // from here on: the expert's first entry
   }
-  if (r == kThreads - 1) {
-    rt.n_live = base.x + own.x;
-    rt.start[base.x + own.x] = static_cast<int16_t>(base.y + own.y);
-  }
+  if (r == kThreads - 1) rt.n_live = base.x + own.x;
   __syncthreads();
-  if (e >= 0) rt.route[rt.at[first] + place] = static_cast<int16_t>(r);
+  if (e >= 0) rt.route[bits[e] + __popc(below)] = static_cast<int16_t>(r);
   __syncthreads();
 }
 
-template <int DT, int NT, int S>
-__global__ void __launch_bounds__(kThreads, 1) fp8_moe_kernel(const Fp8MoeArgs a,
-                                                              const Fp8MoePlan plan) {
-  extern __shared__ __align__(128) uint8_t smem[];
+// Rows of x as codes and scales in the workspace, spread over the grid's warps from the
+// last block on (the first ones have the router's experts).
+template <int DT>
+__device__ __forceinline__ void quantise_tokens(const Fp8MoeArgs& a, int columns) {
+  const int lane = threadIdx.x & 31;
+  const int chunks = (a.K + 511) / 512;
+  for (int i = (threadIdx.x >> 5) * gridDim.x + gridDim.x - 1 - blockIdx.x; i < a.T * chunks;
+       i += kWarps * gridDim.x) {
+    const int t = i / chunks, k = (i - t * chunks) * 512 + lane * 16;
+    float v[16];
+    if (k < a.K) {
+      load_row16<DT, false>(a.x, t * a.ld, a.K, k, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+    }
+    const BlockScale s(block_amax(v));
+    if (k >= a.K) continue;
+    uint4 q;
+    uint32_t* qw = reinterpret_cast<uint32_t*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      qw[j] = e4m3x4(s.quotient(v[4 * j]), s.quotient(v[4 * j + 1]), s.quotient(v[4 * j + 2]),
+                     s.quotient(v[4 * j + 3]));
+    *reinterpret_cast<uint4*>(a.xq + t * a.ld_xq + k) = q;
+    if ((lane & 7) == 0) __stcg(a.xs + (k / kFp8Block) * columns + t, s.scale);
+  }
+}
+
+// What the first barrier waits for.
+template <int DT, int TB>
+__device__ __forceinline__ void before_gate(const Fp8MoeArgs& a, float (*part)[TB]) {
+  quantise_tokens<DT>(a, TB);
+  if (!a.router) return;
+  if (a.router_type == NVFP4_FP32) router_logits<DT, NVFP4_FP32, TB>(a, part);
+  else router_logits<DT, DT, TB>(a, part);
+}
+
+template <int TB>
+__global__ void __launch_bounds__(kThreads, 1)
+fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ CUtensorMap t2,
+               const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap th,
+               const __grid_constant__ Fp8MoeArgs a) {
+  using S = Shape<TB>;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ Routes rt;
-  __shared__ float head[kWarps][32][NT * 4];
-  __shared__ float part[kWarps][NT * 8];
+  __shared__ float part[kWarps][TB];
   __shared__ int2 scan[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem);
-  const uint32_t ring_scales = base + kWarps * S * kStageBytes;
-  const uint32_t act_codes = ring_scales + kWarps * S * 8;
-  float* act_scales = reinterpret_cast<float*>(smem + kWarps * S * (kStageBytes + 8) +
-                                               plan.act_rows * plan.act_stride);
-  const Layer<DT, NT, S> layer{a, rt, head, base + warp * S * kStageBytes,
-                               ring_scales + warp * S * 8, warp, lane};
+  __shared__ uint32_t bits[kGateMaxExperts];
+  Block<TB> b;
+  b.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~static_cast<uintptr_t>(1023));
+  b.base = smem_u32(b.smem);
+  b.ctl = reinterpret_cast<CtaCtl*>(b.smem + S::kCtlOffset);
+  b.status = a.status;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b.smem + S::kCtlOffset + 16);
+  const int warp = threadIdx.x >> 5;
   cg::grid_group grid = cg::this_grid();
 
-  const int units2 = (a.N + 15) / 16;
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < units2; i += gridDim.x * kThreads)
-    __stcg(a.arrived + i, 0u);
-  if (a.router) {
-    if (a.router_type == NVFP4_FP32) router_logits<DT, NVFP4_FP32, NT * 8>(a, part);
-    else router_logits<DT, DT, NT * 8>(a, part);
-  }
-  Acts act{act_codes, plan.act_stride, act_scales, (a.K + 127) / 128};
-  {
-    const int chunks = (a.K + 511) / 512;
-    for (int i = warp; i < a.T * chunks; i += kWarps) {
-      const int t = i / chunks, k = (i - t * chunks) * 512 + lane * 16;
-      float v[16];
-      if (k < a.K) {
-        load_row16<DT, false>(a.x, t * a.ld, a.K, k, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = 0.f;
-      }
-      put_codes<BlockScale>(act, t, k, v);
+  if (threadIdx.x == 0) {
+    prefetch_map(&t1);
+    prefetch_map(&t2);
+    prefetch_map(&tx);
+    prefetch_map(&th);
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(b.full(s), 1);
+      mbar_init(b.empty(s), 1);
     }
+    for (int i = 0; i < kAccBufs; ++i) {
+      mbar_init(b.accf(i), 2);                  // the sums, and the factors
+      mbar_init(b.acce(i), 4);
+    }
+    mbar_init(b.drain(), 1);
+    mbar_init(b.meet(), 128);
+    b.ctl->abort = 0;
+    b.ctl->timeout_ns = a.timeout_ns;
+    fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), S::kTmemCols);
+    tmem_relinquish();
+  }
+  const int units1 = (a.I + 127) / 128, units2 = (a.N + 255) / 256;
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.items1 + 4 * units2;
+       i += gridDim.x * kThreads)
+    __stcg(a.arrived + i, 0u);
+  if (a.type == NVFP4_BF16) before_gate<NVFP4_BF16, TB>(a, part);
+  else before_gate<NVFP4_FP16, TB>(a, part);
+  fence_proxy_async_global();                   // the codes are read by TMA
+  tc_fence_before();
+  grid.sync();
+  tc_fence_after();
+  b.tmem = *tmem_slot;
+
   if (a.router) {
-    grid.sync();
     for (int t = warp; t < a.T; t += kWarps) {
       if (a.rule.E <= 128) gate_token<4>(a, rt, t);
       else if (a.rule.E <= 256) gate_token<8>(a, rt, t);
@@ -554,131 +736,199 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_moe_kernel(const Fp8MoeArgs a
     }
   }
   __syncthreads();
-  list_experts(a, rt, scan);
+  list_experts(a, rt, bits, scan);
 
-  Phase p;
-  auto place = [&](int units) {
-    p.units = units;
-    const int64_t items = static_cast<int64_t>(rt.n_live) * units;
-    p.first = share(items, blockIdx.x, gridDim.x);
-    p.count = share(items, blockIdx.x + 1, gridDim.x) - p.first;
+  Phase p1, p2;
+  p1.set(0, (a.K + 127) / 128, units1, rt.n_live);
+  p2.set(1, (a.I + 127) / 128, units2, rt.n_live);
+  const int early = min(S::kStages, p2.count);  // down tiles whose weights go ahead
+  Ring ring, acc;
+  const uint32_t idesc = idesc_e4m3(128, S::kCols);
+  const bool lead = warp < 2 && elect_one();
+  Cursor c;
+  uint32_t issued = 0;
+  bool alive = true;
+
+  auto multiply = [&](const Phase& p) {
+    for (int i = 0; i < p.count && alive; ++i) {
+      if (!wait_both(b.acce(acc.slot), acc.phase ^ 1u, b.full(ring.slot), ring.phase, b.ctl,
+                     b.status)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t s = b.stage(ring.slot), d = b.tmem + acc.slot * 2 * S::kCols;
+      const uint64_t tok = sdesc_sw128(s + S::kTokOffset);
+      tc_mma_e4m3_k128(d, sdesc_sw128(s), tok, idesc);
+      tc_mma_e4m3_k128(d + S::kCols, sdesc_sw128(s + kGroupBytes), tok, idesc);
+      tc_commit(b.accf(acc.slot));
+      tc_commit(b.empty(ring.slot));
+      ring.next(S::kStages);
+      acc.next(kAccBufs);
+    }
   };
-  float acc[NT][4];
-  Cursor in;
-  p.w = a.w1; p.s = a.s1; p.K = a.K; p.nkb = (a.K + 127) / 128;
-  p.nnb = (2 * a.I + 127) / 128; p.rows = 2 * a.I; p.half = a.I;
-  place(a.I / 8);
-  layer.prime(p, in);
-  Tail tail = layer.template stream<false>(p, act, 0, in, acc);
-  const Phase gate_up = p;
-  p.w = a.w2; p.s = a.s2; p.K = a.I; p.nkb = (a.I + 127) / 128;
-  p.nnb = (a.N + 127) / 128; p.rows = a.N; p.half = 0;
-  place(units2);
-  layer.prime(p, in);                       // on their way across the barrier
-  __syncthreads();
-  layer.template join<false>(gate_up, tail, acc);
+  Epilogue<TB> epi{b, a, rt, static_cast<int>(threadIdx.x) & 127};
+
+  // ------------------------------------------------------------------ gate_up
+  if (warp == 0) {
+    if (lead) {
+      fence_proxy_async_global();
+      const Producer<TB> first{b, rt, &t1, &tx, l2_policy_evict_first(), l2_policy_evict_last()};
+      c.at(p1, p1.first);
+      for (int i = 0; i < p1.count; ++i) {
+        if (!wait_soon(b.empty(ring.slot), ring.phase ^ 1u, b.ctl, b.status)) {
+          alive = false;
+          break;
+        }
+        first.weights(p1, c, ring.slot);
+        first.tokens(p1, c, ring.slot);
+        ++issued;
+        ring.next(S::kStages);
+        c.next(p1);
+      }
+      // down weights as the stages come free: they need no h
+      const Producer<TB> then{b, rt, &t2, &th, first.wpol, first.tpol};
+      Ring r = ring;
+      c.at(p2, p2.first);
+      for (int i = 0; i < early && alive; ++i) {
+        if (!wait_soon(b.empty(r.slot), r.phase ^ 1u, b.ctl, b.status)) {
+          alive = false;
+          break;
+        }
+        then.weights(p2, c, r.slot);
+        ++issued;
+        r.next(S::kStages);
+        c.next(p2);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lead) multiply(p1);
+    __syncwarp();
+  } else if (warp == 2) {
+    factors<TB>(b, a, rt, p1, acc);
+  } else if (warp >= 4) {
+    alive = epi.run(p1, acc);
+    fence_proxy_async_global();                 // so are the codes of h
+  }
   grid.sync();
 
-  act.nkb = (a.I + 127) / 128;
-  int entry0 = 0;
-  if (p.count > 0) {
-    const int x1 = (p.first + p.count - 1) / p.units;
-    entry0 = rt.start[p.first / p.units];
-    const int rows = rt.start[x1 + 1] - entry0;
-    const int chunks = (a.I + 511) / 512;
-    for (int i = warp; i < rows * chunks; i += kWarps) {
-      const int j = i / chunks, k = (i - j * chunks) * 512 + lane * 16;
-      float v[16];
-      const float4* src = reinterpret_cast<const float4*>(
-          a.h + static_cast<int64_t>(rt.route[entry0 + j]) * a.I + k);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 f = k < a.I ? __ldcg(src + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+  // --------------------------------------------------------------------- down
+  if (warp == 0) {
+    if (lead) {
+      fence_proxy_async_global();
+      const Producer<TB> then{b, rt, &t2, &th, l2_policy_evict_first(), l2_policy_evict_last()};
+      c.at(p2, p2.first);
+      for (int i = 0; i < p2.count; ++i) {
+        if (i >= early) {
+          if (!alive || !wait_soon(b.empty(ring.slot), ring.phase ^ 1u, b.ctl, b.status)) break;
+          then.weights(p2, c, ring.slot);
+          ++issued;
+        } else if (!alive) {
+          break;
+        }
+        then.tokens(p2, c, ring.slot);
+        ring.next(S::kStages);
+        c.next(p2);
       }
-      put_codes<BlockScale32>(act, j, k, v);
+      // what is on its way lands before the shared memory goes away
+      const uint32_t late = issued > static_cast<uint32_t>(S::kStages) ? issued - S::kStages : 0u;
+      for (uint32_t i = late; i < issued; ++i)
+        wait_drain(b.full(static_cast<int>(i % S::kStages)), (i / S::kStages) & 1u,
+                   b.ctl->timeout_ns);
     }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lead) {
+      multiply(p2);
+      tc_commit(b.drain());
+      wait_drain(b.drain(), 0, b.ctl->timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    factors<TB>(b, a, rt, p2, acc);
+  } else if (warp >= 4) {
+    if (alive) epi.run(p2, acc);
   }
-  __syncthreads();
-  tail = layer.template stream<true>(p, act, entry0, in, acc);
-  __syncthreads();
-  layer.template join<true>(p, tail, acc);
-  cp_wait<0>();
-  if (rt.n_live == 0)                       // no route at all
+  if (rt.n_live == 0)                           // no route at all
     for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * a.N;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
       static_cast<uint16_t*>(a.out)[i / a.N * a.ldo + i % a.N] = 0;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(b.tmem, S::kTmemCols);
+  }
 }
 
-template <int DT, int NT, int S>
-cudaError_t go(const Fp8MoeArgs& a, const Fp8MoePlan& p, cudaStream_t s) {
-  void* args[] = {const_cast<Fp8MoeArgs*>(&a), const_cast<Fp8MoePlan*>(&p)};
-  return cudaLaunchCooperativeKernel(fp8_moe_kernel<DT, NT, S>, dim3(p.grid), dim3(kThreads), args,
-                                     p.smem, s);
-}
-template <int DT, int NT>
-cudaError_t by_stages(const Fp8MoeArgs& a, const Fp8MoePlan& p, cudaStream_t s) {
-  if (p.stages == 12) return go<DT, NT, 12>(a, p, s);
-  if (p.stages == 8) return go<DT, NT, 8>(a, p, s);
-  return go<DT, NT, 5>(a, p, s);
-}
-template <int DT>
-cudaError_t by_tiles(const Fp8MoeArgs& a, const Fp8MoePlan& p, cudaStream_t s) {
-  return p.tiles == 1 ? by_stages<DT, 1>(a, p, s) : by_stages<DT, 2>(a, p, s);
+template <int TB>
+cudaError_t go(const CUtensorMap& t1, const CUtensorMap& t2, const CUtensorMap& tx,
+               const CUtensorMap& th, const Fp8MoeArgs& a, int sms, cudaStream_t s) {
+  void* args[] = {const_cast<CUtensorMap*>(&t1), const_cast<CUtensorMap*>(&t2),
+                  const_cast<CUtensorMap*>(&tx), const_cast<CUtensorMap*>(&th),
+                  const_cast<Fp8MoeArgs*>(&a)};
+  return cudaLaunchCooperativeKernel(fp8_moe_kernel<TB>,
+                                     dim3(sms < kMoeMaxGrid ? sms : kMoeMaxGrid), dim3(kThreads),
+                                     args, Shape<TB>::kSmemBytes, s);
 }
 
-template <int DT, int NT, int S>
+template <int TB>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(fp8_moe_kernel<DT, NT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kMoeSmemMost));
-}
-template <int DT, int NT>
-cudaError_t set_stages() {
-  cudaError_t e = set_smem<DT, NT, 12>();
-  if (e == cudaSuccess) e = set_smem<DT, NT, 8>();
-  if (e == cudaSuccess) e = set_smem<DT, NT, 5>();
-  return e;
+  return cudaFuncSetAttribute(fp8_moe_kernel<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<TB>::kSmemBytes);
 }
 
 }  // namespace
 
 cudaError_t init_fp8_moe_attributes() {
-  cudaError_t e = set_stages<NVFP4_BF16, 1>();
-  if (e == cudaSuccess) e = set_stages<NVFP4_BF16, 2>();
-  if (e == cudaSuccess) e = set_stages<NVFP4_FP16, 1>();
-  if (e == cudaSuccess) e = set_stages<NVFP4_FP16, 2>();
+  cudaError_t e = set_smem<8>();
+  if (e == cudaSuccess) e = set_smem<16>();
+  if (e == cudaSuccess) e = set_smem<32>();
   return e;
 }
 
-bool fp8_moe_plan(int T, int topk, int E, int64_t K, int64_t I, int64_t N, int sms, Fp8MoePlan* p) {
-  if (T > kMoeMaxTokens || T * topk > kMoeMaxRoutes || E > kGateMaxExperts ||
+int fp8_moe_box_rows(int columns) { return columns < 16 ? 16 : columns; }
+
+bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N,
+                    MoeLayout* m) {
+  if (T <= 0 || topk <= 0 || E <= 0 || topk > E || K <= 0 || I <= 0 || N <= 0 || K % 16 != 0 ||
+      I % 16 != 0 || T > kMoeMaxTokens || T * topk > kMoeMaxRoutes || E > kGateMaxExperts ||
       topk > kGateMaxTopk || K > (1 << 20) || I > (1 << 20) || N > (1 << 20))
     return false;
-  p->tiles = T > 8 ? 2 : 1;
-  p->grid = sms;
-  // the rows of h that a block can need: those of the experts that its items span
-  const int64_t R = static_cast<int64_t>(T) * topk, live = R < E ? R : E;
-  const int64_t units = (N + 15) / 16, run = (live * units + sms - 1) / sms;
-  const int64_t span = run <= 1 ? 1 : (run - 2) / units + 2;
-  const int64_t rows = span * T < R ? span * T : R;
-  const int64_t kx = (K + 127) / 128, kh = (I + 127) / 128;
-  const int64_t wide = kx > kh ? kx : kh;
-  p->act_rows = static_cast<int>(T > rows ? T : rows);
-  p->act_stride = static_cast<int>(wide * 128 + 64);       // two rows' chunks in different banks
-  const int64_t acts = p->act_rows * (p->act_stride + wide * 4);
-  for (int s : {12, 8, 5}) {
-    const int64_t bytes = static_cast<int64_t>(kWarps) * s * (kStageBytes + 8) + acts;
-    if (bytes <= static_cast<int64_t>(kMoeSmemMost)) {
-      p->stages = s;
-      p->smem = static_cast<size_t>(bytes);
-      return true;
-    }
-  }
-  return false;
+  const int64_t R = T * topk;
+  const int64_t live = R < E ? R : E, kx = (K + 127) / 128, kh = (I + 127) / 128;
+  const int64_t units2 = (N + 255) / 256;
+  if (live * kh * kx > 0x3FFFFFFF || live * kh * units2 > 0x3FFFFFFF) return false;   // tiles
+  size_t end = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = end;
+    end += static_cast<size_t>((bytes + 255) / 256 * 256);
+    return at;
+  };
+  m->columns = T > 16 ? 32 : T > 8 ? 16 : 8;
+  m->experts = static_cast<int>(live);
+  m->ld_xq = kx * 128;
+  m->ld_hq = kh * 128;
+  take(T * E * 4);
+  m->xq = take(m->columns * m->ld_xq);
+  m->xs = take(kx * m->columns * 4);
+  m->hq = take(live * m->columns * m->ld_hq);
+  m->hs = take(live * kh * m->columns * 4);
+  m->part = take(static_cast<int64_t>(2) * kMoeMaxGrid * 2 * m->columns * 128 * 4);
+  m->arrived = take((live * kh + 4 * units2) * 4);
+  m->bytes = end;
+  return true;
 }
 
-cudaError_t launch_fp8_moe(const Fp8MoeArgs& a, const Fp8MoePlan& p, int dtype, cudaStream_t s) {
-  return dtype == NVFP4_BF16 ? by_tiles<NVFP4_BF16>(a, p, s) : by_tiles<NVFP4_FP16>(a, p, s);
+cudaError_t launch_fp8_moe(const CUtensorMap& t1, const CUtensorMap& t2, const CUtensorMap& tx,
+                           const CUtensorMap& th, const Fp8MoeArgs& a, int columns, int sms,
+                           cudaStream_t s) {
+  switch (columns) {
+    case 8: return go<8>(t1, t2, tx, th, a, sms, s);
+    case 16: return go<16>(t1, t2, tx, th, a, sms, s);
+    default: return go<32>(t1, t2, tx, th, a, sms, s);
+  }
 }
 
 }  // namespace nvfp4

@@ -3,46 +3,64 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "gate.cuh"
 
 namespace nvfp4 {
 
-constexpr int kMoeMaxTokens = 16;
-constexpr int kMoeMaxRoutes = 256;
+constexpr int kMoeMaxTokens = 32;
+constexpr int kMoeMaxRoutes = 256;           // one thread each
+constexpr int kMoeMaxGrid = 160;
 
 struct Fp8MoeArgs {
   const void* x;                   // [T, K] BF16 or FP16, row stride ld
   int64_t ld;
+  int32_t type;                    // nvfp4_dtype of x and out
   const void* router;              // [E, K] (dense), or NULL: ids and weights are given
   int32_t router_type;             // nvfp4_dtype
   GateRule rule;                   // E and topk always; the rest with a router
   int32_t T, K, I, N;
-  const uint8_t* w1;               // codes [E, 2 I, K]: gate half, up half
-  const float* s1;                 // [E, ceil(2 I / 128), ceil(K / 128)]
-  const uint8_t* w2;               // codes [E, N, I]
-  const float* s2;                 // [E, ceil(N / 128), ceil(I / 128)]
+  const float* s1;                 // gate_up scales [E, ceil(2 I / 128), ceil(K / 128)]
+  const float* s2;                 // down scales [E, ceil(N / 128), ceil(I / 128)]
   int32_t* ids;                    // [T, topk]
   float* weights;                  // [T, topk]
   void* out;                       // [T, N], type of x, row stride ldo
   int64_t ldo;
-  float* logits;                   // workspace [T, E]
-  float* h;                        // workspace [T * topk, I]
-  float* part;                     // workspace [T * topk, N]
-  uint32_t* arrived;               // workspace [ceil(N / 16)]
+  // workspace (MoeLayout)
+  float* logits;                   // [T, E]
+  uint8_t* xq;                     // codes of x [columns, ld_xq]
+  int64_t ld_xq;
+  float* xs;                       // scales [blocks of K][columns]
+  uint8_t* hq;                     // codes of h [experts * columns, ld_hq]
+  int64_t ld_hq;
+  float* hs;                       // scales [experts][blocks of I][columns]
+  float* part;                     // [2 * grid][2][columns][128]
+  uint32_t* arrived;               // items1 of gate_up's items, then four of each of down's
+  int32_t items1;
   int* status;
+  uint64_t timeout_ns;
 };
 
-struct Fp8MoePlan {
-  int stages, tiles;               // ring stages of a warp; 8-token tiles
-  int act_stride, act_rows;        // activations in shared memory
-  size_t smem;
-  int grid;
+// Sizes that follow from a call's: token columns, live experts at most, and where
+// the workspace's parts begin.
+struct MoeLayout {
+  int columns, experts;
+  int64_t ld_xq, ld_hq;
+  size_t xq, xs, hq, hs, part, arrived, bytes;
 };
-// Whether the sizes fit the kernel, and its shape.
-bool fp8_moe_plan(int T, int topk, int E, int64_t K, int64_t I, int64_t N, int sms, Fp8MoePlan* p);
+// False for sizes that the kernel does not take.
+bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N,
+                    MoeLayout* m);
+
 cudaError_t init_fp8_moe_attributes();
-cudaError_t launch_fp8_moe(const Fp8MoeArgs& a, const Fp8MoePlan& p, int dtype, cudaStream_t s);
+// Rows of the maps' boxes of activations.
+int fp8_moe_box_rows(int columns);
+// t1: gate_up [2 E, I, K], t2: down [E, N, I] (boxes of 128 x 128); tx, th: codes of x
+// and h (boxes of fp8_moe_box_rows() x 128).
+cudaError_t launch_fp8_moe(const CUtensorMap& t1, const CUtensorMap& t2, const CUtensorMap& tx,
+                           const CUtensorMap& th, const Fp8MoeArgs& a, int columns, int sms,
+                           cudaStream_t s);
 
 }  // namespace nvfp4

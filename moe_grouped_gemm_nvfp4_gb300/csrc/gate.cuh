@@ -120,6 +120,7 @@ __device__ __noinline__ int gate_choose64(const GateRule& r, const float (&l)[L]
     }
   }
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j < r.topk; ++j) {
     unsigned long long best = 0;
     int at = 0;
@@ -169,6 +170,7 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
   int mine = 0;
   float chosen = 0.f, last_s = 0.f, last = 0.f;                   // last: the pick before
   bool near = false;
+#pragma unroll 1
   for (int j = 0; j < picks; ++j) {
     uint32_t best = 0;
     int at = 0;
@@ -197,6 +199,7 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
   if (near) {                                       // the same in every lane
     mine = gate_choose64<L>(r, l, g.max);
     // the score again, from the expert's lane
+#pragma unroll 1
     for (int j = 0; j < r.topk; ++j) {
       const int e = __shfl_sync(kFullWarp, mine, j);
       float val = 0.f;

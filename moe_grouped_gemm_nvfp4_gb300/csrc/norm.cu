@@ -149,12 +149,28 @@ __global__ void __launch_bounds__(MOST) rms_norm_kernel(const NormArgs a, int th
   for (int i = 0; i < V; ++i) {
     const int c = (i * threads + tid) * VEC;
     float y[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) y[j] = h[i * VEC + j] * rstd * w[i * VEC + j];
     if constexpr (FP8) {
+      // The quotient 448 y / max |y| does not hold rstd: it is taken from the products
+      // h w (exact for 16-bit factors), so that codes are rounded from the real quotient
+      // also next to a border; with rstd only where a maximum leaves the normal range.
       float amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) amax = fmaxf(amax, fabsf(y[j]));
+      for (int j = 0; j < VEC; ++j) {
+        y[j] = h[i * VEC + j] * w[i * VEC + j];
+        amax = fmaxf(amax, fabsf(y[j]));
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      const bool direct = amax >= kAmaxFloor && amax * rstd >= kAmaxFloor && amax < INFINITY;
+      if (!direct) {
+        amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          y[j] = h[i * VEC + j] * rstd * w[i * VEC + j];
+          amax = fmaxf(amax, fabsf(y[j]));
+        }
+      }
+      // (`direct` is the same in the 16 lanes of a block, not in the warp's two blocks)
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
       if (on && c < a.D) {
@@ -163,9 +179,12 @@ __global__ void __launch_bounds__(MOST) rms_norm_kernel(const NormArgs a, int th
         q.x = e4m3x4(b.quotient(y[0]), b.quotient(y[1]), b.quotient(y[2]), b.quotient(y[3]));
         q.y = e4m3x4(b.quotient(y[4]), b.quotient(y[5]), b.quotient(y[6]), b.quotient(y[7]));
         *reinterpret_cast<uint2*>(a.codes + row * a.D + c) = q;
-        if ((c & 127) == 0) a.scales[static_cast<int64_t>(c >> 7) * a.T + row] = b.scale;
+        if ((c & 127) == 0)
+          a.scales[static_cast<int64_t>(c >> 7) * a.T + row] = direct ? b.scale * rstd : b.scale;
       }
     } else if (on && c < a.D) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) y[j] = h[i * VEC + j] * rstd * w[i * VEC + j];
       Pack<DT, VEC> p;
       p.from(y);
       store<DT, VEC>(a.y, row * a.D + c, p);

@@ -357,10 +357,10 @@ class Fp8MLP:
         return tokens.combine(y, pos, topk_weights, offsets)
 
     def step_few(self, x, topk_ids, topk_weights, stream=None):
-        """step() of a few tokens in one launch: at most 16, whose activations fit
-        shared memory (ValueError for more).  gate_up's product and the experts' rows
-        stay FP32 here, where step() rounds them to x's type.  An expert that a token
-        names twice counts with both weights."""
+        """step() of a few tokens in one launch: at most 32 tokens and 256 routes
+        (ValueError for more).  gate_up's product and the experts' rows stay FP32 here,
+        where step() rounds them to x's type.  An expert that a token names twice counts
+        with both weights."""
         if forward_ad._current_level >= 0:
             tokens.refuse_tangents(x, topk_weights, *self.gate_up, *self.down)
         if stream is not None:
@@ -372,7 +372,7 @@ class Fp8MLP:
             return done[0]
         if x.shape[0] == 0:
             return x.new_empty((0, self.down[0].shape[1]))
-        raise ValueError("more tokens or wider rows than one launch takes: use step()")
+        raise ValueError("more tokens or routes than one launch takes: use step()")
 
 
 class Fp8MoE:
@@ -380,8 +380,8 @@ class Fp8MoE:
     experts (weights as in Fp8MLP).  router [E, K] has the tokens' type or is FP32;
     bias, score, renormalize and scale are the gate's (gating.topk_gate).
 
-    step() of a few tokens (up to 16 whose activations fit shared memory,
-    nvfp4.nvfp4_fp8_moe_layer_workspace_bytes) runs in one launch.  More go through
+    step() of a few tokens (at most 32, and 256 routes) runs in one launch
+    (nvfp4.nvfp4_fp8_moe_layer).  More go through
     the router's product with FP32 logits, gating.topk_gate and Fp8MLP.step, whose
     gate_up product and expert rows are rounded to the tokens' type; the router's
     sums also have another order, which can change the choice between nearly equal
