@@ -739,8 +739,7 @@ nvfp4_status nvfp4_topk_gate_grad(const float* dweights, const void* logits, int
                                   uint32_t flags, float scale, void* dlogits, void* stream);
 
 /* ------------------------------------------------------------------------
- * A whole MoE layer for a few tokens, in one launch: router, gate, FP8 experts,
- * weighted sum.
+ * A whole MoE layer for a few tokens: router, gate, FP8 experts, weighted sum.
  *
  *   logits = x . router^T (FP32);  ids and weights by the gate (above)
  *   h = SiLU(xq . gate_e^T) * (xq . up_e^T),   out = sum_k weight_k * hq_k . down_e^T
@@ -757,13 +756,12 @@ nvfp4_status nvfp4_topk_gate_grad(const float* dweights, const void* logits, int
  *            ceil(K / 128)];  W2, s2: down codes [E, N, I], scales likewise
  *   topk_ids, topk_weights  int32 and FP32 [T, topk]; outputs with a router
  *   out      [T, N] of x's type, row stride ldo
- * K % 16 == 0, I % 16 == 0.  T <= 32, T * topk <= 256, topk <= min(E, 32), E <= 1024,
- * K, I and N <= 2^20: nvfp4_fp8_moe_layer_workspace_bytes is 0 for sizes that this
+ * K % 16 == 0, I % 16 == 0.  T <= 8, topk <= min(E, 32), E <= 1024, K, I and N
+ * <= 2^20: nvfp4_fp8_moe_layer_workspace_bytes is 0 for sizes that this
  * call refuses as NVFP4_ERR_UNSUPPORTED.  workspace: 16-byte aligned, of that many
- * bytes, overwritten; calls that may overlap need one each.  A cooperative launch
- * (its blocks meet at barriers): it waits until every SM has room for a block.
- * The waits of a block on its own copies and products are bounded: one that runs out
- * records NVFP4_ERR_TIMEOUT in the device status word.
+ * bytes, overwritten; calls that may overlap need one each.  Two launches, the second
+ * overlapping the first.  All waits inside are bounded: one that runs out records
+ * NVFP4_ERR_TIMEOUT in the device status word.
  * ------------------------------------------------------------------------ */
 size_t nvfp4_fp8_moe_layer_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I,
                                            int64_t N);

@@ -1660,19 +1660,20 @@ nvfp4_status nvfp4_fp8_moe_layer(const void* x, int64_t ld, int64_t T, int32_t d
   a.ld_hq = m.ld_hq;
   a.hs = reinterpret_cast<float*>(ws + m.hs);
   a.part = reinterpret_cast<float*>(ws + m.part);
-  a.arrived = reinterpret_cast<uint32_t*>(ws + m.arrived);
+  a.counters = reinterpret_cast<uint32_t*>(ws + m.counters);
   a.items1 = static_cast<int32_t>(m.experts * ((I + 127) / 128));
+  a.experts = m.experts;
   a.status = d->status;
   a.timeout_ns = g_timeout_ns.load();
   CUtensorMap t1, t2, tx, th;
-  const uint32_t box = static_cast<uint32_t>(nvfp4::fp8_moe_box_rows(m.columns));
+  const uint32_t box = static_cast<uint32_t>(nvfp4::fp8_moe_box_rows());
   if (make_fp8_map(&t1, W1, K, K, I, 2 * static_cast<uint64_t>(E), 128, 3) != NVFP4_OK ||
       make_fp8_map(&t2, W2, I, I, N, E, 128, 3) != NVFP4_OK ||
       make_fp8_map(&tx, a.xq, K, m.ld_xq, m.columns, 1, box, 2) != NVFP4_OK ||
       make_fp8_map(&th, a.hq, I, m.ld_hq, static_cast<uint64_t>(m.experts) * m.columns, 1, box,
                    2) != NVFP4_OK)
     return NVFP4_ERR_UNSUPPORTED;
-  return launched(nvfp4::launch_fp8_moe(t1, t2, tx, th, a, m.columns, d->sms,
+  return launched(nvfp4::launch_fp8_moe(t1, t2, tx, th, a, d->sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -531,7 +531,7 @@ PyObject* topk_gate_grad(PyObject* const* a) {
 
 // moe_layer(x, router | None, gate_up, gate_up_scale, down, down_scale, topk, bias | None,
 //           sigmoid, renormalize, scale, ids | None, weights | None)
-//   -> (out, ids, weights), or None for sizes that the call does not take
+//   -> (out, ids, weights), or None for more tokens than the call takes
 PyObject* moe_layer(PyObject* const* a) {
   Tensor x = tensor(a[0], "x: expected a tensor");
   const Tensor& w1 = tensor(a[2], "gate_up: expected a tensor");

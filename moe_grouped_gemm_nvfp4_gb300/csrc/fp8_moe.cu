@@ -1,4 +1,4 @@
-// A whole MoE layer for a few tokens (up to 32) over FP8 experts, in one launch:
+// A whole MoE layer for a few tokens (up to 8) over FP8 experts:
 //
 //   l = x . router^T;  experts e_tk and weights w_tk by the top-k gate (gate.cuh)
 //   h_tk = SiLU(xq . gate_e^T) * (xq . up_e^T),   out_t = sum_k w_tk hq_tk . down_e^T
@@ -8,22 +8,28 @@
 //
 // Bound: the chosen experts' bytes (HBM).  The design serves that stream:
 //
-// * One block per SM (a cooperative launch).  The blocks meet at two grid barriers: when
-//   the logits and the codes of x are written, and when the codes of h are.
-// * Weights are the MMA's 128 rows (tcgen05, M 128), the tokens its 16 or 32 columns: all
+// * Two launches.  The first, small one writes the logits (router rows spread over the
+//   blocks) and the codes of x; the second is launched to overlap it and waits for it with
+//   its set-up done.  Every block of the second makes the choice for itself.
+// * Weights are the MMA's 128 rows (tcgen05, M 128), the tokens half of its 16 columns: all
 //   tokens, so that nothing is gathered; an expert's columns of other tokens are dropped.
 //   A tile is 256 weight rows x 128 K (32 KB, two TMA boxes): the gate and up rows of 128
 //   columns of h, so that one thread holds both factors of its h, or 256 down rows.
 //   Rows past a matrix read as zeros.
 // * The tiles of a phase stand in one line (gate_up: expert, 128 columns, K block; down:
-//   256 columns, expert, K block) that is cut into equal runs, one a block, wherever that
-//   falls: a token's eight experts have some thousands of tiles, and every SM streams the
-//   same bytes.  An item (128 columns of one expert's h; 256 output columns over all
-//   experts) whose tiles lie in several blocks is joined by the last of them to finish,
-//   which adds the parts in block order.
+//   256 columns, expert, K block) that is cut into equal runs, as many as blocks, wherever
+//   that falls: a token's eight experts have some thousands of tiles, and every SM streams
+//   the same bytes.  An item (128 columns of one expert's h; 256 output columns over all
+//   experts) whose tiles lie in several runs is joined by the last run to finish, which
+//   adds the parts in the order of the runs.
+// * Blocks take runs by a counter, all of gate_up's before the first of down's, and a down
+//   run waits (bounded) until all gate_up runs are done.  Those are then in the hands of
+//   blocks that run, so that no block has to wait for one that has not started: a plain
+//   launch, whatever else is on the GPU.  (As one cooperative launch with grid barriers a
+//   call took 9 us more: its launch, and every SM waiting for the slowest one twice.)
 // * Six stages are on their way (192 KB an SM).  When a block has asked for all its gate_up
-//   tiles, its producer goes on with the weights of its first down tiles, before the grid
-//   barrier that the codes of h wait for: HBM does not idle there.
+//   tiles, its producer takes its down run and goes on with the weights of the first down
+//   tiles, before it waits for the codes of h: HBM does not idle there.
 // * Both scales differ by K block, so every K block has accumulators of its own in tensor
 //   memory, which four warps read and add as FP32 times the factor (weight scale * token
 //   scale, for down also * routing weight) that a warp of its own lays out.
@@ -31,13 +37,9 @@
 // (A first form with mma.sync, eight warps with rings of their own: it spent 280
 // instructions on 2 KB of weights, converting codes, and reached 4.3 TB/s: one token
 // through 128 experts of 6144 x 2048, eight of them chosen, in 96 us.)
-#include <cooperative_groups.h>
-
 #include "fp8_common.cuh"
 #include "fp8_moe.h"
 #include "fp8_quant.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace nvfp4 {
 
@@ -46,22 +48,19 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroupBytes = 128 * 128;      // 128 weight rows of a K block
-constexpr int kAccBufs = 8;                 // of 2 x 16 or 2 x 32 columns
+constexpr int kAccBufs = 8;                 // of 2 x 16 columns
 
-// TB: token columns (8, 16 or 32).
-template <int TB>
-struct Shape {
-  static constexpr int kCols = TB < 16 ? 16 : TB;           // of the MMA
-  static constexpr int kStages = TB == 32 ? 5 : 6;
-  static constexpr int kTokOffset = 2 * kGroupBytes;
-  static constexpr int kStageBytes = kTokOffset + kCols * 128;
-  static constexpr int kFacOffset = kStages * kStageBytes;  // [bufs][3][TB] floats
-  static constexpr int kRedOffset = kFacOffset + kAccBufs * 3 * TB * 4;   // [4][TB] maxima
-  static constexpr int kBarOffset = kRedOffset + 4 * TB * 4;
-  static constexpr int kCtlOffset = kBarOffset + 8 * (2 * kStages + 2 * kAccBufs + 2);
-  static constexpr int kSmemBytes = kCtlOffset + 32 + 1024;
-  static constexpr uint32_t kTmemCols = kAccBufs * 2 * kCols;             // 256 or 512
-};
+constexpr int TB = kMoeMaxTokens;           // token columns that are read
+constexpr int kCols = 16;                   // of the MMA: its fewest
+constexpr int kStages = 6;
+constexpr int kTokOffset = 2 * kGroupBytes;
+constexpr int kStageBytes = kTokOffset + kCols * 128;
+constexpr int kFacOffset = kStages * kStageBytes;           // [bufs][3][TB] floats
+constexpr int kRedOffset = kFacOffset + kAccBufs * 3 * TB * 4;   // [4][TB] maxima
+constexpr int kBarOffset = kRedOffset + 4 * TB * 4;
+constexpr int kCtlOffset = kBarOffset + 8 * (2 * kStages + 2 * kAccBufs + 6);
+constexpr int kSmemBytes = kCtlOffset + 32 + 1024;
+constexpr uint32_t kTmemCols = kAccBufs * 2 * kCols;
 
 // The distinct experts in order of first appearance, and each one's routes.
 struct Routes {
@@ -89,13 +88,20 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
+__device__ __forceinline__ void ld_shared8(uint32_t addr, float (&f)[8]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]) : "r"(addr + 16) : "memory");
+}
+
 // Uses of r stay behind the wait for its load (volatile statements keep their order).
 __device__ __forceinline__ void keep_after(uint32_t (&r)[8]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
                     "+r"(r[6]), "+r"(r[7]));
 }
 
-// One phase's line of tiles and the block's run of it.
+// One phase's line of tiles, cut into runs.
 struct Phase {
   int down;
   int nkb;                                  // K blocks of an item's expert
@@ -103,22 +109,23 @@ struct Phase {
   int experts;
   int per_item;                             // tiles of an item
   int grain, grains;                        // runs begin at multiples of `grain` tiles
-  int parts;                                // blocks that have tiles
-  int first, count;                         // the block's run
+  int parts;                                // runs
 
-  __device__ __forceinline__ int begin(int block) const {
-    return grain * static_cast<int>(static_cast<int64_t>(grains) * block / parts);
+  // (the host refuses sizes whose tiles times runs pass 32 bits)
+  __device__ __forceinline__ int begin(int run) const {
+    return grain * static_cast<int>(static_cast<uint32_t>(grains) * run / static_cast<uint32_t>(parts));
   }
-  // The block whose run holds a tile.
+  // The run that holds a tile.
   __device__ __forceinline__ int owner(int tile) const {
-    return static_cast<int>(((static_cast<int64_t>(tile / grain) + 1) * parts - 1) / grains);
+    return static_cast<int>(((static_cast<uint32_t>(tile) / grain + 1) * parts - 1) /
+                            static_cast<uint32_t>(grains));
   }
   // Runs of whole items need no join, which takes about 4 us behind the last tile; runs of
   // single tiles are all equally long.  A tile takes 0.76 us while all SMs draw on HBM and
   // at least 0.53 us (62 GB/s is all that one SM draws); a join 5 tiles' time.  At most about
-  // eight blocks share an item: the last one reads all parts.
+  // eight runs share an item: the last one reads all parts.
   __device__ __forceinline__ void set(int is_down, int k_blocks, int n_units, int n_experts) {
-    const int blocks = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+    const int blocks = static_cast<int>(gridDim.x);
     down = is_down;
     nkb = k_blocks;
     units = n_units;
@@ -126,14 +133,20 @@ struct Phase {
     per_item = max(down ? nkb * experts : nkb, 1);
     const int items = down ? units * min(experts, 1) : units * experts;
     const int rest = items % blocks;
-    const int64_t rounds = 100 * (items / blocks) + (rest ? max(70, 100 * rest / blocks) : 0);
-    const bool whole = rounds * per_item <= 100 * static_cast<int64_t>(items) * per_item / blocks + 500;
+    // (in floating point: the products can pass 32 bits)
+    const float rounds = static_cast<float>(items / blocks) +
+                         (rest ? fmaxf(0.7f, static_cast<float>(rest) / blocks) : 0.f);
+    const bool whole = rounds * per_item <= static_cast<float>(items) * per_item / blocks + 5.f;
     grain = whole ? per_item : 1;
     grains = whole ? items : items * per_item;
     parts = min(blocks, min(grains, 8 * items));
-    first = b < parts ? begin(b) : 0;
-    count = b < parts ? begin(b + 1) - first : 0;
   }
+};
+
+// A run that the block has taken.
+struct Run {
+  int phase;                                // 2: no more
+  int number, first, count;
 };
 
 // A tile of the line: live expert, unit, K block.
@@ -162,33 +175,85 @@ struct Cursor {
 };
 
 // Shared memory of a block.
-template <int TB>
 struct Block {
-  using S = Shape<TB>;
   uint32_t base;
   uint8_t* smem;
   CtaCtl* ctl;
   int* status;
   uint32_t tmem;
-  __device__ __forceinline__ uint32_t stage(int s) const { return base + s * S::kStageBytes; }
-  __device__ __forceinline__ uint32_t bar(int i) const { return base + S::kBarOffset + 8u * i; }
+  __device__ __forceinline__ uint32_t stage(int s) const { return base + s * kStageBytes; }
+  __device__ __forceinline__ uint32_t bar(int i) const { return base + kBarOffset + 8u * i; }
   __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
-  __device__ __forceinline__ uint32_t empty(int s) const { return bar(S::kStages + s); }
-  __device__ __forceinline__ uint32_t accf(int b) const { return bar(2 * S::kStages + b); }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bar(kStages + s); }
+  __device__ __forceinline__ uint32_t accf(int b) const { return bar(2 * kStages + b); }
   __device__ __forceinline__ uint32_t acce(int b) const {
-    return bar(2 * S::kStages + kAccBufs + b);
+    return bar(2 * kStages + kAccBufs + b);
   }
-  __device__ __forceinline__ uint32_t drain() const { return bar(2 * S::kStages + 2 * kAccBufs); }
+  __device__ __forceinline__ uint32_t drain() const { return bar(2 * kStages + 2 * kAccBufs); }
   __device__ __forceinline__ uint32_t meet() const {
-    return bar(2 * S::kStages + 2 * kAccBufs + 1);
+    return bar(2 * kStages + 2 * kAccBufs + 1);
+  }
+  __device__ __forceinline__ uint32_t run_given(int i) const {
+    return bar(2 * kStages + 2 * kAccBufs + 2 + i);
+  }
+  __device__ __forceinline__ uint32_t run_taken(int i) const {
+    return bar(2 * kStages + 2 * kAccBufs + 4 + i);
   }
   __device__ __forceinline__ float* fac(int b) const {
-    return reinterpret_cast<float*>(smem + S::kFacOffset) + b * 3 * TB;
+    return reinterpret_cast<float*>(smem + kFacOffset) + b * 3 * TB;
+  }
+  __device__ __forceinline__ uint32_t fac_at(int i) const {
+    return base + kFacOffset + i * 3 * TB * 4;
   }
   __device__ __forceinline__ float* red() const {
-    return reinterpret_cast<float*>(smem + S::kRedOffset);
+    return reinterpret_cast<float*>(smem + kRedOffset);
   }
 };
+
+// What the roles of a block wait on for their next run: the producer takes it, the MMA's
+// lane, the factors' warp and the four warps of the epilogue each read it once.
+constexpr int kRunReaders = 6;
+
+struct Runs {
+  const Block& b;
+  Run* slots;                               // [2]
+  uint32_t n = 0;
+  __device__ __forceinline__ bool give(const Run& r) {
+    if (!wait_soon(b.run_taken(n & 1u), (n >> 1 & 1u) ^ 1u, b.ctl, b.status)) return false;
+    slots[n & 1u] = r;
+    mbar_arrive(b.run_given(n & 1u));
+    ++n;
+    return true;
+  }
+  // `whole`: by all lanes of a warp.
+  __device__ __forceinline__ bool take(Run* r, bool whole) {
+    bool ok = wait_soon(b.run_given(n & 1u), n >> 1 & 1u, b.ctl, b.status);
+    if (whole) ok = __all_sync(kFullWarp, ok);
+    if (!ok) return false;
+    *r = slots[n & 1u];
+    if (whole) __syncwarp();
+    if (!whole || (threadIdx.x & 31) == 0) mbar_arrive(b.run_taken(n & 1u));
+    ++n;
+    return true;
+  }
+};
+
+// Waits (acquire) until *p >= target; bounded like the other waits.
+__device__ __forceinline__ bool wait_runs(const uint32_t* p, uint32_t target, CtaCtl* ctl,
+                                          int* status) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 0; i < 0x7FFFFFFFu; ++i) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    if (v >= target) return true;
+    if (*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) return false;
+    if (globaltimer() - t0 > ctl->timeout_ns) break;
+    __nanosleep(32);
+  }
+  *reinterpret_cast<volatile uint32_t*>(&ctl->abort) = 1u;
+  raise_status(status, NVFP4_ERR_TIMEOUT);
+  return false;
+}
 
 // Counts a role's passes over a ring of n slots.
 struct Ring {
@@ -201,18 +266,16 @@ struct Ring {
 
 // ------------------------------------------------------------------ producer
 
-template <int TB>
 struct Producer {
-  const Block<TB>& b;
+  const Block& b;
   const Routes& rt;
   const CUtensorMap* w;
   const CUtensorMap* tok;
   uint64_t wpol, tpol;
 
   __device__ __forceinline__ void weights(const Phase& p, const Cursor& c, int s) const {
-    using S = Shape<TB>;
-    const int e = rt.live[c.x];
-    mbar_arrive_expect_tx(b.full(s), S::kStageBytes);
+      const int e = rt.live[c.x];
+    mbar_arrive_expect_tx(b.full(s), kStageBytes);
     if (p.down) {
       tma_load_3d(b.stage(s), w, b.full(s), c.kb * 128, c.unit * 256, e, wpol);
       tma_load_3d(b.stage(s) + kGroupBytes, w, b.full(s), c.kb * 128, c.unit * 256 + 128, e, wpol);
@@ -223,7 +286,7 @@ struct Producer {
     }
   }
   __device__ __forceinline__ void tokens(const Phase& p, const Cursor& c, int s) const {
-    tma_load_2d(b.stage(s) + Shape<TB>::kTokOffset, tok, b.full(s), c.kb * 128,
+    tma_load_2d(b.stage(s) + kTokOffset, tok, b.full(s), c.kb * 128,
                 p.down ? c.x * TB : 0, tpol);
   }
 };
@@ -233,12 +296,11 @@ struct Producer {
 // One warp: for each tile the products of the weight scales (gate or first 128 rows; up
 // or second 128 rows, whose scale can change within the 128 rows where I is no multiple
 // of 128) and of each token's scale (times its routing weight in the down phase).
-template <int TB>
-__device__ __forceinline__ void factors(const Block<TB>& b, const Fp8MoeArgs& a, const Routes& rt,
-                                        const Phase& p, Ring& acc) {
+__device__ __forceinline__ void factors(const Block& b, const Fp8MoeArgs& a, const Routes& rt,
+                                        const Phase& p, const Run& run, Ring& acc) {
   const int lane = threadIdx.x & 31;
   Cursor c;
-  c.at(p, p.first);
+  c.at(p, run.first);
   const float* ws = p.down ? a.s2 : a.s1;
   const int nnb = p.down ? (a.N + 127) / 128 : (2 * a.I + 127) / 128;
   int x = -1;
@@ -262,9 +324,9 @@ __device__ __forceinline__ void factors(const Block<TB>& b, const Fp8MoeArgs& a,
     r.tok = lane < TB && lane < a.T ? __ldcg(ts + lane) : 0.f;
     return r;
   };
-  Raw next{};
-  if (p.count > 0) next = load(c);
-  for (int i = 0; i < p.count; ++i) {
+  Raw next = load(c);
+#pragma unroll 1
+  for (int i = 0; i < run.count; ++i) {
     const Raw r = next;
     if (p.down && c.x != x) {
       x = c.x;
@@ -273,8 +335,9 @@ __device__ __forceinline__ void factors(const Block<TB>& b, const Fp8MoeArgs& a,
       weight = tokens >> lane & 1u ? rt.weight[rt.route[j]] : 0.f;
     }
     c.next(p);
-    if (i + 1 < p.count) next = load(c);
-    if (!__all_sync(kFullWarp, wait_soon(b.acce(acc.slot), acc.phase ^ 1u, b.ctl, b.status))) return;
+    if (i + 1 < run.count) next = load(c);
+    if (!__all_sync(kFullWarp, wait_soon(b.acce(acc.slot), acc.phase ^ 1u, b.ctl, b.status)))
+      return;
     if (lane < TB) {
       float* f = b.fac(acc.slot);
       // the weight's scale first: the product with the token's stays in the result's range
@@ -292,9 +355,8 @@ __device__ __forceinline__ void factors(const Block<TB>& b, const Fp8MoeArgs& a,
 
 // Four warps: thread r holds rows r and r + 128 of the tile (gate and up row of column
 // r of the unit, or two output columns) for all tokens.
-template <int TB>
 struct Epilogue {
-  const Block<TB>& b;
+  const Block& b;
   const Fp8MoeArgs& a;
   const Routes& rt;
   int r;                                    // 0 .. 127
@@ -308,35 +370,40 @@ struct Epilogue {
     return __all_sync(kFullWarp, ok);
   }
 
-  // h of the unit's column r for the expert's tokens, quantised over the unit's columns.
-  __device__ __forceinline__ bool finish_h(int x, int unit, const float (&g)[TB],
-                                           const float (&u)[TB]) {
-    const int col = unit * 128 + r, warp = r >> 5, lane = r & 31;
-    const uint32_t tokens = rt.tokens[x];
-    const int nkb = (a.I + 127) / 128;
-    float h[TB];
+  // h of the unit's column r for one of the expert's tokens.
+  __device__ __forceinline__ float h_of(const float (&g)[TB], const float (&u)[TB], int token,
+                                        bool in) const {
+    float gate = 0.f, up = 0.f;
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      h[t] = 0.f;
-      if (tokens >> t & 1u) {
-        if (col < a.I) h[t] = g[t] / (1.f + __expf(-g[t])) * u[t];
-        // magnitudes order as integers; a NaN counts as nothing
-        const float m = fmaxf(fabsf(h[t]), 0.f);
-        const uint32_t top = __reduce_max_sync(kFullWarp, __float_as_uint(m));
-        if (lane == 0) b.red()[warp * TB + t] = __uint_as_float(top);
-      }
+    for (int t = 0; t < TB; ++t)
+      if (t == token) { gate = g[t]; up = u[t]; }
+    return in ? gate / (1.f + __expf(-gate)) * up : 0.f;
+  }
+  // The unit's columns of h for the expert's tokens, quantised together.  (A loop over the
+  // tokens: unrolled, its instructions took longer to fetch than to run.)
+  __device__ __forceinline__ bool finish_h(int x, int unit, uint32_t tokens, const float (&g)[TB],
+                                           const float (&u)[TB]) {
+    const int col = unit * 128 + r, warp = r >> 5;
+    const bool in = col < a.I;
+#pragma unroll 1
+    for (uint32_t m = tokens; m; m &= m - 1) {
+      const int t = __ffs(m) - 1;
+      // magnitudes order as integers; a NaN counts as nothing
+      const float top = fmaxf(fabsf(h_of(g, u, t, in)), 0.f);
+      const uint32_t most = __reduce_max_sync(kFullWarp, __float_as_uint(top));
+      if ((r & 31) == 0) b.red()[warp * TB + t] = __uint_as_float(most);
     }
     if (!meet()) return false;
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      if (tokens >> t & 1u) {
-        const float* m = b.red() + t;
-        const BlockScale32 s(fmaxf(fmaxf(m[0], m[TB]), fmaxf(m[2 * TB], m[3 * TB])));
-        if (col < a.I)
-          a.hq[(static_cast<int64_t>(x) * TB + t) * a.ld_hq + col] =
-              static_cast<uint8_t>(e4m3x4(s.quotient(h[t]), 0.f, 0.f, 0.f));
-        if (r == 0) __stcg(a.hs + (static_cast<int64_t>(x) * nkb + unit) * TB + t, s.scale);
-      }
+#pragma unroll 1
+    for (uint32_t m = tokens; m; m &= m - 1) {
+      const int t = __ffs(m) - 1;
+      const float* top = b.red() + t;
+      const BlockScale32 s(fmaxf(fmaxf(top[0], top[TB]), fmaxf(top[2 * TB], top[3 * TB])));
+      if (in)
+        a.hq[(static_cast<int64_t>(x) * TB + t) * a.ld_hq + col] =
+            static_cast<uint8_t>(e4m3x4(s.quotient(h_of(g, u, t, in)), 0.f, 0.f, 0.f));
+      if (r == 0)
+        __stcg(a.hs + (static_cast<int64_t>(x) * ((a.I + 127) / 128) + unit) * TB + t, s.scale);
     }
     return meet();                          // the maxima have been read
   }
@@ -353,24 +420,23 @@ struct Epilogue {
     }
   }
 
-  // The block's tiles of an item are added up: the item is finished here, or by the last
-  // block to come with its part.
-  __device__ __forceinline__ bool finish(const Phase& p, int item, bool whole, float (&v)[TB],
-                                         float (&w)[TB]) {
-    const int x = p.down ? 0 : item / p.units;
-    const int unit = p.down ? item : item % p.units;
+  // A run's tiles of an item are added up: the item is finished here, or by the last run to
+  // come with its part.
+  __device__ __forceinline__ bool finish(const Phase& p, const Run& run, int item, int x, int unit,
+                                         bool whole, float (&v)[TB], float (&w)[TB]) {
     if (!whole) {
       const int c0 = p.owner(item * p.per_item), c1 = p.owner((item + 1) * p.per_item - 1);
-      // A block's first item is its part 0, its last one (if another) its part 1: of an
-      // item's blocks only the first can have begun with another.
+      // A run's first item is its part 0, its last one (if another) its part 1: of an
+      // item's runs only the first can have begun with another.
       const int other = p.begin(c0) / p.per_item == item ? 0 : 1;
-      auto part = [&](int block) {
-        return a.part + (2 * block + (block == c0 ? other : 0)) * (2 * TB * 128) + r;
+      auto part = [&](int number) {
+        return a.part + (2 * number + (number == c0 ? other : 0)) * (2 * TB * 128) + r;
       };
-      float* mine = part(static_cast<int>(blockIdx.x));
+      float* mine = part(run.number);
+      const uint32_t tokens = p.down ? (1u << a.T) - 1u : rt.tokens[x];
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        if (t < a.T) {
+        if (tokens >> t & 1u) {
           __stcg(mine + t * 128, v[t]);
           __stcg(mine + (TB + t) * 128, w[t]);
         }
@@ -381,13 +447,13 @@ struct Epilogue {
       if (p.down) {
         // output columns stand alone: the last of each warp's 64
         __syncwarp();
-        if ((r & 31) == 0) before = atomicAdd(a.arrived + a.items1 + 4 * item + (r >> 5), 1u);
+        if ((r & 31) == 0) before = atomicAdd(a.counters + 4 + a.items1 + 4 * item + (r >> 5), 1u);
         before = __shfl_sync(kFullWarp, before, 0);
       } else {
         // a block of h is quantised together
         if (!meet()) return false;
         uint32_t* said = reinterpret_cast<uint32_t*>(b.red());
-        if (r == 0) *said = atomicAdd(a.arrived + item, 1u);
+        if (r == 0) *said = atomicAdd(a.counters + 4 + item, 1u);
         if (!meet()) return false;
         before = *said;
         if (!meet()) return false;          // it has been read
@@ -396,8 +462,8 @@ struct Epilogue {
       __threadfence();
 #pragma unroll
       for (int t = 0; t < TB; ++t) v[t] = w[t] = 0.f;
-      // the parts in block order, 64 reads on their way (a read takes about 0.7 us)
-      constexpr int kTogether = 32 / TB;
+      // the parts in the order of the runs, 64 reads on their way (a read takes about 0.7 us)
+      constexpr int kTogether = 4;
 #pragma unroll 1
       for (int c = c0; c <= c1; c += kTogether) {
         float pv[kTogether][TB], pw[kTogether][TB];
@@ -406,8 +472,8 @@ struct Epilogue {
           const float* q = part(min(c + i, c1));
 #pragma unroll
           for (int t = 0; t < TB; ++t) {
-            pv[i][t] = t < a.T ? __ldcg(q + t * 128) : 0.f;
-            pw[i][t] = t < a.T ? __ldcg(q + (TB + t) * 128) : 0.f;
+            pv[i][t] = tokens >> t & 1u ? __ldcg(q + t * 128) : 0.f;
+            pw[i][t] = tokens >> t & 1u ? __ldcg(q + (TB + t) * 128) : 0.f;
           }
         }
 #pragma unroll
@@ -423,54 +489,62 @@ struct Epilogue {
       finish_out(unit, v, w);
       return true;
     }
-    return finish_h(x, unit, v, w);
+    return finish_h(x, unit, x < rt.n_live ? rt.tokens[x] : 1u, v, w);
   }
 
-  __device__ __forceinline__ bool run(const Phase& p, Ring& acc) {
-    using S = Shape<TB>;
-    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(r >> 5) << 21);
+  __device__ __forceinline__ bool add(const Phase& p, const Run& run, Ring& acc, bool warm) {
+      const uint32_t lanes = b.tmem + (static_cast<uint32_t>(r >> 5) << 21);
     Cursor c;
-    c.at(p, p.first);
-    int item = p.first / p.per_item, inner = p.first - item * p.per_item;
+    c.at(p, run.first);
+    int item = run.first / p.per_item, inner = run.first - item * p.per_item;
     bool from_start = inner == 0;
     float v[TB], w[TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t) v[t] = w[t] = 0.f;
-    for (int i = 0; i < p.count; ++i) {
-      const bool ok = wait_soon(b.accf(acc.slot), acc.phase, b.ctl, b.status);
-      if (!__all_sync(kFullWarp, ok)) return false;
-      tc_fence_after();
-      // which of the two scales of the second group: rows past a multiple of 128
-      const int second =
-          !p.down && (a.I + c.unit * 128 + r) / 128 != (a.I + c.unit * 128) / 128 ? 2 : 1;
-      const uint32_t tokens = p.down ? rt.tokens[c.x] : ~0u;
-      const float* f0 = b.fac(acc.slot);
-      const float* f1 = f0 + second * TB;
-#pragma unroll
-      for (int t0 = 0; t0 < TB; t0 += 8) {
-        uint32_t d[8], e[8];
-        tmem_ld8(lanes + acc.slot * 2 * S::kCols + t0, d);
-        tmem_ld8(lanes + acc.slot * 2 * S::kCols + S::kCols + t0, e);
+    // Step -1 (warm), while the first weights are on their way: an item of zeros for an
+    // expert that is none, so that what ends an item is in the instruction cache when the
+    // first one does (5 us behind the last tile otherwise).
+#pragma unroll 1
+    for (int i = warm ? -1 : 0; i < run.count; ++i) {
+      if (i >= 0) {
+        const bool ok = wait_soon(b.accf(acc.slot), acc.phase, b.ctl, b.status);
+        if (!__all_sync(kFullWarp, ok)) return false;
+        tc_fence_after();
+        // which of the two scales of the second group: rows past a multiple of 128
+        const int second =
+            !p.down && (a.I + c.unit * 128 + r) / 128 != (a.I + c.unit * 128) / 128 ? 2 : 1;
+        const uint32_t f0 = b.fac_at(acc.slot), f1 = f0 + 4 * second * TB;
+        const uint32_t tokens = rt.tokens[c.x];
+        uint32_t d[TB], e[TB];
+        tmem_ld8(lanes + acc.slot * 2 * kCols, d);
+        tmem_ld8(lanes + acc.slot * 2 * kCols + kCols, e);
+        float fd[TB], fe[TB];
+        ld_shared8(f0, fd);
+        ld_shared8(f1, fe);
         tmem_ld_wait();
         keep_after(d);
         keep_after(e);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          // a token that the expert does not have brings codes of no meaning
-          if (tokens >> (t0 + t) & 1u) {
-            v[t0 + t] = fmaf(__uint_as_float(d[t]), f0[t0 + t], v[t0 + t]);
-            w[t0 + t] = fmaf(__uint_as_float(e[t]), f1[t0 + t], w[t0 + t]);
+        for (int t = 0; t < TB; ++t) {
+          // the columns of other tokens: in the down phase products with codes of no meaning
+          if (tokens >> t & 1u) {
+            v[t] = fmaf(__uint_as_float(d[t]), fd[t], v[t]);
+            w[t] = fmaf(__uint_as_float(e[t]), fe[t], w[t]);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(b.acce(acc.slot));
+        acc.next(kAccBufs);
+        c.next(p);
+        ++inner;
       }
-      tc_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(b.acce(acc.slot));
-      acc.next(kAccBufs);
-      c.next(p);
-      if (++inner == p.per_item || i + 1 == p.count) {
-        if (!finish(p, item, from_start && inner == p.per_item, v, w)) return false;
-        if (inner == p.per_item) {
+      if (i < 0 || inner == p.per_item || i + 1 == run.count) {
+        const int x = i < 0 ? a.experts : p.down ? 0 : item / p.units;
+        const int unit = i < 0 ? 0 : p.down ? item : item - x * p.units;
+        if (!finish(p, run, item, x, unit, i < 0 || (from_start && inner == p.per_item), v, w))
+          return false;
+        if (i >= 0 && inner == p.per_item) {
           inner = 0;
           ++item;
           from_start = true;
@@ -479,72 +553,71 @@ struct Epilogue {
         for (int t = 0; t < TB; ++t) v[t] = w[t] = 0.f;
       }
     }
+    if (!p.down) {
+      // the run is done: its codes of h are read by TMA and by other blocks
+      fence_proxy_async_global();
+      __threadfence();
+      if (!meet()) return false;
+      if (r == 0)
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" :: "l"(a.counters + 2) : "memory");
+    }
     return true;
   }
 };
 
-// Logits of the block's experts: the threads share K, the weights' loads are issued
-// together and a token's ahead of the one before it.
-template <int DT, int RT, int TB>
-__device__ __forceinline__ void router_logits(const Fp8MoeArgs& a, float (*part)[TB]) {
+// Logits, a router's row and up to four tokens at a time: the threads share K, three
+// 8-element chunks each, with the loads of the row and of the tokens on their way together.
+template <int DT, int RT>
+__device__ __forceinline__ void router_logits(const Fp8MoeArgs& a, float (*part)[4]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kChunks = 4, kPass = kThreads * 8 * kChunks;
-  const int k0 = threadIdx.x * 8;
-  for (int e = blockIdx.x; e < a.rule.E; e += gridDim.x) {
-    for (int from = 0; from < a.K; from += kPass) {
-      Pack<DT, 8> x[kChunks];
-      float w[kChunks][8];
-      auto load = [&](int t) {
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int k = from + k0 + c * kThreads * 8;
-          x[c].zero();
-          if (k < a.K && t < a.T) x[c].load(a.x, t * a.ld + k);
-        }
-      };
-      load(0);
+  constexpr int kChunks = 3, kTogether = 4, N = elems_per_16b<RT>();
+  const int sets = (a.T + kTogether - 1) / kTogether;
+  for (int i = blockIdx.x; i < a.rule.E * sets; i += gridDim.x) {
+    const int e = i % a.rule.E, t0 = i / a.rule.E * kTogether;
+    float sum[kTogether] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int from = threadIdx.x * 8; from < a.K; from += kThreads * 8 * kChunks) {
+      Pack<RT, N> w[kChunks][8 / N];
+      Pack<DT, 8> x[kTogether][kChunks];
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        const int k = from + k0 + c * kThreads * 8;
-        const int64_t at = static_cast<int64_t>(e) * a.K + k;
-        if constexpr (RT == NVFP4_FP32) {
-          Pack<NVFP4_FP32, 4> lo, hi;
-          lo.zero();
-          hi.zero();
-          if (k < a.K) { lo.load(a.router, at); hi.load(a.router, at + 4); }
+        const int k = from + c * kThreads * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) { w[c][i] = lo.get(i); w[c][4 + i] = hi.get(i); }
-        } else {
-          Pack<RT, 8> v;
-          v.zero();
-          if (k < a.K) v.load(a.router, at);
+        for (int j = 0; j < 8 / N; ++j) {
+          w[c][j].zero();
+          if (k < a.K) w[c][j].load(a.router, static_cast<int64_t>(e) * a.K + k + j * N);
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[c][i] = v.get(i);
+        for (int t = 0; t < kTogether; ++t) {
+          x[t][c].zero();
+          if (t0 + t < a.T && k < a.K) x[t][c].load(a.x, (t0 + t) * a.ld + k);
         }
       }
-#pragma unroll 1
-      for (int t = 0; t < a.T; ++t) {
-        float sum[kChunks];
-        Pack<DT, 8> now[kChunks];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) now[c] = x[c];
-        load(t + 1);
+      for (int t = 0; t < kTogether; ++t) {
+        if (t0 + t >= a.T) break;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          sum[c] = 0.f;
+          float dot = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[c] = fmaf(now[c].get(i), w[c][i], sum[c]);
+          for (int j = 0; j < 8; ++j) dot = fmaf(x[t][c].get(j), w[c][j / N].get(j % N), dot);
+          sum[t] += dot;
         }
-        const float v = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-        if (lane == 0) part[warp][t] = from == 0 ? v : part[warp][t] + v;
       }
     }
+#pragma unroll
+    for (int t = 0; t < kTogether; ++t) {
+      if (t0 + t >= a.T) break;
+      sum[t] = warp_sum(sum[t]);
+      if (lane == 0) part[warp][t] = sum[t];
+    }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < a.T) {
+    const int t = threadIdx.x;
+    if (t < kTogether && t0 + t < a.T) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
-      __stcg(a.logits + static_cast<int64_t>(threadIdx.x) * a.rule.E + e, v);
+      for (int w = 0; w < kWarps; ++w) v += part[w][t];
+      __stcg(a.logits + static_cast<int64_t>(t0 + t) * a.rule.E + e, v);
     }
     __syncthreads();
   }
@@ -628,7 +701,7 @@ __device__ __forceinline__ void list_experts(const Fp8MoeArgs& a, Routes& rt, ui
 // Rows of x as codes and scales in the workspace, spread over the grid's warps from the
 // last block on (the first ones have the router's experts).
 template <int DT>
-__device__ __forceinline__ void quantise_tokens(const Fp8MoeArgs& a, int columns) {
+__device__ __forceinline__ void quantise_tokens(const Fp8MoeArgs& a) {
   const int lane = threadIdx.x & 31;
   const int chunks = (a.K + 511) / 512;
   for (int i = (threadIdx.x >> 5) * gridDim.x + gridDim.x - 1 - blockIdx.x; i < a.T * chunks;
@@ -650,46 +723,51 @@ __device__ __forceinline__ void quantise_tokens(const Fp8MoeArgs& a, int columns
       qw[j] = e4m3x4(s.quotient(v[4 * j]), s.quotient(v[4 * j + 1]), s.quotient(v[4 * j + 2]),
                      s.quotient(v[4 * j + 3]));
     *reinterpret_cast<uint4*>(a.xq + t * a.ld_xq + k) = q;
-    if ((lane & 7) == 0) __stcg(a.xs + (k / kFp8Block) * columns + t, s.scale);
+    if ((lane & 7) == 0) __stcg(a.xs + (k / kFp8Block) * TB + t, s.scale);
   }
 }
 
-// What the first barrier waits for.
-template <int DT, int TB>
-__device__ __forceinline__ void before_gate(const Fp8MoeArgs& a, float (*part)[TB]) {
-  quantise_tokens<DT>(a, TB);
+// The first launch.
+template <int DT>
+__global__ void __maxnreg__(96) fp8_moe_router_kernel(const Fp8MoeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float part[kWarps][4];
+  const int counters = 4 + a.items1 + 4 * ((a.N + 255) / 256);
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < counters; i += gridDim.x * kThreads)
+    a.counters[i] = 0u;
+  quantise_tokens<DT>(a);
   if (!a.router) return;
-  if (a.router_type == NVFP4_FP32) router_logits<DT, NVFP4_FP32, TB>(a, part);
-  else router_logits<DT, DT, TB>(a, part);
+  if (a.router_type == NVFP4_FP32) router_logits<DT, NVFP4_FP32>(a, part);
+  else router_logits<DT, DT>(a, part);
 }
 
-template <int TB>
-__global__ void __launch_bounds__(kThreads, 1)
+// (registers: few enough that a block starts beside one of the first launch)
+__global__ void __maxnreg__(160)
 fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ CUtensorMap t2,
                const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap th,
                const __grid_constant__ Fp8MoeArgs a) {
-  using S = Shape<TB>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Routes rt;
-  __shared__ float part[kWarps][TB];
+  __shared__ Phase phase[2];
+  __shared__ Run run_slots[2];
   __shared__ int2 scan[kWarps];
   __shared__ uint32_t bits[kGateMaxExperts];
-  Block<TB> b;
+  Block b;
   b.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~static_cast<uintptr_t>(1023));
   b.base = smem_u32(b.smem);
-  b.ctl = reinterpret_cast<CtaCtl*>(b.smem + S::kCtlOffset);
+  b.ctl = reinterpret_cast<CtaCtl*>(b.smem + kCtlOffset);
   b.status = a.status;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b.smem + S::kCtlOffset + 16);
-  const int warp = threadIdx.x >> 5;
-  cg::grid_group grid = cg::this_grid();
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b.smem + kCtlOffset + 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units1 = (a.I + 127) / 128, units2 = (a.N + 255) / 256;
 
   if (threadIdx.x == 0) {
     prefetch_map(&t1);
     prefetch_map(&t2);
     prefetch_map(&tx);
     prefetch_map(&th);
-    for (int s = 0; s < S::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(b.full(s), 1);
       mbar_init(b.empty(s), 1);
     }
@@ -699,31 +777,27 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     }
     mbar_init(b.drain(), 1);
     mbar_init(b.meet(), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b.run_given(i), 1);
+      mbar_init(b.run_taken(i), kRunReaders);
+    }
     b.ctl->abort = 0;
     b.ctl->timeout_ns = a.timeout_ns;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), S::kTmemCols);
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  const int units1 = (a.I + 127) / 128, units2 = (a.N + 255) / 256;
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.items1 + 4 * units2;
-       i += gridDim.x * kThreads)
-    __stcg(a.arrived + i, 0u);
-  if (a.type == NVFP4_BF16) before_gate<NVFP4_BF16, TB>(a, part);
-  else before_gate<NVFP4_FP16, TB>(a, part);
-  fence_proxy_async_global();                   // the codes are read by TMA
   tc_fence_before();
-  grid.sync();
-  tc_fence_after();
-  b.tmem = *tmem_slot;
-
+  grid_dependency_wait();
+  uint32_t ticket = 0;
+  if (threadIdx.x == 0) ticket = atomicAdd(a.counters, 1u);     // on its way meanwhile
   if (a.router) {
-    for (int t = warp; t < a.T; t += kWarps) {
-      if (a.rule.E <= 128) gate_token<4>(a, rt, t);
-      else if (a.rule.E <= 256) gate_token<8>(a, rt, t);
-      else gate_token<32>(a, rt, t);
+    if (warp < a.T) {
+      if (a.rule.E <= 128) gate_token<4>(a, rt, warp);
+      else if (a.rule.E <= 256) gate_token<8>(a, rt, warp);
+      else gate_token<32>(a, rt, warp);
     }
   } else {
     const int r = threadIdx.x;
@@ -737,119 +811,117 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
   }
   __syncthreads();
   list_experts(a, rt, bits, scan);
-
-  Phase p1, p2;
-  p1.set(0, (a.K + 127) / 128, units1, rt.n_live);
-  p2.set(1, (a.I + 127) / 128, units2, rt.n_live);
-  const int early = min(S::kStages, p2.count);  // down tiles whose weights go ahead
+  if (warp == 0 && lane < 2)
+    phase[lane].set(lane, ((lane ? a.I : a.K) + 127) / 128, lane ? units2 : units1, rt.n_live);
+  __syncthreads();
+  tc_fence_after();
+  b.tmem = *tmem_slot;
+  Runs runs{b, run_slots};
   Ring ring, acc;
-  const uint32_t idesc = idesc_e4m3(128, S::kCols);
-  const bool lead = warp < 2 && elect_one();
-  Cursor c;
-  uint32_t issued = 0;
-  bool alive = true;
 
-  auto multiply = [&](const Phase& p) {
-    for (int i = 0; i < p.count && alive; ++i) {
-      if (!wait_both(b.acce(acc.slot), acc.phase ^ 1u, b.full(ring.slot), ring.phase, b.ctl,
-                     b.status)) {
-        alive = false;
-        break;
+  if (threadIdx.x == 0) {
+    // -------------------------------------------------------------- producer
+    const uint64_t wpol = l2_policy_evict_first(), tpol = l2_policy_evict_last();
+    fence_proxy_async_global();                 // the codes of x were written before
+    uint32_t issued = 0;
+    bool alive = true;
+    int ph = 0;
+#pragma unroll 1
+    while (alive) {
+      while (ph < 2 && ticket >= static_cast<uint32_t>(phase[ph].parts)) {
+        ++ph;
+        if (ph < 2) ticket = atomicAdd(a.counters + ph, 1u);
       }
-      tc_fence_after();
-      const uint32_t s = b.stage(ring.slot), d = b.tmem + acc.slot * 2 * S::kCols;
-      const uint64_t tok = sdesc_sw128(s + S::kTokOffset);
-      tc_mma_e4m3_k128(d, sdesc_sw128(s), tok, idesc);
-      tc_mma_e4m3_k128(d + S::kCols, sdesc_sw128(s + kGroupBytes), tok, idesc);
-      tc_commit(b.accf(acc.slot));
-      tc_commit(b.empty(ring.slot));
-      ring.next(S::kStages);
-      acc.next(kAccBufs);
-    }
-  };
-  Epilogue<TB> epi{b, a, rt, static_cast<int>(threadIdx.x) & 127};
-
-  // ------------------------------------------------------------------ gate_up
-  if (warp == 0) {
-    if (lead) {
-      fence_proxy_async_global();
-      const Producer<TB> first{b, rt, &t1, &tx, l2_policy_evict_first(), l2_policy_evict_last()};
-      c.at(p1, p1.first);
-      for (int i = 0; i < p1.count; ++i) {
-        if (!wait_soon(b.empty(ring.slot), ring.phase ^ 1u, b.ctl, b.status)) {
-          alive = false;
-          break;
+      Run run{ph, static_cast<int>(ticket), 0, 0};
+      if (ph < 2) {
+        run.first = phase[ph].begin(run.number);
+        run.count = phase[ph].begin(run.number + 1) - run.first;
+      }
+      if (!runs.give(run) || ph == 2) break;
+      const Phase& p = phase[ph];
+      const Producer copy{b, rt, p.down ? &t2 : &t1, p.down ? &th : &tx, wpol, tpol};
+      // the weights of the first down tiles need no h
+      const int early = p.down ? min(kStages, run.count) : 0;
+      Ring ahead = ring;
+      Cursor c;
+      c.at(p, run.first);
+#pragma unroll 1
+      for (int i = -early; i < run.count; ++i) {
+        if (i == 0 && early) {
+          alive = wait_runs(a.counters + 2, static_cast<uint32_t>(phase[0].parts), b.ctl, b.status);
+          if (!alive) break;
+          fence_proxy_async_global();           // the codes of h
+          c.at(p, run.first);
         }
-        first.weights(p1, c, ring.slot);
-        first.tokens(p1, c, ring.slot);
-        ++issued;
-        ring.next(S::kStages);
-        c.next(p1);
-      }
-      // down weights as the stages come free: they need no h
-      const Producer<TB> then{b, rt, &t2, &th, first.wpol, first.tpol};
-      Ring r = ring;
-      c.at(p2, p2.first);
-      for (int i = 0; i < early && alive; ++i) {
-        if (!wait_soon(b.empty(r.slot), r.phase ^ 1u, b.ctl, b.status)) {
-          alive = false;
-          break;
-        }
-        then.weights(p2, c, r.slot);
-        ++issued;
-        r.next(S::kStages);
-        c.next(p2);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lead) multiply(p1);
-    __syncwarp();
-  } else if (warp == 2) {
-    factors<TB>(b, a, rt, p1, acc);
-  } else if (warp >= 4) {
-    alive = epi.run(p1, acc);
-    fence_proxy_async_global();                 // so are the codes of h
-  }
-  grid.sync();
-
-  // --------------------------------------------------------------------- down
-  if (warp == 0) {
-    if (lead) {
-      fence_proxy_async_global();
-      const Producer<TB> then{b, rt, &t2, &th, l2_policy_evict_first(), l2_policy_evict_last()};
-      c.at(p2, p2.first);
-      for (int i = 0; i < p2.count; ++i) {
-        if (i >= early) {
-          if (!alive || !wait_soon(b.empty(ring.slot), ring.phase ^ 1u, b.ctl, b.status)) break;
-          then.weights(p2, c, ring.slot);
+        const bool weights = i < 0 || i >= early;
+        Ring& at = i < 0 ? ahead : ring;
+        if (weights) {
+          if (!wait_soon(b.empty(at.slot), at.phase ^ 1u, b.ctl, b.status)) {
+            alive = false;
+            break;
+          }
+          copy.weights(p, c, at.slot);
           ++issued;
-        } else if (!alive) {
+        }
+        if (i >= 0) copy.tokens(p, c, at.slot);
+        at.next(kStages);
+        c.next(p);
+      }
+      if (alive) ticket = atomicAdd(a.counters + ph, 1u);
+    }
+    // what is on its way lands before the shared memory goes away
+    const uint32_t late = issued > static_cast<uint32_t>(kStages) ? issued - kStages : 0u;
+    for (uint32_t i = late; i < issued; ++i)
+      wait_drain(b.full(static_cast<int>(i % kStages)), (i / kStages) & 1u,
+                 b.ctl->timeout_ns);
+  } else if (threadIdx.x == 32) {
+    // ------------------------------------------------------------------- MMA
+    const uint32_t idesc = idesc_e4m3(128, kCols);
+    bool alive = true;
+    Run run;
+#pragma unroll 1
+    while (alive && runs.take(&run, false) && run.phase < 2) {
+#pragma unroll 1
+      for (int i = 0; i < run.count; ++i) {
+        if (!wait_both(b.acce(acc.slot), acc.phase ^ 1u, b.full(ring.slot), ring.phase, b.ctl,
+                       b.status)) {
+          alive = false;
           break;
         }
-        then.tokens(p2, c, ring.slot);
-        ring.next(S::kStages);
-        c.next(p2);
+        tc_fence_after();
+        const uint32_t s = b.stage(ring.slot), d = b.tmem + acc.slot * 2 * kCols;
+        const uint64_t tok = sdesc_sw128(s + kTokOffset);
+        tc_mma_e4m3_k128(d, sdesc_sw128(s), tok, idesc);
+        tc_mma_e4m3_k128(d + kCols, sdesc_sw128(s + kGroupBytes), tok, idesc);
+        tc_commit(b.accf(acc.slot));
+        tc_commit(b.empty(ring.slot));
+        ring.next(kStages);
+        acc.next(kAccBufs);
       }
-      // what is on its way lands before the shared memory goes away
-      const uint32_t late = issued > static_cast<uint32_t>(S::kStages) ? issued - S::kStages : 0u;
-      for (uint32_t i = late; i < issued; ++i)
-        wait_drain(b.full(static_cast<int>(i % S::kStages)), (i / S::kStages) & 1u,
-                   b.ctl->timeout_ns);
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lead) {
-      multiply(p2);
-      tc_commit(b.drain());
-      wait_drain(b.drain(), 0, b.ctl->timeout_ns);
-    }
-    __syncwarp();
+    tc_commit(b.drain());
+    wait_drain(b.drain(), 0, b.ctl->timeout_ns);
   } else if (warp == 2) {
-    factors<TB>(b, a, rt, p2, acc);
+    Run run;
+    while (runs.take(&run, true) && run.phase < 2) {
+      if (run.phase == 1) {                     // the scales of h
+        bool ok = true;
+        if (lane == 0)
+          ok = wait_runs(a.counters + 2, static_cast<uint32_t>(phase[0].parts), b.ctl, b.status);
+        if (!__all_sync(kFullWarp, ok)) break;
+      }
+      factors(b, a, rt, phase[run.phase], run, acc);
+    }
   } else if (warp >= 4) {
-    if (alive) epi.run(p2, acc);
+    Epilogue epi{b, a, rt, static_cast<int>(threadIdx.x) & 127};
+    Run run;
+    bool warm = true;
+    while (runs.take(&run, true) && run.phase < 2) {
+      if (!epi.add(phase[run.phase], run, acc, warm && run.phase == 0)) break;
+      warm = false;
+    }
   }
+  __syncwarp();
   if (rt.n_live == 0)                           // no route at all
     for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * a.N;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
@@ -857,38 +929,27 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
-    tmem_dealloc(b.tmem, S::kTmemCols);
+    tmem_dealloc(b.tmem, kTmemCols);
   }
-}
-
-template <int TB>
-cudaError_t go(const CUtensorMap& t1, const CUtensorMap& t2, const CUtensorMap& tx,
-               const CUtensorMap& th, const Fp8MoeArgs& a, int sms, cudaStream_t s) {
-  void* args[] = {const_cast<CUtensorMap*>(&t1), const_cast<CUtensorMap*>(&t2),
-                  const_cast<CUtensorMap*>(&tx), const_cast<CUtensorMap*>(&th),
-                  const_cast<Fp8MoeArgs*>(&a)};
-  return cudaLaunchCooperativeKernel(fp8_moe_kernel<TB>,
-                                     dim3(sms < kMoeMaxGrid ? sms : kMoeMaxGrid), dim3(kThreads),
-                                     args, Shape<TB>::kSmemBytes, s);
-}
-
-template <int TB>
-cudaError_t set_smem() {
-  return cudaFuncSetAttribute(fp8_moe_kernel<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Shape<TB>::kSmemBytes);
 }
 
 }  // namespace
 
 cudaError_t init_fp8_moe_attributes() {
-  cudaError_t e = set_smem<8>();
-  if (e == cudaSuccess) e = set_smem<16>();
-  if (e == cudaSuccess) e = set_smem<32>();
+  cudaError_t e = cudaFuncSetAttribute(fp8_moe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBytes);
+  // The first launch has the SM's memory split as the second needs it: a block of that can
+  // then start beside one of this (with another split it starts when the SM is empty).
+  for (auto* f : {fp8_moe_router_kernel<NVFP4_BF16>, fp8_moe_router_kernel<NVFP4_FP16>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
   return e;
 }
 
-int fp8_moe_box_rows(int columns) { return columns < 16 ? 16 : columns; }
+int fp8_moe_box_rows() { return kCols; }
 
 bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N,
                     MoeLayout* m) {
@@ -899,36 +960,49 @@ bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, in
   const int64_t R = T * topk;
   const int64_t live = R < E ? R : E, kx = (K + 127) / 128, kh = (I + 127) / 128;
   const int64_t units2 = (N + 255) / 256;
-  if (live * kh * kx > 0x3FFFFFFF || live * kh * units2 > 0x3FFFFFFF) return false;   // tiles
+  // tiles times blocks stay below 2^32
+  if (live * kh * (kx > units2 ? kx : units2) > 0xFFFFFFFFLL / kMoeMaxGrid - 1) return false;
   size_t end = 0;
   auto take = [&](int64_t bytes) {
     const size_t at = end;
     end += static_cast<size_t>((bytes + 255) / 256 * 256);
     return at;
   };
-  m->columns = T > 16 ? 32 : T > 8 ? 16 : 8;
+  m->columns = TB;
   m->experts = static_cast<int>(live);
   m->ld_xq = kx * 128;
   m->ld_hq = kh * 128;
   take(T * E * 4);
   m->xq = take(m->columns * m->ld_xq);
   m->xs = take(kx * m->columns * 4);
-  m->hq = take(live * m->columns * m->ld_hq);
-  m->hs = take(live * kh * m->columns * 4);
+  // (one expert more: see Epilogue::run)
+  m->hq = take((live + 1) * m->columns * m->ld_hq);
+  m->hs = take((live + 1) * kh * m->columns * 4);
   m->part = take(static_cast<int64_t>(2) * kMoeMaxGrid * 2 * m->columns * 128 * 4);
-  m->arrived = take((live * kh + 4 * units2) * 4);
+  m->counters = take((4 + live * kh + 4 * units2) * 4);
   m->bytes = end;
   return true;
 }
 
 cudaError_t launch_fp8_moe(const CUtensorMap& t1, const CUtensorMap& t2, const CUtensorMap& tx,
-                           const CUtensorMap& th, const Fp8MoeArgs& a, int columns, int sms,
-                           cudaStream_t s) {
-  switch (columns) {
-    case 8: return go<8>(t1, t2, tx, th, a, sms, s);
-    case 16: return go<16>(t1, t2, tx, th, a, sms, s);
-    default: return go<32>(t1, t2, tx, th, a, sms, s);
-  }
+                           const CUtensorMap& th, const Fp8MoeArgs& a, int sms, cudaStream_t s) {
+  const int grid = sms < kMoeMaxGrid ? sms : kMoeMaxGrid;
+  // one or two blocks an SM: a row and four tokens each, as far as that goes
+  const int first = a.router && a.rule.E * ((a.T + 3) / 4) > grid ? 2 * grid : grid;
+  if (a.type == NVFP4_BF16) fp8_moe_router_kernel<NVFP4_BF16><<<first, kThreads, 0, s>>>(a);
+  else fp8_moe_router_kernel<NVFP4_FP16><<<first, kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_moe_kernel, t1, t2, tx, th, a);
 }
 
 }  // namespace nvfp4

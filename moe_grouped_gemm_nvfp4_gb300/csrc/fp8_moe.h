@@ -10,7 +10,7 @@
 
 namespace nvfp4 {
 
-constexpr int kMoeMaxTokens = 32;
+constexpr int kMoeMaxTokens = 8;
 constexpr int kMoeMaxRoutes = 256;           // one thread each
 constexpr int kMoeMaxGrid = 160;
 
@@ -33,22 +33,25 @@ struct Fp8MoeArgs {
   uint8_t* xq;                     // codes of x [columns, ld_xq]
   int64_t ld_xq;
   float* xs;                       // scales [blocks of K][columns]
-  uint8_t* hq;                     // codes of h [experts * columns, ld_hq]
+  uint8_t* hq;                     // codes of h [(experts + 1) * columns, ld_hq]
   int64_t ld_hq;
-  float* hs;                       // scales [experts][blocks of I][columns]
+  float* hs;                       // scales [experts + 1][blocks of I][columns]
   float* part;                     // [2 * grid][2][columns][128]
-  uint32_t* arrived;               // items1 of gate_up's items, then four of each of down's
-  int32_t items1;
+  // runs of gate_up and of down that are taken, gate_up runs that are done, unused; then
+  // what arrived of each of gate_up's items (items1) and four of each of down's
+  uint32_t* counters;
+  int32_t items1;                  // items of gate_up at most
+  int32_t experts;                 // live ones at most
   int* status;
   uint64_t timeout_ns;
 };
 
-// Sizes that follow from a call's: token columns, live experts at most, and where
-// the workspace's parts begin.
+// Sizes that follow from a call's: token columns, live experts at most, and where the
+// workspace's parts begin.
 struct MoeLayout {
   int columns, experts;
   int64_t ld_xq, ld_hq;
-  size_t xq, xs, hq, hs, part, arrived, bytes;
+  size_t xq, xs, hq, hs, part, counters, bytes;
 };
 // False for sizes that the kernel does not take.
 bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N,
@@ -56,11 +59,10 @@ bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, in
 
 cudaError_t init_fp8_moe_attributes();
 // Rows of the maps' boxes of activations.
-int fp8_moe_box_rows(int columns);
+int fp8_moe_box_rows();
 // t1: gate_up [2 E, I, K], t2: down [E, N, I] (boxes of 128 x 128); tx, th: codes of x
 // and h (boxes of fp8_moe_box_rows() x 128).
 cudaError_t launch_fp8_moe(const CUtensorMap& t1, const CUtensorMap& t2, const CUtensorMap& tx,
-                           const CUtensorMap& th, const Fp8MoeArgs& a, int columns, int sms,
-                           cudaStream_t s);
+                           const CUtensorMap& th, const Fp8MoeArgs& a, int sms, cudaStream_t s);
 
 }  // namespace nvfp4

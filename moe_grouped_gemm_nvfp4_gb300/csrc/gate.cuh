@@ -5,9 +5,9 @@
 //   [/ their sum] * scale
 //
 // Lane i of the warp holds the experts i, i + 32, ...: a choice is a maximum of
-// order-preserving integers over the lane's own, then over the lanes (two integer
-// reductions: the key, then the lowest number that has it).  A NaN counts as the
-// largest value.  With a bias the chosen order hangs on sums whose 32-bit rounding
+// order-preserving integers over the lane's own, then over the lanes (an integer
+// reduction, a vote for who has it, among equals another for the lowest number).  A NaN
+// counts as the largest value.  With a bias the chosen order hangs on sums whose 32-bit rounding
 // can swap neighbours; where two neighbours of the order (the first one left out
 // among them) are nearer than that rounding, the token is chosen again on 64-bit
 // keys.  That is about one token in a thousand at 128 sigmoid scores; 64-bit
@@ -47,16 +47,19 @@ __device__ __forceinline__ uint32_t gate_key(float f) {
   const uint32_t b = __float_as_uint(f + 0.f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+// The float of a key that is no NaN's.
+__device__ __forceinline__ float gate_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
 __device__ __forceinline__ unsigned long long gate_key64(double f) {
   if (f != f) return ~0ull;
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(f + 0.0));
   return b >> 63 ? ~b : b | (1ull << 63);
 }
 
+// v: no NaN
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, o));
-  return v;
+  return gate_value(__reduce_max_sync(kFullWarp, gate_key(v)));
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -165,6 +168,33 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
     s[i] = r.bias && e < r.E ? g.of(l[i]) : l[i];
     key[i] = e < r.E ? gate_key(r.bias ? s[i] + __ldg(r.bias + e) : s[i]) : 0u;
   }
+  // Few per lane: its experts in order, so that its best is always its first (a scan at every
+  // pick took twice as long).
+  int at[L];
+  constexpr bool kSorted = L <= 8;
+#pragma unroll
+  for (int i = 0; i < L; ++i) at[i] = i;
+  float val[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) val[i] = s[i];
+  if constexpr (kSorted) {
+#pragma unroll
+    for (int n = L; n > 1; --n)
+#pragma unroll
+      for (int i = 0; i + 1 < n; ++i) {
+        // (equals stay in order: the lower number first)
+        const bool swap = key[i] < key[i + 1];
+        const uint32_t k0 = key[i];
+        const float v0 = val[i];
+        const int a0 = at[i];
+        key[i] = swap ? key[i + 1] : k0;
+        val[i] = swap ? val[i + 1] : v0;
+        at[i] = swap ? at[i + 1] : a0;
+        key[i + 1] = swap ? k0 : key[i + 1];
+        val[i + 1] = swap ? v0 : val[i + 1];
+        at[i + 1] = swap ? a0 : at[i + 1];
+      }
+  }
   // one more than wanted where neighbours are compared
   const int picks = r.bias && r.topk < r.E ? r.topk + 1 : r.topk;
   int mine = 0;
@@ -172,19 +202,36 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
   bool near = false;
 #pragma unroll 1
   for (int j = 0; j < picks; ++j) {
-    uint32_t best = 0;
-    int at = 0;
-    float val = 0.f;
+    uint32_t best = key[0];
+    int place = at[0];
+    float v = val[0];
+    if constexpr (!kSorted) {
 #pragma unroll
-    for (int i = 0; i < L; ++i)
-      if (key[i] > best) { best = key[i]; at = i; val = s[i]; }
+      for (int i = 1; i < L; ++i)
+        if (key[i] > best) { best = key[i]; place = i; v = val[i]; }
+    }
     const uint32_t top = __reduce_max_sync(kFullWarp, best);
-    const int e = static_cast<int>(
-        __reduce_min_sync(kFullWarp, best == top ? static_cast<uint32_t>(lane + 32 * at) : ~0u));
-    const float v = __shfl_sync(kFullWarp, val, e & 31);
+    const uint32_t who = __ballot_sync(kFullWarp, best == top);
+    int from = __ffs(who) - 1;
+    if (who & (who - 1))                            // equals: the lowest number
+      from = static_cast<int>(__reduce_min_sync(
+                 kFullWarp, best == top ? static_cast<uint32_t>(lane + 32 * place) : ~0u)) & 31;
+    const int e = __shfl_sync(kFullWarp, lane + 32 * place, from);
+    v = __shfl_sync(kFullWarp, v, from);
+    if (lane == from) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        if constexpr (kSorted) {
+          key[i] = i + 1 < L ? key[i + 1 < L ? i + 1 : 0] : 0u;
+          val[i] = val[i + 1 < L ? i + 1 : 0];
+          at[i] = at[i + 1 < L ? i + 1 : 0];
+        } else if (i == place) {
+          key[i] = 0;
+        }
+      }
+    }
     if (r.bias) {
-      const float k = top == 0xFFFFFFFFu ? NAN
-                      : __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+      const float k = top == 0xFFFFFFFFu ? NAN : gate_value(top);
       // a score's relative error is below 1e-6, the sum's half a step of the key
       if (j > 0)
         near |= !(last - k > 2e-6f * (fabsf(last_s) + fabsf(v)) + 2.4e-7f * (fabsf(last) + fabsf(k)));
@@ -192,9 +239,6 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
       last = k;
     }
     if (j == lane && j < r.topk) { mine = e; chosen = v; }
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-      if (lane + 32 * i == e) key[i] = 0;
   }
   if (near) {                                       // the same in every lane
     mine = gate_choose64<L>(r, l, g.max);
@@ -202,12 +246,12 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
 #pragma unroll 1
     for (int j = 0; j < r.topk; ++j) {
       const int e = __shfl_sync(kFullWarp, mine, j);
-      float val = 0.f;
+      float v = 0.f;
 #pragma unroll
       for (int i = 0; i < L; ++i)
-        if (lane + 32 * i == e) val = s[i];
-      val = __shfl_sync(kFullWarp, val, e & 31);
-      if (j == lane) chosen = val;
+        if (lane + 32 * i == e) v = s[i];
+      v = __shfl_sync(kFullWarp, v, e & 31);
+      if (j == lane) chosen = v;
     }
   }
   const bool on = lane < r.topk;

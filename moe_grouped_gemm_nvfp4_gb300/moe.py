@@ -357,8 +357,8 @@ class Fp8MLP:
         return tokens.combine(y, pos, topk_weights, offsets)
 
     def step_few(self, x, topk_ids, topk_weights, stream=None):
-        """step() of a few tokens in one launch: at most 32 tokens and 256 routes
-        (ValueError for more).  gate_up's product and the experts' rows stay FP32 here,
+        """step() of at most 8 tokens (ValueError for more) in one call of the library,
+        without a route-ordered copy of anything.  gate_up's product and the experts' rows stay FP32 here,
         where step() rounds them to x's type.  An expert that a token names twice counts
         with both weights."""
         if forward_ad._current_level >= 0:
@@ -372,7 +372,7 @@ class Fp8MLP:
             return done[0]
         if x.shape[0] == 0:
             return x.new_empty((0, self.down[0].shape[1]))
-        raise ValueError("more tokens or routes than one launch takes: use step()")
+        raise ValueError("step_few takes at most 8 tokens: use step()")
 
 
 class Fp8MoE:
@@ -380,7 +380,7 @@ class Fp8MoE:
     experts (weights as in Fp8MLP).  router [E, K] has the tokens' type or is FP32;
     bias, score, renormalize and scale are the gate's (gating.topk_gate).
 
-    step() of a few tokens (at most 32, and 256 routes) runs in one launch
+    step() of at most 8 tokens is one call of the library
     (nvfp4.nvfp4_fp8_moe_layer).  More go through
     the router's product with FP32 logits, gating.topk_gate and Fp8MLP.step, whose
     gate_up product and expert rows are rounded to the tokens' type; the router's
