@@ -72,6 +72,7 @@ nvfp4_status device_state(DeviceState** out) {
       if (nvfp4::init_fp8_gemm_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_fp8_rows_attributes() != cudaSuccess) return cuda_fail();
       if (nvfp4::init_fp8_moe_attributes() != cudaSuccess) return cuda_fail();
+      if (nvfp4::init_norm_attributes() != cudaSuccess) return cuda_fail();
     }
     if (!g_encode) {
       void* fn = nullptr;
@@ -386,6 +387,13 @@ nvfp4_status check_norm_rows(const void* x, int64_t ld, const void* r, int64_t l
   const unsigned es = dtype_bytes(dtype);
   if (!aligned_to(x, es) || !aligned_to(r, es) || !aligned_to(h, es)) return NVFP4_ERR_UNSUPPORTED;
   return NVFP4_OK;
+}
+
+// Whether rows p (stride ld) lie where dense rows q lie within 16 bytes.
+bool same_offset(const void* p, int64_t ld, const void* q, int64_t T, int64_t D, int32_t dtype) {
+  if (!p || !q) return true;
+  return ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) == 0 &&
+         (T <= 1 || ((ld - D) * dtype_bytes(dtype)) % 16 == 0);
 }
 
 nvfp4_status check_gate(const void* logits, int64_t ld, int64_t T, int32_t E, int32_t dtype,
@@ -1465,7 +1473,10 @@ nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld, const void* residual, int
   if (st == NVFP4_OK) st = check_norm_rows(x, ld, residual, ld_residual, T, D, dtype, h);
   if (st != NVFP4_OK) return st;
   if (T > 0 && !y) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned_to(y, dtype_bytes(dtype))) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned_to(y, dtype_bytes(dtype)) || !same_offset(x, ld, y, T, D, dtype) ||
+      !same_offset(residual, ld_residual, y, T, D, dtype) ||
+      (residual && !same_offset(h, D, y, T, D, dtype)))
+    return NVFP4_ERR_UNSUPPORTED;
   DeviceState* d = nullptr;
   st = device_state(&d);
   if (st != NVFP4_OK) return st;
@@ -1519,7 +1530,9 @@ nvfp4_status nvfp4_rms_norm_fp8(const void* x, int64_t ld, const void* residual,
 
 size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t T, int64_t D) {
   if (T <= 0 || D <= 0 || D > nvfp4::kNormMaxWidth) return 0;
-  return static_cast<size_t>(nvfp4::norm_grad_parts(T, D)) * static_cast<size_t>(D) * sizeof(float);
+  const int narrow = nvfp4::norm_grad_parts(T, D, NVFP4_BF16);
+  const int wide = nvfp4::norm_grad_parts(T, D, NVFP4_FP32);
+  return static_cast<size_t>(narrow > wide ? narrow : wide) * static_cast<size_t>(D) * sizeof(float);
 }
 
 nvfp4_status nvfp4_rms_norm_grad(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
@@ -1532,7 +1545,9 @@ nvfp4_status nvfp4_rms_norm_grad(const void* dy, int64_t ld_dy, const void* h, i
   if (st != NVFP4_OK) return st;
   if (ld_dy < D || !dweight || (T > 0 && (!dy || !dx || !workspace))) return NVFP4_ERR_INVALID_ARG;
   if (!aligned_to(dy, dtype_bytes(dtype)) || !aligned_to(dweight, dtype_bytes(weight_dtype)) ||
-      !aligned_to(workspace, 4) || workspace_bytes < nvfp4_rms_norm_grad_workspace_bytes(T, D))
+      !aligned_to(workspace, 4) || workspace_bytes < nvfp4_rms_norm_grad_workspace_bytes(T, D) ||
+      !same_offset(h, ld_h, dx, T, D, dtype) || !same_offset(dy, ld_dy, dx, T, D, dtype) ||
+      !same_offset(dh, ld_dh, dx, T, D, dtype))
     return NVFP4_ERR_UNSUPPORTED;
   DeviceState* d = nullptr;
   st = device_state(&d);

@@ -377,13 +377,23 @@ Tensor norm_weight(const On& on, PyObject* o, const Tensor& x) {
   return w.contiguous();
 }
 
+// Rows that lie where a dense matrix's do within 16 bytes (a copy where they do not).
+Tensor norm_rows(const Tensor& t) {
+  Tensor r = rows_of(t);
+  const int64_t es = static_cast<int64_t>(r.element_size());
+  if ((reinterpret_cast<uintptr_t>(r.data_ptr()) & 15u) ||
+      (r.size(0) > 1 && (r.stride(0) - r.size(1)) * es % 16))
+    return r.clone(at::MemoryFormat::Contiguous);
+  return r;
+}
+
 // A second operand of x's shape and type, or None.
 Tensor like_rows(const On& on, PyObject* o, const Tensor& x, const char* what) {
   if (o == Py_None) return {};
   const Tensor& t = tensor(o, what);
   need(t.sizes() == x.sizes() && t.scalar_type() == x.scalar_type(), what);
   on.same(t);
-  return rows_of(t);
+  return norm_rows(t);
 }
 Tensor aligned_rows(const Tensor& t) { return t.defined() ? rows16_of(t) : t; }
 const void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -406,7 +416,7 @@ PyObject* rms_norm(PyObject* const* a) {
   const On on(x);
   Tensor w = norm_weight(on, a[1], x);
   Tensor r = like_rows(on, a[2], x, "residual: expected rows of x's shape and type");
-  x = rows_of(x);
+  x = norm_rows(x);
   const int64_t T = x.size(0), D = x.size(1);
   Tensor h;
   if (r.defined()) h = on.empty({T, D}, x.scalar_type());
@@ -444,7 +454,7 @@ PyObject* rms_norm_grad(PyObject* const* a) {
   Tensor dy = like_rows(on, a[0], h, "dy: expected rows of h's shape and type");
   Tensor w = norm_weight(on, a[2], h);
   Tensor dh = like_rows(on, a[3], h, "dh: expected rows of h's shape and type");
-  h = rows_of(h);
+  h = norm_rows(h);
   const int64_t T = h.size(0), D = h.size(1);
   Tensor dx = on.empty({T, D}, h.scalar_type());
   Tensor dw = on.empty({D}, w.scalar_type());

@@ -10,8 +10,7 @@
 // counts as the largest value.  With a bias the chosen order hangs on sums whose 32-bit rounding
 // can swap neighbours; where two neighbours of the order (the first one left out
 // among them) are nearer than that rounding, the token is chosen again on 64-bit
-// keys.  That is about one token in a thousand at 128 sigmoid scores; 64-bit
-// exponentials for all would take longer than everything else here.
+// keys.  64-bit exponentials for all would take longer than everything else here.
 #pragma once
 
 #include <cstdint>
@@ -232,9 +231,12 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
     }
     if (r.bias) {
       const float k = top == 0xFFFFFFFFu ? NAN : gate_value(top);
-      // a score's relative error is below 1e-6, the sum's half a step of the key
+      // What 32 bits can be off by, with room: a sigmoid two steps of a value (its exponential,
+      // sum and quotient are rounded once each), a softmax score 2e-6 of it (its argument and
+      // total too), the sum with the bias half a step.
       if (j > 0)
-        near |= !(last - k > 2e-6f * (fabsf(last_s) + fabsf(v)) + 2.4e-7f * (fabsf(last) + fabsf(k)));
+        near |= !(last - k > (r.sigmoid ? 4e-7f : 2e-6f) * (fabsf(last_s) + fabsf(v)) +
+                                 1.2e-7f * (fabsf(last) + fabsf(k)));
       last_s = v;
       last = k;
     }

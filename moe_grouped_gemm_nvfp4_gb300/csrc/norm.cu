@@ -6,16 +6,28 @@
 //   dx = rstd (g - h rstd^2 mean(g h)) + dh,   g = dy w
 //   dw = sum_t dy h rstd
 //
-// One pass: a row stays in its threads' registers between the reduction and the
-// products, so every byte moves once.  The output is y in the rows' type or, for the
-// FP8 products, E4M3 codes with one scale per 128 columns, taken from the unrounded
-// y (one rounding).  A thread holds 8 or 16 elements of a row and rows share a
-// block where they are narrow; rows whose bases, strides or width are no multiple of
-// 16 bytes move element by element, neighbouring threads on neighbouring elements.
+// One pass: a row stays in its threads' registers between the reduction and the products,
+// so every byte moves once.  The output is y in the rows' type or, for the FP8 products,
+// E4M3 codes with one scale per 128 columns, taken from the unrounded y (one rounding).
+//
+// Blocks walk the rows.  A thread holds 8, 16 or 32 elements of one, in chunks of 16 bytes, and
+// copies its chunks of the next rows to shared memory meanwhile (asynchronous copies that
+// only it reads: no barrier), two rows on their way (four were no faster).  With one row at
+// a time an SM had 24 KB on its way: 8192 rows of 6144 BF16 took 51 us, now 39, their
+// gradient with dh 126 us, now 75.  Narrow rows share a block.
+//
+// Where rows are no multiple of 16 bytes apart, chunks are the aligned ones of memory: all
+// tensors of a call have their rows at the same offset in a chunk (the first and last chunk
+// of a row are masked), and a block's rows are eight apart or a multiple, so that they all
+// start at the same offset and the block's weights stay in registers there too.
 //
 // dw: each block keeps its rows' sums in registers (a thread has the same columns of
 // every row), writes them once, and a second launch adds the blocks' in order.  No
-// atomics: results repeat bit for bit.  Sums are FP32.  Bound: HBM.
+// atomics: results repeat bit for bit.  Sums are FP32.
+//
+// Bound: HBM; 8192 x 6144 BF16 with residual 65 us (0.91 of the copy rate), its gradient with
+// dh 75 us (0.79), the codes with residual 85 us (0.61: half of the issue slots go to the
+// quotients, conversions and maxima, and the scales' rows are written four bytes at a time).
 #include "fp8_quant.cuh"
 #include "norm.h"
 
@@ -24,11 +36,14 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kSms = 152;                 // the workspace's size hangs on it
+constexpr int kNormSmem = 200 * 1024;     // of an SM for the rows on their way
 
-// Threads of a row, and rows of a block.
+// Threads of a row, rows of a block, rows on their way.
 struct NormShape {
-  int ept, threads, rows;
+  int ept, threads, rows, depth, grid;
+  size_t smem;
 };
+constexpr int kMostDepth = 2;
 
 // The sum over a row's threads of N values, the same in each of them: lanes, then warps
 // in shared memory (which calls of one kernel share: a barrier first).
@@ -60,208 +75,335 @@ __device__ __forceinline__ float weight_at(const void* w, int type, int c) {
   return type == NVFP4_BF16 ? elem_to_f32<NVFP4_BF16>(b) : elem_to_f32<NVFP4_FP16>(b);
 }
 
-// VEC weights from column c on (base aligned to 16 bytes where VEC > 1).
-template <int VEC>
-__device__ __forceinline__ void load_weights(const void* w, int type, int c, float* f) {
-  if constexpr (VEC == 1) {
-    f[0] = weight_at(w, type, c);
-  } else if (type == NVFP4_FP32) {
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + i));
-      f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
-    }
-  } else if constexpr (VEC == 8) {
-    if (type == NVFP4_BF16) {
-      Pack<NVFP4_BF16, 8> p;
-      p.load(w, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = p.get(i);
-    } else {
-      Pack<NVFP4_FP16, 8> p;
-      p.load(w, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = p.get(i);
-    }
+// A chunk of floats in the rows' type, two per conversion.
+template <int DT, int N>
+__device__ __forceinline__ void pack(Pack<DT, N>& p, const float (&f)[N]) {
+  if constexpr (DT == NVFP4_FP32) {
+    p.from(f);
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = weight_at(w, type, c + i);
-  }
-}
-
-template <int DT, int VEC>
-__device__ __forceinline__ void store(void* base, int64_t at, const Pack<DT, VEC>& p) {
-  using Bits = typename Elem<DT>::Bits;
-  Bits* d = static_cast<Bits*>(base) + at;
-  if constexpr (VEC == 1) *d = static_cast<Bits>(p.w[0]);
-  else *reinterpret_cast<uint4*>(d) = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
-}
-
-template <int DT, int VEC, int EPT, bool FP8, int MOST>
-__global__ void __launch_bounds__(MOST) rms_norm_kernel(const NormArgs a, int threads, int rows) {
-  constexpr int V = EPT / VEC;
-  __shared__ float part[32][1];
-  const int sub = threadIdx.x / threads, tid = threadIdx.x - sub * threads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + sub;
-  const bool on = row < a.T;
-  Pack<DT, VEC> px[V], pr[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * threads + tid) * VEC;
-    px[i].zero();
-    pr[i].zero();
-    if (on && c < a.D) {
-      px[i].load(a.x, row * a.ld + c);
-      if (a.r) pr[i].load(a.r, row * a.ld_r + c);
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (DT == NVFP4_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p.w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+      else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p.w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
     }
   }
-  float w[EPT], h[EPT], sum[1] = {0.f};
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  const int n = in ? 16 : 0;                        // the rest of the 16 bytes: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest n groups.
+__device__ __forceinline__ void cp_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
+
+// A thread's chunks of a row: DT's type, EPT elements, the chunks next to each other
+// (TOGETHER) or a row's threads apart.  Without ALIGNED a row starts `lead` elements after
+// the start of its first chunk.
+template <int DT, int EPT, bool TOGETHER, bool ALIGNED>
+struct Chunks {
+  static constexpr int N = elems_per_16b<DT>(), V = EPT / N;
+  int threads, tid, D, lead;
+  __device__ __forceinline__ int column(int i) const {       // may be negative without ALIGNED
+    const int c = TOGETHER ? tid * V + i : i * threads + tid;
+    return c * N - (ALIGNED ? 0 : lead);
+  }
+  __device__ __forceinline__ bool any(int i) const { return column(i) < D; }
+  __device__ __forceinline__ bool whole(int i) const {
+    return ALIGNED || (column(i) >= 0 && column(i) + N <= D);
+  }
+  __device__ __forceinline__ bool in(int i, int j) const {
+    return ALIGNED || (column(i) + j >= 0 && column(i) + j < D);
+  }
+  // A row's copies to shared memory, `apart` bytes between the chunks' places.
+  __device__ __forceinline__ void copy(uint32_t dst, int apart, const void* base, int64_t ld,
+                                       int64_t row, bool on) const {
+    const char* p = static_cast<const char*>(base) + row * ld * elem_bytes<DT>();
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * threads + tid) * VEC;
-    if (c < a.D) {
-      load_weights<VEC>(a.w, a.w_type, c, w + i * VEC);
+    for (int i = 0; i < V; ++i) {
+      const bool go = on && any(i);
+      cp16(dst + i * apart, go ? p + column(i) * elem_bytes<DT>() : static_cast<const char*>(base), go);
+    }
+  }
+  __device__ __forceinline__ void take(uint32_t src, int apart, Pack<DT, N> (&p)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(p[i].w[0]), "=r"(p[i].w[1]), "=r"(p[i].w[2]), "=r"(p[i].w[3])
+                   : "r"(src + i * apart) : "memory");
+      if (!whole(i)) {                              // what lies outside the row is not the row's
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if constexpr (N == 4) {
+            if (!in(i, w)) p[i].w[w] = 0u;
+          } else {
+            p[i].w[w] &= (in(i, 2 * w) ? 0xFFFFu : 0u) | (in(i, 2 * w + 1) ? 0xFFFF0000u : 0u);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void put(void* base, int64_t row, int i, const Pack<DT, N>& p) const {
+    using Bits = typename Elem<DT>::Bits;
+    Bits* d = static_cast<Bits*>(base) + row * D + column(i);
+    if (whole(i)) {
+      *reinterpret_cast<uint4*>(d) = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) w[i * VEC + j] = 0.f;
+      for (int j = 0; j < N; ++j)
+        if (in(i, j)) d[j] = static_cast<Bits>(N == 4 ? p.w[j & 3] : p.w[j >> 1] >> (16 * (j & 1)));
     }
   }
+  __device__ __forceinline__ void weights(const void* w, int type, float (&f)[EPT]) const {
+    const bool vectors = ALIGNED && (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i) {
+      const int c = column(i);
+      if (vectors && any(i)) {
+        if (type == NVFP4_FP32) {
+#pragma unroll
+          for (int j = 0; j < N; j += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + j));
+            f[i * N + j] = v.x; f[i * N + j + 1] = v.y;
+            f[i * N + j + 2] = v.z; f[i * N + j + 3] = v.w;
+          }
+        } else if constexpr (DT != NVFP4_FP32) {
+          Pack<DT, N> v;                            // the rows' type
+          v.load(w, c);
+#pragma unroll
+          for (int j = 0; j < N; ++j) f[i * N + j] = v.get(j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          f[i * N + j] = any(i) && in(i, j) ? weight_at(w, type, c + j) : 0.f;
+      }
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ int lead_of(const void* base, int64_t ld, int64_t row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(base) + row * ld * elem_bytes<DT>()) & 15u) /
+         elem_bytes<DT>();
+}
+
+template <int DT, int EPT, bool FP8, bool ALIGNED, int REGS>
+__global__ void __maxnreg__(REGS) rms_norm_kernel(const NormArgs a, int threads, int rows,
+                                                  int depth) {
+  using C = Chunks<DT, EPT, FP8, ALIGNED>;
+  constexpr int N = C::N, V = C::V;
+  extern __shared__ uint4 staged[];                 // [depth][arrays][V][threads of the block]
+  __shared__ float part[32][1];
+  const int sub = threadIdx.x / threads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
+  const C c{threads, static_cast<int>(threadIdx.x) - sub * threads, a.D,
+            ALIGNED ? 0 : lead_of<DT>(a.x, a.ld, first + sub)};
+  const int apart = blockDim.x * 16, arrays = a.r ? 2 : 1;
+  const uint32_t mine = smem_u32(staged) + threadIdx.x * 16;
+  auto place = [&](int slot, int array) { return mine + ((slot * arrays + array) * V) * apart; };
+  auto copy = [&](int64_t base, int slot) {
+    const int64_t row = base + sub;
+    c.copy(place(slot, 0), apart, a.x, a.ld, row, row < a.T);
+    if (a.r) c.copy(place(slot, 1), apart, a.r, a.ld_r, row, row < a.T);
+    cp_commit();
+  };
+  for (int i = 0; i < depth; ++i) copy(first + i * step, i);
+  float w[EPT];
+  c.weights(a.w, a.w_type, w);
+  int slot = 0;
+#pragma unroll 1
+  for (int64_t base = first; base < a.T; base += step) {
+    const int64_t row = base + sub;
+    const bool on = row < a.T;
+    cp_wait(depth - 1);
+    Pack<DT, N> px[V];
+    c.take(place(slot, 0), apart, px);
+    float sum[1] = {0.f};
     if (a.r) {
-      float f[VEC];
+      Pack<DT, N> pr[V];
+      c.take(place(slot, 1), apart, pr);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = px[i].get(j) + pr[i].get(j);
-      px[i].from(f);
-      const int c = (i * threads + tid) * VEC;
-      if (on && c < a.D) store<DT, VEC>(a.h, row * a.D + c, px[i]);
+      for (int i = 0; i < V; ++i) {
+        float f[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] = px[i].get(j) + pr[i].get(j);
+        pack<DT, N>(px[i], f);
+        if (on && c.any(i)) c.put(a.h, row, i, px[i]);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float f = px[i].get(j);
-      h[i * VEC + j] = f;
-      sum[0] = fmaf(f, f, sum[0]);
-    }
-  }
-  row_sum<1>(sum, threads, part);
-  const float rstd = 1.f / sqrtf(sum[0] / static_cast<float>(a.D) + a.eps);
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * threads + tid) * VEC;
-    float y[VEC];
+      for (int j = 0; j < N; ++j) sum[0] = fmaf(px[i].get(j), px[i].get(j), sum[0]);
+    row_sum<1>(sum, threads, part);
+    copy(base + depth * step, slot);                // the slot has been read
+    if (++slot == depth) slot = 0;
+    const float rstd = 1.f / sqrtf(sum[0] / static_cast<float>(a.D) + a.eps);
     if constexpr (FP8) {
-      // The quotient 448 y / max |y| does not hold rstd: it is taken from the products
-      // h w (exact for 16-bit factors), so that codes are rounded from the real quotient
-      // also next to a border; with rstd only where a maximum leaves the normal range.
-      float amax = 0.f;
+      // The quotient 448 y / max |y| does not hold rstd: it is taken from the products h w
+      // (exact for 16-bit factors), so that codes are rounded from the real quotient also
+      // next to a border; with rstd only where a maximum leaves the normal range.  For BF16
+      // factors the products have 16 bits, a border times the maximum 21, so a quotient
+      // meets a border or misses it by 2^-21 of its value, and BlockScale's, good to 2^-23,
+      // will do.
+      constexpr int kLanes = 128 / EPT;             // of a block of 128 columns
+      float y[EPT], amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        y[j] = h[i * VEC + j] * w[i * VEC + j];
+      for (int j = 0; j < EPT; ++j) {
+        y[j] = px[j / N].get(j % N) * w[j];
         amax = fmaxf(amax, fabsf(y[j]));
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
       const bool direct = amax >= kAmaxFloor && amax * rstd >= kAmaxFloor && amax < INFINITY;
-      if (!direct) {
-        amax = 0.f;
+      if (!__all_sync(0xFFFFFFFFu, direct)) {
+        float again = 0.f;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          y[j] = h[i * VEC + j] * rstd * w[i * VEC + j];
-          amax = fmaxf(amax, fabsf(y[j]));
+        for (int j = 0; j < EPT; ++j) {
+          if (!direct) y[j] = px[j / N].get(j % N) * rstd * w[j];
+          again = fmaxf(again, fabsf(y[j]));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+          again = fmaxf(again, __shfl_xor_sync(0xFFFFFFFFu, again, o));
+        amax = again;
+      }
+      const int col = c.column(0);
+      if (on && col < a.D) {                        // D % 16 == 0: whole sixteens
+        uint32_t q[EPT / 4];
+        float scale;
+        auto codes = [&](const auto& b) {
+          scale = b.scale;
+#pragma unroll
+          for (int j = 0; j < EPT / 4; ++j)
+            q[j] = e4m3x4(b.quotient(y[4 * j]), b.quotient(y[4 * j + 1]),
+                          b.quotient(y[4 * j + 2]), b.quotient(y[4 * j + 3]));
+        };
+        if (DT == NVFP4_BF16 && a.w_type == NVFP4_BF16 && direct) codes(BlockScale(amax));
+        else codes(BlockScale32(amax));
+        uint8_t* out = a.codes + row * a.D + col;
+        if constexpr (EPT == 8) {
+          *reinterpret_cast<uint2*>(out) = make_uint2(q[0], q[1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < EPT / 16; ++j)
+            if (col + 16 * j < a.D)
+              *reinterpret_cast<uint4*>(out + 16 * j) =
+                  make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+        }
+        if ((col & 127) == 0)
+          a.scales[static_cast<int64_t>(col >> 7) * a.T + row] = direct ? scale * rstd : scale;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (on && c.any(i)) {
+          float y[N];
+#pragma unroll
+          for (int j = 0; j < N; ++j) y[j] = px[i].get(j) * rstd * w[i * N + j];
+          Pack<DT, N> p;
+          pack<DT, N>(p, y);
+          c.put(a.y, row, i, p);
         }
       }
-      // (`direct` is the same in the 16 lanes of a block, not in the warp's two blocks)
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-      if (on && c < a.D) {
-        const BlockScale32 b(amax);
-        uint2 q;
-        q.x = e4m3x4(b.quotient(y[0]), b.quotient(y[1]), b.quotient(y[2]), b.quotient(y[3]));
-        q.y = e4m3x4(b.quotient(y[4]), b.quotient(y[5]), b.quotient(y[6]), b.quotient(y[7]));
-        *reinterpret_cast<uint2*>(a.codes + row * a.D + c) = q;
-        if ((c & 127) == 0)
-          a.scales[static_cast<int64_t>(c >> 7) * a.T + row] = direct ? b.scale * rstd : b.scale;
-      }
-    } else if (on && c < a.D) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = h[i * VEC + j] * rstd * w[i * VEC + j];
-      Pack<DT, VEC> p;
-      p.from(y);
-      store<DT, VEC>(a.y, row * a.D + c, p);
     }
   }
+  cp_wait(0);
 }
 
-template <int DT, int VEC, int EPT, int MOST>
-__global__ void __launch_bounds__(MOST) rms_norm_grad_kernel(const NormArgs a, int threads,
-                                                             int rows) {
-  constexpr int V = EPT / VEC;
+template <int DT, int EPT, bool ALIGNED, int REGS>
+__global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int threads, int rows,
+                                                       int depth) {
+  using C = Chunks<DT, EPT, false, ALIGNED>;
+  constexpr int N = C::N, V = C::V;
+  extern __shared__ uint4 staged[];
   __shared__ float part[32][2];
-  const int sub = threadIdx.x / threads, tid = threadIdx.x - sub * threads;
+  const int sub = threadIdx.x / threads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
+  const C c{threads, static_cast<int>(threadIdx.x) - sub * threads, a.D,
+            ALIGNED ? 0 : lead_of<DT>(a.x, a.ld, first + sub)};
+  const int apart = blockDim.x * 16, arrays = a.r ? 3 : 2;
+  const uint32_t mine = smem_u32(staged) + threadIdx.x * 16;
+  auto place = [&](int slot, int array) { return mine + ((slot * arrays + array) * V) * apart; };
+  auto copy = [&](int64_t base, int slot) {
+    const int64_t row = base + sub;
+    c.copy(place(slot, 0), apart, a.x, a.ld, row, row < a.T);
+    c.copy(place(slot, 1), apart, a.dy, a.ld_dy, row, row < a.T);
+    if (a.r) c.copy(place(slot, 2), apart, a.r, a.ld_r, row, row < a.T);
+    cp_commit();
+  };
+  for (int i = 0; i < depth; ++i) copy(first + i * step, i);
   float w[EPT], dw[EPT];
+  c.weights(a.w, a.w_type, w);
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) w[i] = dw[i] = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * threads + tid) * VEC;
-    if (c < a.D) load_weights<VEC>(a.w, a.w_type, c, w + i * VEC);
-  }
+  for (int i = 0; i < EPT; ++i) dw[i] = 0.f;
   const float over = 1.f / static_cast<float>(a.D);
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows; base < a.T;
-       base += static_cast<int64_t>(gridDim.x) * rows) {
+  int slot = 0;
+#pragma unroll 1
+  for (int64_t base = first; base < a.T; base += step) {
     const int64_t row = base + sub;
     const bool on = row < a.T;
-    Pack<DT, VEC> ph[V], pd[V], pr[V];
+    cp_wait(depth - 1);
+    Pack<DT, N> ph[V], pd[V], pr[V];
+    c.take(place(slot, 0), apart, ph);
+    c.take(place(slot, 1), apart, pd);
+    if (a.r) {
+      c.take(place(slot, 2), apart, pr);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * threads + tid) * VEC;
-      ph[i].zero();
-      pd[i].zero();
-      pr[i].zero();
-      if (on && c < a.D) {
-        ph[i].load(a.x, row * a.ld + c);
-        pd[i].load(a.dy, row * a.ld_dy + c);
-        if (a.r) pr[i].load(a.r, row * a.ld_r + c);
-      }
+      for (int i = 0; i < V; ++i) pr[i].zero();
     }
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < N; ++j) {
         const float h = ph[i].get(j);
         sum[0] = fmaf(h, h, sum[0]);
-        sum[1] = fmaf(pd[i].get(j) * w[i * VEC + j], h, sum[1]);
+        sum[1] = fmaf(pd[i].get(j) * w[i * N + j], h, sum[1]);
       }
     row_sum<2>(sum, threads, part);
+    copy(base + depth * step, slot);                // the slot has been read
+    if (++slot == depth) slot = 0;
     const float rstd = 1.f / sqrtf(sum[0] * over + a.eps);
     const float back = rstd * rstd * (sum[1] * over);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (i * threads + tid) * VEC;
-      float f[VEC];
+      float f[N];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < N; ++j) {
         const float h = ph[i].get(j), d = pd[i].get(j);
-        f[j] = rstd * fmaf(d, w[i * VEC + j], -h * back) + pr[i].get(j);
-        dw[i * VEC + j] = fmaf(d, h * rstd, dw[i * VEC + j]);
+        f[j] = rstd * fmaf(d, w[i * N + j], -h * back) + pr[i].get(j);
+        dw[i * N + j] = fmaf(d, h * rstd, dw[i * N + j]);
       }
-      if (on && c < a.D) {
-        Pack<DT, VEC> p;
-        p.from(f);
-        store<DT, VEC>(a.y, row * a.D + c, p);
+      if (on && c.any(i)) {
+        Pack<DT, N> p;
+        pack<DT, N>(p, f);
+        c.put(a.y, row, i, p);
       }
     }
   }
-  float* out = a.part + (static_cast<int64_t>(blockIdx.x) * rows + sub) * a.D;
+  cp_wait(0);
+  float* out = a.part + (first + sub) * a.D;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * threads + tid) * VEC;
-    if (c < a.D) {
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) out[c + j] = dw[i * VEC + j];
-    }
-  }
+    for (int j = 0; j < N; ++j)
+      if (c.any(i) && c.in(i, j)) out[c.column(i) + j] = dw[i * N + j];
 }
 
 // dw[c] = sum of the parts' column c: 32 columns a block, 32 warps on every 32nd part.
@@ -286,88 +428,151 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, in
 }
 
 // Elements a thread takes of a row: 8 while there are few rows (a row's time is then
-// its latency) or a row has few elements, 16 where rows fill the SMs anyway.
-NormShape shape_of(int64_t T, int64_t D) {
+// its latency) or a row has few elements, 16 where rows fill the SMs anyway, 32 for rows
+// that are wider than 512 threads of 16.  Registers a thread: 64, `most`, 96
+// (up to five warps share the 16384 of a quarter of the SM).
+NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int rounds) {
+  const int es = dtype == NVFP4_FP32 ? 4 : 2;
+  const int64_t width = D % (16 / es) ? D + 16 / es - 1 : D;    // a chunk more, begun anywhere
   NormShape s{};
-  s.ept = (T > 2 * kSms && D > 32 * 4 * 8) || D > 1024 * 8 ? 16 : 8;
-  s.threads = static_cast<int>((D + 32 * s.ept - 1) / (32 * s.ept)) * 32;
+  s.ept = width > 512 * 16 ? 32 : T > 2 * kSms && width > 32 * 4 * 8 ? 16 : 8;
+  s.threads = static_cast<int>((width + 32 * s.ept - 1) / (32 * s.ept)) * 32;
   s.rows = s.threads >= 256 ? 1 : 256 / s.threads;
+  const int block = s.threads * s.rows;
+  const int regs = s.ept == 8 ? 64 : s.ept == 16 ? most : 96;
+  int per_sm = 16384 / (regs * 32 * ((block + 127) / 128));
+  if (per_sm > 2048 / block) per_sm = 2048 / block;
+  if (per_sm > 8) per_sm = 8;
+  if (per_sm < 1) per_sm = 1;
+  // rows on their way: what fits beside the other blocks of the SM
+  const int64_t row_bytes = static_cast<int64_t>(block) * s.ept * es * arrays;
+  const int64_t want = (T + s.rows - 1) / s.rows;
+  while (per_sm > 1 && row_bytes * 2 > kNormSmem / per_sm) --per_sm;
+  int64_t depth = kNormSmem / per_sm / row_bytes;
+  if (depth > kMostDepth) depth = kMostDepth;
+  // (the grid: a multiple of eight, or one step for every block)
+  int64_t grid = static_cast<int64_t>(kSms) * per_sm;
+  // Many rows: several rounds of blocks, since SMs are not equally fast (norm with residual
+  // of 8192 x 6144 72 -> 65 us); not where one block fills an SM (4096 x 8192 47 -> 50 us),
+  // nor for the codes (85 -> 89 us).
+  if (rounds > 1 && per_sm > 1 && want >= 4 * rounds * grid) grid *= rounds;
+  s.grid = static_cast<int>(want < grid ? want : grid);
+  const int64_t steps = s.grid > 0 ? (want + s.grid - 1) / s.grid : 1;
+  if (depth > steps) depth = steps;
+  s.depth = static_cast<int>(depth < 1 ? 1 : depth);
+  s.smem = static_cast<size_t>(row_bytes) * s.depth;
   return s;
 }
+constexpr int kForwardRegs = 80, kFp8Regs = 80, kGradRegs = 128;
+int forward_arrays(const NormArgs& a) { return a.r ? 2 : 1; }
+// (with or without dh the same shape: the workspace's size hangs on it)
+constexpr int kGradArrays = 3;
 
-bool vectors(const NormArgs& a, int dtype, bool grad) {
+template <int DT, int EPT, bool FP8, bool ALIGNED, int REGS>
+cudaError_t go(const NormArgs& a, const NormShape& s, cudaStream_t st) {
+  rms_norm_kernel<DT, EPT, FP8, ALIGNED, REGS>
+      <<<s.grid, s.threads * s.rows, s.smem, st>>>(a, s.threads, s.rows, s.depth);
+  return cudaGetLastError();
+}
+template <int DT, bool FP8, bool ALIGNED>
+cudaError_t forward(const NormArgs& a, int dtype, cudaStream_t st) {
+  constexpr int kRegs = FP8 ? kFp8Regs : kForwardRegs;
+  const NormShape s = shape_of(a.T, a.D, dtype, forward_arrays(a), kRegs, FP8 ? 1 : 4);
+  if (s.ept == 8) return go<DT, 8, FP8, ALIGNED, 64>(a, s, st);
+  if (s.ept == 16) return go<DT, 16, FP8, ALIGNED, kRegs>(a, s, st);
+  return go<DT, 32, FP8, ALIGNED, 96>(a, s, st);
+}
+
+template <int DT, int EPT, bool ALIGNED, int REGS>
+void go_grad(const NormArgs& a, const NormShape& s, cudaStream_t st) {
+  rms_norm_grad_kernel<DT, EPT, ALIGNED, REGS>
+      <<<s.grid, s.threads * s.rows, s.smem, st>>>(a, s.threads, s.rows, s.depth);
+}
+template <int DT, bool ALIGNED>
+cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
+  const NormShape s = shape_of(a.T, a.D, dtype, kGradArrays, kGradRegs, 1);
+  if (s.grid > 0) {
+    if (s.ept == 8) go_grad<DT, 8, ALIGNED, 64>(a, s, st);
+    else if (s.ept == 16) go_grad<DT, 16, ALIGNED, kGradRegs>(a, s, st);
+    else go_grad<DT, 32, ALIGNED, 96>(a, s, st);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  rms_norm_dw_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.part, s.grid * s.rows, a.D, a.w_type,
+                                                       a.dw);
+  return cudaGetLastError();
+}
+
+template <int DT, int EPT, int REGS, int FP8_REGS, int GRAD_REGS>
+cudaError_t set_smem() {
+  constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, true, REGS>, kAttr, kNormSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, false, REGS>, kAttr, kNormSmem);
+  if constexpr (DT != NVFP4_FP32)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, true, true, FP8_REGS>, kAttr, kNormSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, EPT, true, GRAD_REGS>, kAttr, kNormSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, EPT, false, GRAD_REGS>, kAttr, kNormSmem);
+  return e;
+}
+template <int DT>
+cudaError_t set_all() {
+  cudaError_t e = set_smem<DT, 8, 64, 64, 64>();
+  if (e == cudaSuccess) e = set_smem<DT, 32, 96, 96, 96>();
+  if (e == cudaSuccess) e = set_smem<DT, 16, kForwardRegs, kFp8Regs, kGradRegs>();
+  return e;
+}
+
+// Whether every row is made of whole chunks.
+bool aligned(const NormArgs& a, int dtype, bool grad) {
   const int es = dtype == NVFP4_FP32 ? 4 : 2;
   auto row16 = [&](const void* p, int64_t ld) {
     return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (a.T <= 1 || ld * es % 16 == 0));
   };
   return static_cast<int64_t>(a.D) * es % 16 == 0 && row16(a.x, a.ld) && row16(a.r, a.ld_r) &&
-         row16(a.w, 0) && row16(a.h, a.D) && row16(a.y, a.D) && (!grad || row16(a.dy, a.ld_dy));
-}
-
-template <int DT, int VEC, bool FP8>
-cudaError_t forward(const NormArgs& a, const NormShape& s, cudaStream_t st) {
-  const int64_t blocks = (a.T + s.rows - 1) / s.rows;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const unsigned g = static_cast<unsigned>(blocks), n = static_cast<unsigned>(s.threads * s.rows);
-  if (s.ept == 8) rms_norm_kernel<DT, VEC, 8, FP8, 1024><<<g, n, 0, st>>>(a, s.threads, s.rows);
-  else if (n <= 512) rms_norm_kernel<DT, VEC, 16, FP8, 512><<<g, n, 0, st>>>(a, s.threads, s.rows);
-  else rms_norm_kernel<DT, VEC, 16, FP8, 1024><<<g, n, 0, st>>>(a, s.threads, s.rows);
-  return cudaGetLastError();
-}
-
-int grad_blocks(int64_t T, const NormShape& s) {
-  const int64_t want = (T + s.rows - 1) / s.rows;
-  const int64_t most = static_cast<int64_t>(kSms) * (s.threads * s.rows > 512 ? 1 : 2);
-  return static_cast<int>(want < most ? want : most);
-}
-
-template <int DT, int VEC>
-cudaError_t backward(const NormArgs& a, cudaStream_t st) {
-  const NormShape s = shape_of(a.T, a.D);
-  const unsigned g = static_cast<unsigned>(grad_blocks(a.T, s));
-  const unsigned n = static_cast<unsigned>(s.threads * s.rows);
-  if (g > 0) {
-    if (s.ept == 8)
-      rms_norm_grad_kernel<DT, VEC, 8, 1024><<<g, n, 0, st>>>(a, s.threads, s.rows);
-    else if (n <= 512)
-      rms_norm_grad_kernel<DT, VEC, 16, 512><<<g, n, 0, st>>>(a, s.threads, s.rows);
-    else
-      rms_norm_grad_kernel<DT, VEC, 16, 1024><<<g, n, 0, st>>>(a, s.threads, s.rows);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  rms_norm_dw_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.part, static_cast<int>(g) * s.rows, a.D,
-                                                       a.w_type, a.dw);
-  return cudaGetLastError();
+         row16(a.h, a.D) && row16(a.y, a.D) && (!grad || row16(a.dy, a.ld_dy));
 }
 
 template <int DT>
-cudaError_t by_vector(const NormArgs& a, bool fp8, cudaStream_t st) {
-  const NormShape s = shape_of(a.T, a.D);
+cudaError_t by_alignment(const NormArgs& a, int dtype, bool fp8, cudaStream_t st) {
   if constexpr (DT != NVFP4_FP32)
-    if (fp8) return forward<DT, 8, true>(a, s, st);
-  return vectors(a, DT, false) ? forward<DT, elems_per_16b<DT>(), false>(a, s, st)
-                               : forward<DT, 1, false>(a, s, st);
+    if (fp8) return forward<DT, true, true>(a, dtype, st);
+  return aligned(a, dtype, false) ? forward<DT, false, true>(a, dtype, st)
+                                  : forward<DT, false, false>(a, dtype, st);
+}
+template <int DT>
+cudaError_t grad_by_alignment(const NormArgs& a, int dtype, cudaStream_t st) {
+  return aligned(a, dtype, true) ? backward<DT, true>(a, dtype, st)
+                                 : backward<DT, false>(a, dtype, st);
 }
 
 }  // namespace
 
-int norm_grad_parts(int64_t T, int64_t D) {
-  const NormShape s = shape_of(T, D);
-  return grad_blocks(T, s) * s.rows;
+cudaError_t init_norm_attributes() {
+  cudaError_t e = set_all<NVFP4_BF16>();
+  if (e == cudaSuccess) e = set_all<NVFP4_FP16>();
+  if (e == cudaSuccess) e = set_all<NVFP4_FP32>();
+  return e;
+}
+
+int norm_grad_parts(int64_t T, int64_t D, int dtype) {
+  const NormShape s = shape_of(T, D, dtype, kGradArrays, kGradRegs, 1);
+  return s.grid * s.rows;
 }
 
 cudaError_t launch_rms_norm(const NormArgs& a, int dtype, bool fp8, cudaStream_t s) {
-  if (dtype == NVFP4_BF16) return by_vector<NVFP4_BF16>(a, fp8, s);
-  if (dtype == NVFP4_FP16) return by_vector<NVFP4_FP16>(a, fp8, s);
-  return by_vector<NVFP4_FP32>(a, fp8, s);
+  if (dtype == NVFP4_BF16) return by_alignment<NVFP4_BF16>(a, dtype, fp8, s);
+  if (dtype == NVFP4_FP16) return by_alignment<NVFP4_FP16>(a, dtype, fp8, s);
+  return by_alignment<NVFP4_FP32>(a, dtype, fp8, s);
 }
 
 cudaError_t launch_rms_norm_grad(const NormArgs& a, int dtype, cudaStream_t s) {
-  const bool v = vectors(a, dtype, true);
-  if (dtype == NVFP4_BF16) return v ? backward<NVFP4_BF16, 8>(a, s) : backward<NVFP4_BF16, 1>(a, s);
-  if (dtype == NVFP4_FP16) return v ? backward<NVFP4_FP16, 8>(a, s) : backward<NVFP4_FP16, 1>(a, s);
-  return v ? backward<NVFP4_FP32, 4>(a, s) : backward<NVFP4_FP32, 1>(a, s);
+  if (dtype == NVFP4_BF16) return grad_by_alignment<NVFP4_BF16>(a, dtype, s);
+  if (dtype == NVFP4_FP16) return grad_by_alignment<NVFP4_FP16>(a, dtype, s);
+  return grad_by_alignment<NVFP4_FP32>(a, dtype, s);
 }
 
 }  // namespace nvfp4

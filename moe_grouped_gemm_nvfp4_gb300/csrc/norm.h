@@ -6,7 +6,7 @@
 
 namespace nvfp4 {
 
-constexpr int kNormMaxWidth = 16384;       // 1024 threads of 16 elements
+constexpr int kNormMaxWidth = 16384;       // 512 threads of 32 elements
 
 struct NormArgs {
   const void* x;                   // [T, D], row stride ld (grad: h)
@@ -29,7 +29,8 @@ struct NormArgs {
 };
 
 // Partial sums of the weight's gradient.
-int norm_grad_parts(int64_t T, int64_t D);
+int norm_grad_parts(int64_t T, int64_t D, int dtype);
+cudaError_t init_norm_attributes();
 cudaError_t launch_rms_norm(const NormArgs& a, int dtype, bool fp8, cudaStream_t s);
 cudaError_t launch_rms_norm_grad(const NormArgs& a, int dtype, cudaStream_t s);
 

@@ -4,9 +4,9 @@ and with 8-bit output for the FP8 products.
     h = x + residual                          (rounded to the rows' type)
     y = h / sqrt(mean(h^2) + eps) * weight    (FP32, rounded once)
 
-Rows [.., D] are BF16, FP16 or FP32 of any width up to 16384 and any row stride; the
-weight [D] has the rows' type or is FP32.  Rows whose elements are not neighbours are
-copied first.  `rms_norm` takes part in autograd; `rms_norm_grad` is its gradient as a
+Rows [.., D] are BF16, FP16 or FP32 of any width up to 16384; the weight [D] has the
+rows' type or is FP32.  Rows whose elements are not neighbours, or whose stride differs
+from a dense matrix's by no multiple of 16 bytes, are copied first.  `rms_norm` takes part in autograd; `rms_norm_grad` is its gradient as a
 plain call, which enqueues kernels only.  `rms_norm_fp8` gives E4M3 codes and one FP32
 scale per 128 columns, as fp8.quantize_rows does, from the unrounded y: it rounds and
 has no derivative.  There is no forward-mode derivative.
