@@ -84,6 +84,21 @@ def test_order_of_scores_that_32_bits_cannot_tell_apart():
     assert torch.equal(ids, gate64(l, 8, bias, "sigmoid", True, 1.0)[0])
 
 
+@pytest.mark.parametrize("spread,E", [(1e-6, 128), (1e-7, 20), (3e-7, 300), (1e-5, 64)])
+def test_order_of_clusters_nearer_than_rounding(spread, E):
+    """Scores in clusters a few 32-bit steps wide, around the last chosen place too."""
+    g = torch.Generator().manual_seed(E)
+    centre = torch.randint(0, 6, (200, E), generator=g).float() * 0.5 - 1.5
+    l = (centre + spread * torch.randn((200, E), generator=g)).cuda()
+    bias = (spread * torch.randn(E, generator=g)).cuda()
+    for score in ("sigmoid", "softmax"):
+        for topk in (1, 7, 20):
+            ids, w = gating.topk_gate(l, topk, bias, score, False)
+            rid, rw = gate64(l, topk, bias, score, False, 1.0)
+            assert torch.equal(ids, rid)
+            assert bool(((w.double() - rw).abs() <= rw * 2 * unit(l)).all())
+
+
 def test_masked_rows_infinities_and_nan():
     inf, nan = float("inf"), float("nan")
     l = torch.randn((8, 40), generator=torch.Generator().manual_seed(2)).cuda()
