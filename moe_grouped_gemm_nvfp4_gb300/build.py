@@ -78,7 +78,7 @@ def _build_binding(verbose: bool) -> None:
                                 os.path.join(base, "include", "torch", "csrc", "api", "include"),
                                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"))),
            BINDING_SOURCE, "-o", tmp, f"-L{os.path.join(base, 'lib')}",
-           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or r.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)

@@ -8,12 +8,13 @@
 // raises ValueError, a status other than NVFP4_OK the class given to set_error.
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <initializer_list>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -80,7 +81,8 @@ struct On {
   void same(const Tensor& t) const { need(t.device() == device, "tensors on different devices"); }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(device.index()).stream(); }
   Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    // (past the dispatcher: 0.5 us less an output)
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
   }
 };
 

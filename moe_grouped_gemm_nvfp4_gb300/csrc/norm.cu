@@ -12,7 +12,7 @@
 //
 // Blocks walk the rows.  A thread holds 8, 16 or 32 elements of one, in chunks of 16 bytes, and
 // copies its chunks of the next rows to shared memory meanwhile (asynchronous copies that
-// only it reads: no barrier), two rows on their way (four were no faster).  With one row at
+// only it, or its warp, reads: no barrier), two rows on their way (four were no faster).  With one row at
 // a time an SM had 24 KB on its way: 8192 rows of 6144 BF16 took 51 us, now 39, their
 // gradient with dh 126 us, now 75.  Narrow rows share a block.
 //
@@ -46,7 +46,8 @@ struct NormShape {
 constexpr int kMostDepth = 2;
 
 // The sum over a row's threads of N values, the same in each of them: lanes, then warps
-// in shared memory (which calls of one kernel share: a barrier first).
+// in shared memory.  `part` alternates between two places from row to row: who writes one
+// again has passed the other's barrier, which everybody reaches after reading the first.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int threads, float (*part)[N]) {
 #pragma unroll
@@ -56,7 +57,6 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int threads, float (*part
   if (threads == 32) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = threads >> 5, first = warp / warps * warps;
-  __syncthreads();
   if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) part[warp][i] = v[i];
@@ -109,7 +109,9 @@ __device__ __forceinline__ void cp_wait(int n) {
 
 // A thread's chunks of a row: DT's type, EPT elements, the chunks next to each other
 // (TOGETHER) or a row's threads apart.  Without ALIGNED a row starts `lead` elements after
-// the start of its first chunk.
+// the start of its first chunk.  Copies take neighbouring chunks by neighbouring lanes also
+// where a thread's own chunks lie together: its warp's lanes then copy for each other (own
+// chunks by their lane took every sector of memory twice: codes of 8192 x 6144 82 us).
 template <int DT, int EPT, bool TOGETHER, bool ALIGNED>
 struct Chunks {
   static constexpr int N = elems_per_16b<DT>(), V = EPT / N;
@@ -125,22 +127,31 @@ struct Chunks {
   __device__ __forceinline__ bool in(int i, int j) const {
     return ALIGNED || (column(i) + j >= 0 && column(i) + j < D);
   }
-  // A row's copies to shared memory, `apart` bytes between the chunks' places.
-  __device__ __forceinline__ void copy(uint32_t dst, int apart, const void* base, int64_t ld,
-                                       int64_t row, bool on) const {
+  // Places of the chunk that a thread copies, and of its own, in the block's part for a row.
+  __device__ __forceinline__ int copied(int i) const {
+    return TOGETHER ? (tid & ~31) * V + i * 32 + (tid & 31) : i * threads + tid;
+  }
+  __device__ __forceinline__ uint32_t place(int chunk) const {
+    return (static_cast<int>(threadIdx.x) - tid) * V * 16 + chunk * 16;
+  }
+  // A row's copies to shared memory.
+  __device__ __forceinline__ void copy(uint32_t dst, const void* base, int64_t ld, int64_t row,
+                                       bool on) const {
     const char* p = static_cast<const char*>(base) + row * ld * elem_bytes<DT>();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool go = on && any(i);
-      cp16(dst + i * apart, go ? p + column(i) * elem_bytes<DT>() : static_cast<const char*>(base), go);
+      const int column = copied(i) * N - (ALIGNED ? 0 : lead);
+      const bool go = on && column < D;
+      cp16(dst + place(copied(i)),
+           go ? p + column * elem_bytes<DT>() : static_cast<const char*>(base), go);
     }
   }
-  __device__ __forceinline__ void take(uint32_t src, int apart, Pack<DT, N> (&p)[V]) const {
+  __device__ __forceinline__ void take(uint32_t src, Pack<DT, N> (&p)[V]) const {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(p[i].w[0]), "=r"(p[i].w[1]), "=r"(p[i].w[2]), "=r"(p[i].w[3])
-                   : "r"(src + i * apart) : "memory");
+                   : "r"(src + place(TOGETHER ? tid * V + i : i * threads + tid)) : "memory");
       if (!whole(i)) {                              // what lies outside the row is not the row's
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -204,36 +215,37 @@ __global__ void __maxnreg__(REGS) rms_norm_kernel(const NormArgs a, int threads,
   using C = Chunks<DT, EPT, FP8, ALIGNED>;
   constexpr int N = C::N, V = C::V;
   extern __shared__ uint4 staged[];                 // [depth][arrays][V][threads of the block]
-  __shared__ float part[32][1];
+  __shared__ float part[2][32][1];
   const int sub = threadIdx.x / threads;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
   const C c{threads, static_cast<int>(threadIdx.x) - sub * threads, a.D,
             ALIGNED ? 0 : lead_of<DT>(a.x, a.ld, first + sub)};
-  const int apart = blockDim.x * 16, arrays = a.r ? 2 : 1;
-  const uint32_t mine = smem_u32(staged) + threadIdx.x * 16;
-  auto place = [&](int slot, int array) { return mine + ((slot * arrays + array) * V) * apart; };
+  const int arrays = a.r ? 2 : 1;
+  const uint32_t all = smem_u32(staged), size = blockDim.x * V * 16;
+  auto place = [&](int slot, int array) { return all + (slot * arrays + array) * size; };
   auto copy = [&](int64_t base, int slot) {
     const int64_t row = base + sub;
-    c.copy(place(slot, 0), apart, a.x, a.ld, row, row < a.T);
-    if (a.r) c.copy(place(slot, 1), apart, a.r, a.ld_r, row, row < a.T);
+    c.copy(place(slot, 0), a.x, a.ld, row, row < a.T);
+    if (a.r) c.copy(place(slot, 1), a.r, a.ld_r, row, row < a.T);
     cp_commit();
   };
   for (int i = 0; i < depth; ++i) copy(first + i * step, i);
   float w[EPT];
   c.weights(a.w, a.w_type, w);
-  int slot = 0;
+  int slot = 0, odd = 0;
 #pragma unroll 1
   for (int64_t base = first; base < a.T; base += step) {
     const int64_t row = base + sub;
     const bool on = row < a.T;
     cp_wait(depth - 1);
+    if constexpr (FP8) __syncwarp();                // other lanes' copies
     Pack<DT, N> px[V];
-    c.take(place(slot, 0), apart, px);
+    c.take(place(slot, 0), px);
     float sum[1] = {0.f};
     if (a.r) {
       Pack<DT, N> pr[V];
-      c.take(place(slot, 1), apart, pr);
+      c.take(place(slot, 1), pr);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float f[N];
@@ -247,7 +259,9 @@ __global__ void __maxnreg__(REGS) rms_norm_kernel(const NormArgs a, int threads,
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < N; ++j) sum[0] = fmaf(px[i].get(j), px[i].get(j), sum[0]);
-    row_sum<1>(sum, threads, part);
+    row_sum<1>(sum, threads, part[odd]);
+    odd ^= 1;
+    if constexpr (FP8) __syncwarp();
     copy(base + depth * step, slot);                // the slot has been read
     if (++slot == depth) slot = 0;
     const float rstd = 1.f / sqrtf(sum[0] / static_cast<float>(a.D) + a.eps);
@@ -327,23 +341,24 @@ __global__ void __maxnreg__(REGS) rms_norm_kernel(const NormArgs a, int threads,
 template <int DT, int EPT, bool ALIGNED, int REGS>
 __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int threads, int rows,
                                                        int depth) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using C = Chunks<DT, EPT, false, ALIGNED>;
   constexpr int N = C::N, V = C::V;
   extern __shared__ uint4 staged[];
-  __shared__ float part[32][2];
+  __shared__ float part[2][32][2];
   const int sub = threadIdx.x / threads;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
   const C c{threads, static_cast<int>(threadIdx.x) - sub * threads, a.D,
             ALIGNED ? 0 : lead_of<DT>(a.x, a.ld, first + sub)};
-  const int apart = blockDim.x * 16, arrays = a.r ? 3 : 2;
-  const uint32_t mine = smem_u32(staged) + threadIdx.x * 16;
-  auto place = [&](int slot, int array) { return mine + ((slot * arrays + array) * V) * apart; };
+  const int arrays = a.r ? 3 : 2;
+  const uint32_t all = smem_u32(staged), size = blockDim.x * V * 16;
+  auto place = [&](int slot, int array) { return all + (slot * arrays + array) * size; };
   auto copy = [&](int64_t base, int slot) {
     const int64_t row = base + sub;
-    c.copy(place(slot, 0), apart, a.x, a.ld, row, row < a.T);
-    c.copy(place(slot, 1), apart, a.dy, a.ld_dy, row, row < a.T);
-    if (a.r) c.copy(place(slot, 2), apart, a.r, a.ld_r, row, row < a.T);
+    c.copy(place(slot, 0), a.x, a.ld, row, row < a.T);
+    c.copy(place(slot, 1), a.dy, a.ld_dy, row, row < a.T);
+    if (a.r) c.copy(place(slot, 2), a.r, a.ld_r, row, row < a.T);
     cp_commit();
   };
   for (int i = 0; i < depth; ++i) copy(first + i * step, i);
@@ -352,17 +367,17 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
 #pragma unroll
   for (int i = 0; i < EPT; ++i) dw[i] = 0.f;
   const float over = 1.f / static_cast<float>(a.D);
-  int slot = 0;
+  int slot = 0, odd = 0;
 #pragma unroll 1
   for (int64_t base = first; base < a.T; base += step) {
     const int64_t row = base + sub;
     const bool on = row < a.T;
     cp_wait(depth - 1);
     Pack<DT, N> ph[V], pd[V], pr[V];
-    c.take(place(slot, 0), apart, ph);
-    c.take(place(slot, 1), apart, pd);
+    c.take(place(slot, 0), ph);
+    c.take(place(slot, 1), pd);
     if (a.r) {
-      c.take(place(slot, 2), apart, pr);
+      c.take(place(slot, 2), pr);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) pr[i].zero();
@@ -376,7 +391,8 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
         sum[0] = fmaf(h, h, sum[0]);
         sum[1] = fmaf(pd[i].get(j) * w[i * N + j], h, sum[1]);
       }
-    row_sum<2>(sum, threads, part);
+    row_sum<2>(sum, threads, part[odd]);
+    odd ^= 1;
     copy(base + depth * step, slot);                // the slot has been read
     if (++slot == depth) slot = 0;
     const float rstd = 1.f / sqrtf(sum[0] * over + a.eps);
@@ -398,12 +414,26 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
     }
   }
   cp_wait(0);
-  float* out = a.part + (first + sub) * a.D;
+  // the block's sums: of its rows side by side, where those are several, in their order
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.D;
+  float* all_rows = reinterpret_cast<float*>(staged);            // [rows][D]
+  if (rows > 1) {
+    __syncthreads();
+    out = all_rows + sub * a.D;
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j)
       if (c.any(i) && c.in(i, j)) out[c.column(i) + j] = dw[i * N + j];
+  if (rows > 1) {
+    __syncthreads();
+    for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
+      float v = 0.f;
+      for (int r = 0; r < rows; ++r) v += all_rows[r * a.D + col];
+      a.part[static_cast<int64_t>(blockIdx.x) * a.D + col] = v;
+    }
+  }
 }
 
 // dw[c] = sum of the parts' column c: 32 columns a block, 32 warps on every 32nd part.
@@ -413,7 +443,10 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
+  // launched to overlap the end of the blocks that write the parts
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < D)
+#pragma unroll 8
     for (int p = warp; p < parts; p += 32) v += part[static_cast<int64_t>(p) * D + c];
   sums[warp][lane] = v;
   __syncthreads();
@@ -498,9 +531,16 @@ cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  rms_norm_dw_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.part, s.grid * s.rows, a.D, a.w_type,
-                                                       a.dw);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.D + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = s.grid > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel, static_cast<const float*>(a.part), s.grid, a.D,
+                            a.w_type, a.dw);
 }
 
 template <int DT, int EPT, int REGS, int FP8_REGS, int GRAD_REGS>
@@ -559,8 +599,7 @@ cudaError_t init_norm_attributes() {
 }
 
 int norm_grad_parts(int64_t T, int64_t D, int dtype) {
-  const NormShape s = shape_of(T, D, dtype, kGradArrays, kGradRegs, 1);
-  return s.grid * s.rows;
+  return shape_of(T, D, dtype, kGradArrays, kGradRegs, 1).grid;
 }
 
 cudaError_t launch_rms_norm(const NormArgs& a, int dtype, bool fp8, cudaStream_t s) {
