@@ -93,9 +93,15 @@ __device__ __forceinline__ GateScores gate_scores(const float (&l)[L], int E, in
   return g;
 }
 
-// The choice on 64-bit keys (with a bias): lane j < topk gets the j-th expert.
+// The choice on 64-bit keys (with a bias): lane j < topk gets the j-th expert.  (All by
+// value: a reference would put the caller's logits into memory for every token.)
 template <int L>
-__device__ __noinline__ int gate_choose64(const GateRule& r, const float (&l)[L], float max) {
+struct LaneLogits {
+  float v[L];
+};
+template <int L>
+__device__ __noinline__ int gate_choose64(GateRule r, LaneLogits<L> logits, float max) {
+  const float (&l)[L] = logits.v;
   const int lane = threadIdx.x & 31;
   unsigned long long key[L];
   double inv = 1.0;
@@ -144,28 +150,26 @@ __device__ __noinline__ int gate_choose64(const GateRule& r, const float (&l)[L]
 
 // The order of n <= 32 experts by sigmoid + bias in 64 bits: lane j has expert e, its logit
 // and its score.  One 64-bit exponential a lane; gate_choose64 takes them for all experts.
-__device__ __noinline__ void gate_reorder64(const float* bias, int n, float logit, int* e,
-                                            float* score) {
+__device__ __noinline__ int2 gate_reorder64(const float* bias, int n, float logit, int e,
+                                            float score) {
   const int lane = threadIdx.x & 31;
   const unsigned long long key =
       lane < n ? gate_key64(1.0 / (1.0 + exp(-static_cast<double>(logit))) +
-                            static_cast<double>(__ldg(bias + *e)))
+                            static_cast<double>(__ldg(bias + e)))
                : 0ull;
   int rank = lane < n ? 0 : 32;
   for (int i = 0; i < n; ++i) {
     const unsigned long long k = __shfl_sync(kFullWarp, key, i);
-    const int other = __shfl_sync(kFullWarp, *e, i);
-    if (lane < n && (k > key || (k == key && other < *e))) ++rank;
+    const int other = __shfl_sync(kFullWarp, e, i);
+    if (lane < n && (k > key || (k == key && other < e))) ++rank;
   }
-  int first = *e;
-  float its = *score;
+  int2 mine = make_int2(e, __float_as_int(score));
   for (int i = 0; i < n; ++i) {
-    const int r = __shfl_sync(kFullWarp, rank, i), x = __shfl_sync(kFullWarp, *e, i);
-    const float v = __shfl_sync(kFullWarp, *score, i);
-    if (r == lane) { first = x; its = v; }
+    const int r = __shfl_sync(kFullWarp, rank, i), x = __shfl_sync(kFullWarp, e, i);
+    const float v = __shfl_sync(kFullWarp, score, i);
+    if (r == lane) mine = make_int2(x, __float_as_int(v));
   }
-  *e = first;
-  *score = its;
+  return mine;
 }
 
 // l[i]: logit of expert lane + 32 i, -infinity past E.  Lane j < topk gets the j-th
@@ -272,7 +276,12 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
   if (near) {                                       // the same in every lane
     // (all picks are in lanes, and the last one is clear of what follows, or all are picked)
     const bool few = r.sigmoid && count <= 32 && (!touching || count == r.E);
-    if (!few) mine = gate_choose64<L>(r, l, g.max);
+    if (!few) {
+      LaneLogits<L> row;
+#pragma unroll
+      for (int i = 0; i < L; ++i) row.v[i] = l[i];
+      mine = gate_choose64<L>(r, row, g.max);
+    }
     float logit = 0.f;
     const int n = few ? count : r.topk;
 #pragma unroll 1
@@ -286,7 +295,11 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
       v = __shfl_sync(kFullWarp, v, e & 31);
       if (j == lane) { logit = x; chosen = v; }
     }
-    if (few) gate_reorder64(r.bias, n, logit, &mine, &chosen);
+    if (few) {
+      const int2 m = gate_reorder64(r.bias, n, logit, mine, chosen);
+      mine = m.x;
+      chosen = __int_as_float(m.y);
+    }
   }
   const bool on = lane < r.topk;
   float w = !on ? 0.f : r.bias ? chosen : g.of(chosen);
