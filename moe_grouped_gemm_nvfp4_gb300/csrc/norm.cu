@@ -37,6 +37,8 @@ namespace {
 
 constexpr int kSms = 152;                 // the workspace's size hangs on it
 constexpr int kNormSmem = 200 * 1024;     // of an SM for the rows on their way
+// The widest FP32 gradient begun inside a chunk: 17 warps, three arrays, one row on its way.
+constexpr int kNormSmemMost = 17 * 32 * 32 * 4 * 3;
 
 // Threads of a row, rows of a block, rows on their way.
 struct NormShape {
@@ -546,16 +548,16 @@ cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
 template <int DT, int EPT, int REGS, int FP8_REGS, int GRAD_REGS>
 cudaError_t set_smem() {
   constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, true, REGS>, kAttr, kNormSmem);
+  cudaError_t e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, true, REGS>, kAttr, kNormSmemMost);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, false, REGS>, kAttr, kNormSmem);
+    e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, false, REGS>, kAttr, kNormSmemMost);
   if constexpr (DT != NVFP4_FP32)
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, true, true, FP8_REGS>, kAttr, kNormSmem);
+      e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, true, true, FP8_REGS>, kAttr, kNormSmemMost);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, EPT, true, GRAD_REGS>, kAttr, kNormSmem);
+    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, EPT, true, GRAD_REGS>, kAttr, kNormSmemMost);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, EPT, false, GRAD_REGS>, kAttr, kNormSmem);
+    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, EPT, false, GRAD_REGS>, kAttr, kNormSmemMost);
   return e;
 }
 template <int DT>

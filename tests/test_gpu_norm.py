@@ -231,3 +231,35 @@ def test_linear_of_norm_codes():
         size = (codes.float().double() * sq).abs() @ (wq.float().double() * sw).abs().t()
         assert bool(((y.double() - ref).abs()
                      <= half_step(dtype) * ref.abs() + 400 * 2.0 ** -24 * size).all())
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [16384, 16383, 16382, 16381])
+def test_widest_rows(D, kind):
+    """Up to the limit of the width, also where a row begins inside a chunk of 16 bytes: the
+    norm with residual and the gradient with dh, whose shared memory is then the largest."""
+    g = torch.Generator().manual_seed(D)
+    x, r, dy, dh = (rows(g, 5, D, kind) for _ in range(4))
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(TYPES[kind]).cuda()
+    y, h = norm.rms_norm(x, w, r)
+    ref = y64(h, w, 1e-6)
+    t = x.dtype
+    assert bool(((y.double() - ref).abs() <= ref.abs() * (half_step(t) * (1 + U) + U)).all())
+    dx, dw = norm.rms_norm_grad(dy, h, w, dh)
+    h6 = h.double().requires_grad_()
+    w6 = w.double().requires_grad_()
+    want, want_w = torch.autograd.grad(y64_graph(h6, w6), (h6, w6), dy.double())
+    # dx: the terms' sizes, each with U; the mean of products has D of them
+    rstd = 1 / torch.sqrt(h.double().square().mean(-1, keepdim=True) + 1e-6)
+    g6 = dy.double() * w.double()
+    size = rstd * (g6.abs() + h.double().abs() * rstd.square()
+                   * (g6 * h.double()).abs().mean(-1, keepdim=True)) + dh.double().abs()
+    want = want + dh.double()
+    assert bool(((dx.double() - want).abs() <= half_step(t) * want.abs() + 2 * U * size).all())
+    size_w = (dy.double() * h.double() * rstd).abs().sum(0)
+    assert bool(((dw.double() - want_w).abs()
+                 <= half_step(t) * want_w.abs() + 2 * U * size_w).all())
+
+
+def y64_graph(h, w):
+    return h / torch.sqrt(h.square().mean(-1, keepdim=True) + 1e-6) * w
