@@ -140,12 +140,14 @@ struct Chunks {
   __device__ __forceinline__ void copy(uint32_t dst, const void* base, int64_t ld, int64_t row,
                                        bool on) const {
     const char* p = static_cast<const char*>(base) + row * ld * elem_bytes<DT>();
+    // (an address of 16 bytes also where nothing is read)
+    const char* none = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(base) &
+                                                     ~static_cast<uintptr_t>(15));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int column = copied(i) * N - (ALIGNED ? 0 : lead);
       const bool go = on && column < D;
-      cp16(dst + place(copied(i)),
-           go ? p + column * elem_bytes<DT>() : static_cast<const char*>(base), go);
+      cp16(dst + place(copied(i)), go ? p + column * elem_bytes<DT>() : none, go);
     }
   }
   __device__ __forceinline__ void take(uint32_t src, Pack<DT, N> (&p)[V]) const {
@@ -466,9 +468,10 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, in
 // its latency) or a row has few elements, 16 where rows fill the SMs anyway, 32 for rows
 // that are wider than 512 threads of 16.  Registers a thread: 64, `most`, 96
 // (up to five warps share the 16384 of a quarter of the SM).
-NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int rounds) {
+NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int rounds,
+                   bool aligned) {
   const int es = dtype == NVFP4_FP32 ? 4 : 2;
-  const int64_t width = D % (16 / es) ? D + 16 / es - 1 : D;    // a chunk more, begun anywhere
+  const int64_t width = aligned ? D : D + 16 / es - 1;          // begun anywhere in a chunk
   NormShape s{};
   s.ept = width > 512 * 16 ? 32 : T > 2 * kSms && width > 32 * 4 * 8 ? 16 : 8;
   s.threads = static_cast<int>((width + 32 * s.ept - 1) / (32 * s.ept)) * 32;
@@ -512,7 +515,7 @@ cudaError_t go(const NormArgs& a, const NormShape& s, cudaStream_t st) {
 template <int DT, bool FP8, bool ALIGNED>
 cudaError_t forward(const NormArgs& a, int dtype, cudaStream_t st) {
   constexpr int kRegs = FP8 ? kFp8Regs : kForwardRegs;
-  const NormShape s = shape_of(a.T, a.D, dtype, forward_arrays(a), kRegs, FP8 ? 1 : 4);
+  const NormShape s = shape_of(a.T, a.D, dtype, forward_arrays(a), kRegs, FP8 ? 1 : 4, ALIGNED);
   if (s.ept == 8) return go<DT, 8, FP8, ALIGNED, 64>(a, s, st);
   if (s.ept == 16) return go<DT, 16, FP8, ALIGNED, kRegs>(a, s, st);
   return go<DT, 32, FP8, ALIGNED, 96>(a, s, st);
@@ -525,7 +528,7 @@ void go_grad(const NormArgs& a, const NormShape& s, cudaStream_t st) {
 }
 template <int DT, bool ALIGNED>
 cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
-  const NormShape s = shape_of(a.T, a.D, dtype, kGradArrays, kGradRegs, 1);
+  const NormShape s = shape_of(a.T, a.D, dtype, kGradArrays, kGradRegs, 1, ALIGNED);
   if (s.grid > 0) {
     if (s.ept == 8) go_grad<DT, 8, ALIGNED, 64>(a, s, st);
     else if (s.ept == 16) go_grad<DT, 16, ALIGNED, kGradRegs>(a, s, st);
@@ -601,7 +604,10 @@ cudaError_t init_norm_attributes() {
 }
 
 int norm_grad_parts(int64_t T, int64_t D, int dtype) {
-  return shape_of(T, D, dtype, kGradArrays, kGradRegs, 1).grid;
+  const int other = shape_of(T, D, dtype, kGradArrays, kGradRegs, 1, false).grid;
+  if (D % (dtype == NVFP4_FP32 ? 4 : 8)) return other;
+  const int whole = shape_of(T, D, dtype, kGradArrays, kGradRegs, 1, true).grid;
+  return whole > other ? whole : other;
 }
 
 cudaError_t launch_rms_norm(const NormArgs& a, int dtype, bool fp8, cudaStream_t s) {

@@ -263,3 +263,46 @@ def test_widest_rows(D, kind):
 
 def y64_graph(h, w):
     return h / torch.sqrt(h.square().mean(-1, keepdim=True) + 1e-6) * w
+
+
+def inside(t, off):
+    """A copy of t (dense) that begins `off` elements after a multiple of 16 bytes."""
+    flat = torch.empty(t.numel() + off + 64, dtype=t.dtype, device="cuda")
+    view = flat[off:off + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("kind,off", [("fp32", 1), ("bf16", 3), ("fp16", 7)])
+@pytest.mark.parametrize("T,D", [(1, 8), (5, 256), (400, 256), (700, 512), (320, 4096),
+                                 (3, 16384)])
+def test_rows_begun_inside_a_chunk(T, D, kind, off):
+    """The library's own calls on matrices that all begin inside 16 bytes, of widths that fill
+    their threads: one chunk more a row.  Elements before and after y keep their values."""
+    g = torch.Generator().manual_seed(D + off)
+    x, r, dy, dh = (inside(rows(g, T, D, kind), off) for _ in range(4))
+    w = (1 + 0.3 * torch.randn(D, generator=g)).cuda()
+    t = x.dtype
+    around = [torch.full((T * D + off + 64,), 7.0, dtype=t, device="cuda") for _ in range(3)]
+    h, y, dx = (a[off:off + T * D].view(T, D) for a in around)
+    F.nvfp4_rms_norm(x, r, w, 1e-5, h, y)
+    dw = torch.empty(D, device="cuda")
+    ws = torch.empty(F.nvfp4_rms_norm_grad_workspace_bytes(T, D), dtype=torch.uint8, device="cuda")
+    F.nvfp4_rms_norm_grad(dy, h, dh, w, 1e-5, dx, dw, ws)
+    torch.cuda.synchronize()
+    for a in around:
+        assert bool((a[:off] == 7).all()) and bool((a[off + T * D:] == 7).all())
+    assert torch.equal(h, (x.float() + r.float()).to(t))
+    ref = y64(h, w, 1e-5)
+    assert bool(((y.double() - ref).abs() <= ref.abs() * (half_step(t) * (1 + U) + U) + TINY[t]).all())
+    # the aligned call differs in the order of its sums only
+    ex, ew = norm.rms_norm_grad(dy.clone(), h.clone(), w, dh.clone(), eps=1e-5)
+    rstd = 1 / torch.sqrt(h.double().square().mean(-1, keepdim=True) + 1e-5)
+    g6 = dy.double() * w.double()
+    size = rstd * (g6.abs() + h.double().abs() * rstd.square()
+                   * (g6 * h.double()).abs().mean(-1, keepdim=True)) + dh.double().abs()
+    # (each is half a step from a value of its own, and those are 4 U of the sizes apart)
+    assert bool(((dx.double() - ex.double()).abs()
+                 <= 2 * half_step(t) * ex.double().abs() * 1.01 + 4 * U * size + 2 * TINY[t]).all())
+    size_w = (dy.double() * h.double() * rstd).abs().sum(0)
+    assert bool(((dw.double() - ew.double()).abs() <= 4 * U * size_w).all())
