@@ -25,8 +25,7 @@
 // * Blocks take runs by a counter, all of gate_up's before the first of down's, and a down
 //   run waits (bounded) until all gate_up runs are done.  Those are then in the hands of
 //   blocks that run, so that no block has to wait for one that has not started: a plain
-//   launch, whatever else is on the GPU.  (As one cooperative launch with grid barriers a
-//   call took 9 us more: its launch, and every SM waiting for the slowest one twice.)
+//   launch, whatever else is on the GPU.
 // * Six stages are on their way (192 KB an SM).  When a block has asked for all its gate_up
 //   tiles, its producer takes its down run and goes on with the weights of the first down
 //   tiles, before it waits for the codes of h: HBM does not idle there.
@@ -34,9 +33,12 @@
 //   memory, which four warps read and add as FP32 times the factor (weight scale * token
 //   scale, for down also * routing weight) that a warp of its own lays out.
 //
-// (A first form with mma.sync, eight warps with rings of their own: it spent 280
-// instructions on 2 KB of weights, converting codes, and reached 4.3 TB/s: one token
-// through 128 experts of 6144 x 2048, eight of them chosen, in 96 us.)
+// Measured in a graph, 128 experts, 8 chosen: 6144 x 2048 one token 64 us (302 MB of weights,
+// 0.69 of the copy rate; about 9 us pass before the first weights are asked for, and 6 behind
+// the last ones), 2 tokens 106, 4 tokens 175, 8 tokens 300 us (1.9 GB, 0.94); 2048 x 768 28, 34,
+// 49 and 65 us.  A first form with mma.sync, eight warps with rings of their own, spent 280
+// instructions on 2 KB of weights, converting codes: one token 96 us.  One cooperative launch
+// with the router in it, between grid barriers, instead of the two: 68 us.
 #include "fp8_common.cuh"
 #include "fp8_moe.h"
 #include "fp8_quant.cuh"
@@ -274,7 +276,7 @@ struct Producer {
   uint64_t wpol, tpol;
 
   __device__ __forceinline__ void weights(const Phase& p, const Cursor& c, int s) const {
-      const int e = rt.live[c.x];
+    const int e = rt.live[c.x];
     mbar_arrive_expect_tx(b.full(s), kStageBytes);
     if (p.down) {
       tma_load_3d(b.stage(s), w, b.full(s), c.kb * 128, c.unit * 256, e, wpol);
@@ -493,7 +495,7 @@ struct Epilogue {
   }
 
   __device__ __forceinline__ bool add(const Phase& p, const Run& run, Ring& acc, bool warm) {
-      const uint32_t lanes = b.tmem + (static_cast<uint32_t>(r >> 5) << 21);
+    const uint32_t lanes = b.tmem + (static_cast<uint32_t>(r >> 5) << 21);
     Cursor c;
     c.at(p, run.first);
     int item = run.first / p.per_item, inner = run.first - item * p.per_item;
@@ -643,6 +645,12 @@ __device__ __forceinline__ void gate_token(const Fp8MoeArgs& a, Routes& rt, int 
       a.ids[r] = id;
       a.weights[r] = w;
     }
+    if (a.T == 1) {                         // its experts are distinct: no list to make
+      rt.live[r] = static_cast<int16_t>(id);
+      rt.start[r] = rt.route[r] = static_cast<int16_t>(r);
+      rt.tokens[r] = 1u;
+      if (r == 0) rt.n_live = a.rule.topk;
+    }
   }
 }
 
@@ -790,6 +798,14 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     tmem_relinquish();
   }
   tc_fence_before();
+  auto set_phase = [&](int live) {
+    if (warp == 0 && lane < 2)
+      phase[lane].set(lane, ((lane ? a.I : a.K) + 127) / 128, lane ? units2 : units1, live);
+  };
+  // One token of the gate has topk experts: its phases are known now, and it needs no list
+  // (both between the choice and the first weights otherwise: 64.5 -> 63.6 us).
+  const bool one = a.T == 1 && a.router;
+  if (one) set_phase(a.rule.topk);
   grid_dependency_wait();
   uint32_t ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(a.counters, 1u);     // on its way meanwhile
@@ -810,10 +826,11 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     }
   }
   __syncthreads();
-  list_experts(a, rt, bits, scan);
-  if (warp == 0 && lane < 2)
-    phase[lane].set(lane, ((lane ? a.I : a.K) + 127) / 128, lane ? units2 : units1, rt.n_live);
-  __syncthreads();
+  if (!one) {
+    list_experts(a, rt, bits, scan);
+    set_phase(rt.n_live);
+    __syncthreads();
+  }
   tc_fence_after();
   b.tmem = *tmem_slot;
   Runs runs{b, run_slots};
@@ -975,7 +992,7 @@ bool fp8_moe_layout(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, in
   take(T * E * 4);
   m->xq = take(m->columns * m->ld_xq);
   m->xs = take(kx * m->columns * 4);
-  // (one expert more: see Epilogue::run)
+  // (one expert more: what Epilogue::add warms up on)
   m->hq = take((live + 1) * m->columns * m->ld_hq);
   m->hs = take((live + 1) * kh * m->columns * 4);
   m->part = take(static_cast<int64_t>(2) * kMoeMaxGrid * 2 * m->columns * 128 * 4);

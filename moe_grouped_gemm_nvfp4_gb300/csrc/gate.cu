@@ -7,8 +7,16 @@
 //
 // The sum vanishes for renormalised softmax weights: like the sigmoid's, that
 // gradient is zero outside the chosen experts and needs no other logits, so only the
-// chosen ones are read.  Bound: latency up to some thousand tokens, then HBM (the
-// logits once, the gradient's rows once).
+// chosen ones are read.
+//
+// Bound: the gate's latency up to some thousand tokens (a chain of topk reductions over the
+// warp), then its instructions; its bytes (the logits once) would take a tenth of the time.
+// The gradient: latency, then its instructions (its rows are written once, logits read where
+// they are needed; a quarter to a third of the copy rate).
+// In a graph, FP32 logits, 8 chosen: one token of 128 experts 2.9 us (with a bias 4.3 to 4.5),
+// 8192 tokens of 128 7.1 us (sigmoid with a bias 10, softmax with one 17: its near sums are
+// ordered on 64-bit keys of all experts), of 256 11 us, 65536 of 128 42 us; the gradient 2.1
+// to 2.7, 3.9 to 5.5 (128 experts), 4.9 to 8.0 (256) and 19 to 29 us.
 #include <cuda_fp16.h>
 
 #include "gate.h"

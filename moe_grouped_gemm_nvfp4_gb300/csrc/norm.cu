@@ -10,11 +10,12 @@
 // so every byte moves once.  The output is y in the rows' type or, for the FP8 products,
 // E4M3 codes with one scale per 128 columns, taken from the unrounded y (one rounding).
 //
-// Blocks walk the rows.  A thread holds 8, 16 or 32 elements of one, in chunks of 16 bytes, and
-// copies its chunks of the next rows to shared memory meanwhile (asynchronous copies that
-// only it, or its warp, reads: no barrier), two rows on their way (four were no faster).  With one row at
-// a time an SM had 24 KB on its way: 8192 rows of 6144 BF16 took 51 us, now 39, their
-// gradient with dh 126 us, now 75.  Narrow rows share a block.
+// Blocks walk the rows.  A thread holds 8, 16 or 32 elements of one, in chunks of 16 bytes,
+// and copies its chunks of the next rows to shared memory meanwhile (asynchronous copies
+// that only it, or its warp, reads: no barrier), two rows on their way (four were no faster,
+// with a residual or without).  With one row at a time an SM had 24 KB on its way: 8192 rows
+// of 6144 BF16 took 51 us, now 41, their gradient with dh 126 us, now 74.  Narrow rows share a
+// block.
 //
 // Where rows are no multiple of 16 bytes apart, chunks are the aligned ones of memory: all
 // tensors of a call have their rows at the same offset in a chunk (the first and last chunk
@@ -25,9 +26,12 @@
 // every row), writes them once, and a second launch adds the blocks' in order.  No
 // atomics: results repeat bit for bit.  Sums are FP32.
 //
-// Bound: HBM; 8192 x 6144 BF16 with residual 65 us (0.91 of the copy rate), its gradient with
-// dh 75 us (0.79), the codes with residual 85 us (0.61: half of the issue slots go to the
-// quotients, conversions and maxima, and the scales' rows are written four bytes at a time).
+// Bound: HBM.  8192 x 6144 BF16, and its part of the measured copy rate: norm 41 us (0.73: a
+// row's latency, of copies, sums and stores, on the 24 warps that the registers leave room
+// for; FP32 rows, twice the bytes, 65 us, 0.91), with residual 65 us (0.91), codes with
+// residual 61 us (0.85), gradient 69 us (0.64), with dh 74 us (0.80).  8192 x 6143: 59, 80, -,
+// 88 and 97 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 7.0:
+// latency.  In a graph, one call after the other.
 #include "fp8_quant.cuh"
 #include "norm.h"
 
@@ -113,7 +117,7 @@ __device__ __forceinline__ void cp_wait(int n) {
 // (TOGETHER) or a row's threads apart.  Without ALIGNED a row starts `lead` elements after
 // the start of its first chunk.  Copies take neighbouring chunks by neighbouring lanes also
 // where a thread's own chunks lie together: its warp's lanes then copy for each other (own
-// chunks by their lane took every sector of memory twice: codes of 8192 x 6144 82 us).
+// chunks by their lane took every sector of memory twice: codes of 8192 x 6144 85 -> 61 us).
 template <int DT, int EPT, bool TOGETHER, bool ALIGNED>
 struct Chunks {
   static constexpr int N = elems_per_16b<DT>(), V = EPT / N;
@@ -492,7 +496,7 @@ NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int ro
   int64_t grid = static_cast<int64_t>(kSms) * per_sm;
   // Many rows: several rounds of blocks, since SMs are not equally fast (norm with residual
   // of 8192 x 6144 72 -> 65 us); not where one block fills an SM (4096 x 8192 47 -> 50 us),
-  // nor for the codes (85 -> 89 us).
+  // nor for the codes.
   if (rounds > 1 && per_sm > 1 && want >= 4 * rounds * grid) grid *= rounds;
   s.grid = static_cast<int>(want < grid ? want : grid);
   const int64_t steps = s.grid > 0 ? (want + s.grid - 1) / s.grid : 1;
