@@ -679,8 +679,9 @@ nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, in
  *   h = x + residual            rounded to the rows' type (without a residual: x)
  *   y = h / sqrt(mean(h^2) + eps) * weight
  *
- * FP32 arithmetic on the stored h, one rounding.  x and residual [T, D], row
- * stride >= D; h and y dense; weight [D] of weight_dtype: the rows' type or FP32.
+ * FP32 arithmetic on the stored h, one rounding (a sum of squares past FP32's range
+ * counts as infinity).  x and residual [T, D], row stride >= D; h and y dense;
+ * weight [D] of weight_dtype: the rows' type or FP32.
  * 1 <= D <= 16384, eps >= 0.  A row of any operand lies at the same offset within
  * 16 bytes as that row of the others (dense matrices with 16-byte aligned bases
  * do, of any width); NVFP4_ERR_UNSUPPORTED otherwise.  The 16-byte granules that

@@ -21,7 +21,8 @@
 //   that falls: a token's eight experts have some thousands of tiles, and every SM streams
 //   the same bytes.  An item (128 columns of one expert's h; 256 output columns over all
 //   experts) whose tiles lie in several runs is joined by the last run to finish, which
-//   adds the parts in the order of the runs.
+//   adds the parts in the order of the runs.  (Two to eight shorter runs a block, for SMs that
+//   are not equally fast: the joins cost more, 8 tokens 308 -> 311 to 333 us.)
 // * Blocks take runs by a counter, all of gate_up's before the first of down's, and a down
 //   run waits (bounded) until all gate_up runs are done.  Those are then in the hands of
 //   blocks that run, so that no block has to wait for one that has not started: a plain
@@ -34,9 +35,9 @@
 //   scale, for down also * routing weight) that a warp of its own lays out.
 //
 // Measured in a graph, 128 experts, 8 chosen: 6144 x 2048 one token 64 us (302 MB of weights,
-// 0.69 of the copy rate; about 9 us pass before the first weights are asked for, and 6 behind
-// the last ones), 2 tokens 106, 4 tokens 175, 8 tokens 300 us (1.9 GB, 0.94); 2048 x 768 28, 34,
-// 49 and 65 us.  A first form with mma.sync, eight warps with rings of their own, spent 280
+// 0.70 of the copy rate; about 8 us pass before the first weights are asked for, and 6 behind
+// the last ones), 2 tokens 106, 4 tokens 179, 8 tokens 303 us (1.9 GB, 0.93); 2048 x 768 27, 34,
+// 49 and 66 us.  A first form with mma.sync, eight warps with rings of their own, spent 280
 // instructions on 2 KB of weights, converting codes: one token 96 us.  One cooperative launch
 // with the router in it, between grid barriers, instead of the two: 68 us.
 #include "fp8_common.cuh"

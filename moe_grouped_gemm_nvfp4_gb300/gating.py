@@ -10,7 +10,7 @@ compared in FP64.
 
 `topk_gate` takes part in autograd (the gradient of the logits; the choice and the bias
 have none); `topk_gate_grad` is the gradient as a plain call, which enqueues kernels
-only.  Logits are BF16, FP16 or FP32 [T, E] of any row stride, at most 1024 experts and
+only (the one for a captured step).  Logits are BF16, FP16 or FP32 [T, E] of any row stride, at most 1024 experts and
 32 chosen ones.  There is no forward-mode derivative.
 
 Work goes to the current stream of the tensors' device, whichever device is current,

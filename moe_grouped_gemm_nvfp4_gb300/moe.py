@@ -358,9 +358,9 @@ class Fp8MLP:
 
     def step_few(self, x, topk_ids, topk_weights, stream=None):
         """step() of at most 8 tokens (ValueError for more) in one call of the library,
-        without a route-ordered copy of anything.  gate_up's product and the experts' rows stay FP32 here,
-        where step() rounds them to x's type.  An expert that a token names twice counts
-        with both weights."""
+        without a route-ordered copy of anything.  gate_up's product and the experts'
+        rows stay FP32 here, where step() rounds them to x's type.  An expert that a
+        token names twice counts with both weights."""
         if forward_ad._current_level >= 0:
             tokens.refuse_tangents(x, topk_weights, *self.gate_up, *self.down)
         if stream is not None:
@@ -381,8 +381,8 @@ class Fp8MoE:
     bias, score, renormalize and scale are the gate's (gating.topk_gate).
 
     step() of at most 8 tokens is one call of the library
-    (nvfp4.nvfp4_fp8_moe_layer).  More go through
-    the router's product with FP32 logits, gating.topk_gate and Fp8MLP.step, whose
+    (nvfp4.nvfp4_fp8_moe_layer).  More go through the router's product with FP32
+    logits, gating.topk_gate and Fp8MLP.step, whose
     gate_up product and expert rows are rounded to the tokens' type; the router's
     sums also have another order, which can change the choice between nearly equal
     logits.  Both enqueue kernels only and keep no buffers; the experts are frozen

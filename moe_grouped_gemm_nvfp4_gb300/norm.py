@@ -6,10 +6,14 @@ and with 8-bit output for the FP8 products.
 
 Rows [.., D] are BF16, FP16 or FP32 of any width up to 16384; the weight [D] has the
 rows' type or is FP32.  Rows whose elements are not neighbours, or whose stride differs
-from a dense matrix's by no multiple of 16 bytes, are copied first.  `rms_norm` takes part in autograd; `rms_norm_grad` is its gradient as a
-plain call, which enqueues kernels only.  `rms_norm_fp8` gives E4M3 codes and one FP32
-scale per 128 columns, as fp8.quantize_rows does, from the unrounded y: it rounds and
-has no derivative.  There is no forward-mode derivative.
+from a dense matrix's by no multiple of 16 bytes, are copied first.  The squares are FP32:
+rows whose sum of squares leaves its range (elements from about 2^63 on) have rstd 0.
+
+`rms_norm` takes part in autograd; `rms_norm_grad` is its gradient as a plain call, which
+enqueues kernels only (the one for a captured step: autograd's own bookkeeping can use other
+streams).  `rms_norm_fp8` gives E4M3 codes and one FP32 scale per 128 columns, as
+fp8.quantize_rows does, from the unrounded y: it rounds and has no derivative.  There is no
+forward-mode derivative.
 
 Work goes to the current stream of the tensors' device, whichever device is current,
 or to `stream` (a torch stream of that device or a raw handle).
