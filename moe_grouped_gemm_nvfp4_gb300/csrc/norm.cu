@@ -154,23 +154,24 @@ struct Chunks {
       cp16(dst + place(copied(i)), go ? p + column * elem_bytes<DT>() : none, go);
     }
   }
-  __device__ __forceinline__ void take(uint32_t src, Pack<DT, N> (&p)[V]) const {
+  __device__ __forceinline__ void take(uint32_t src, int i, Pack<DT, N>& p) const {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(p.w[0]), "=r"(p.w[1]), "=r"(p.w[2]), "=r"(p.w[3])
+                 : "r"(src + place(TOGETHER ? tid * V + i : i * threads + tid)) : "memory");
+    if (!whole(i)) {                                // what lies outside the row is not the row's
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(p[i].w[0]), "=r"(p[i].w[1]), "=r"(p[i].w[2]), "=r"(p[i].w[3])
-                   : "r"(src + place(TOGETHER ? tid * V + i : i * threads + tid)) : "memory");
-      if (!whole(i)) {                              // what lies outside the row is not the row's
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if constexpr (N == 4) {
-            if (!in(i, w)) p[i].w[w] = 0u;
-          } else {
-            p[i].w[w] &= (in(i, 2 * w) ? 0xFFFFu : 0u) | (in(i, 2 * w + 1) ? 0xFFFF0000u : 0u);
-          }
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (N == 4) {
+          if (!in(i, w)) p.w[w] = 0u;
+        } else {
+          p.w[w] &= (in(i, 2 * w) ? 0xFFFFu : 0u) | (in(i, 2 * w + 1) ? 0xFFFF0000u : 0u);
         }
       }
     }
+  }
+  __device__ __forceinline__ void take(uint32_t src, Pack<DT, N> (&p)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) take(src, i, p[i]);
   }
   __device__ __forceinline__ void put(void* base, int64_t row, int i, const Pack<DT, N>& p) const {
     using Bits = typename Elem<DT>::Bits;
@@ -352,6 +353,11 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using C = Chunks<DT, EPT, false, ALIGNED>;
   constexpr int N = C::N, V = C::V;
+  // dh is taken with the others, so that the slot's next copies start at once (8192 x 6144
+  // 78 -> 74 us); masked chunks take it behind the sums, when fewer registers are in use (8192
+  // x 6143 97 -> 91 us).  32 elements a thread and their weights and sums leave no registers
+  // for a row: it is read from shared memory again behind the sums (4096 x 12288 216 -> 84 us).
+  constexpr bool kKept = EPT < 32, kEarly = ALIGNED && kKept;
   extern __shared__ uint4 staged[];
   __shared__ float part[2][32][2];
   const int sub = threadIdx.x / threads;
@@ -382,31 +388,39 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
     const bool on = row < a.T;
     cp_wait(depth - 1);
     Pack<DT, N> ph[V], pd[V], pr[V];
-    c.take(place(slot, 0), ph);
-    c.take(place(slot, 1), pd);
-    if (a.r) {
-      c.take(place(slot, 2), pr);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) pr[i].zero();
-    }
+    auto take_dh = [&](int i) {
+      if (a.r) c.take(place(slot, 2), i, pr[i]);
+      else pr[i].zero();
+    };
+    auto next = [&] {                               // the slot has been read
+      copy(base + depth * step, slot);
+      if (++slot == depth) slot = 0;
+    };
     float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+      c.take(place(slot, 0), i, ph[i]);
+      c.take(place(slot, 1), i, pd[i]);
+      if constexpr (kEarly) take_dh(i);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float h = ph[i].get(j);
         sum[0] = fmaf(h, h, sum[0]);
         sum[1] = fmaf(pd[i].get(j) * w[i * N + j], h, sum[1]);
       }
+    }
     row_sum<2>(sum, threads, part[odd]);
     odd ^= 1;
-    copy(base + depth * step, slot);                // the slot has been read
-    if (++slot == depth) slot = 0;
+    if constexpr (kEarly) next();
     const float rstd = 1.f / sqrtf(sum[0] * over + a.eps);
     const float back = rstd * rstd * (sum[1] * over);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      if constexpr (!kKept) {
+        c.take(place(slot, 0), i, ph[i]);
+        c.take(place(slot, 1), i, pd[i]);
+      }
+      if constexpr (!kEarly) take_dh(i);
       float f[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) {
@@ -420,6 +434,7 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
         c.put(a.y, row, i, p);
       }
     }
+    if constexpr (!kEarly) next();
   }
   cp_wait(0);
   // the block's sums: of its rows side by side, where those are several, in their order
