@@ -50,6 +50,8 @@ struct NormShape {
   size_t smem;
 };
 constexpr int kMostDepth = 2;
+constexpr int kForwardRegs = 80, kFp8Regs = 80, kGradRegs = 128;       // of 16 elements
+constexpr int kWideRegs = 96, kWideFp8Regs = 128;                      // of 32
 
 // The sum over a row's threads of N values, the same in each of them: lanes, then warps
 // in shared memory.  `part` alternates between two places from row to row: who writes one
@@ -484,19 +486,23 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, in
 }
 
 // Elements a thread takes of a row: 8 while there are few rows (a row's time is then
-// its latency) or a row has few elements, 16 where rows fill the SMs anyway, 32 for rows
-// that are wider than 512 threads of 16.  Registers a thread: 64, `most`, 96
-// (up to five warps share the 16384 of a quarter of the SM).
+// its latency) or a row has few elements, 16 where rows fill the SMs anyway or 1024 threads
+// of 8 are too narrow, 32 for rows that are wider than the threads of 16 that an SM has
+// registers for: 768 of 80 (codes with residual of 4096 x 12288 64 us, by 32 elements 96), 512
+// of 128.  Registers a thread: 64, `most`, kWideRegs for the grid (up to five warps share the
+// 16384 of a quarter of the SM; codes have up to four, and 128 registers).
 NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int rounds,
                    bool aligned) {
   const int es = dtype == NVFP4_FP32 ? 4 : 2;
   const int64_t width = aligned ? D : D + 16 / es - 1;          // begun anywhere in a chunk
   NormShape s{};
-  s.ept = width > 512 * 16 ? 32 : T > 2 * kSms && width > 32 * 4 * 8 ? 16 : 8;
+  const int widest = (most <= 80 ? 768 : 512) * 16;
+  const bool many = T > 2 * kSms && width > 32 * 4 * 8;
+  s.ept = width > widest ? 32 : many || width > 1024 * 8 ? 16 : 8;
   s.threads = static_cast<int>((width + 32 * s.ept - 1) / (32 * s.ept)) * 32;
   s.rows = s.threads >= 256 ? 1 : 256 / s.threads;
   const int block = s.threads * s.rows;
-  const int regs = s.ept == 8 ? 64 : s.ept == 16 ? most : 96;
+  const int regs = s.ept == 8 ? 64 : s.ept == 16 ? most : kWideRegs;
   int per_sm = 16384 / (regs * 32 * ((block + 127) / 128));
   if (per_sm > 2048 / block) per_sm = 2048 / block;
   if (per_sm > 8) per_sm = 8;
@@ -520,7 +526,6 @@ NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int ro
   s.smem = static_cast<size_t>(row_bytes) * s.depth;
   return s;
 }
-constexpr int kForwardRegs = 80, kFp8Regs = 80, kGradRegs = 128;
 int forward_arrays(const NormArgs& a) { return a.r ? 2 : 1; }
 // (with or without dh the same shape: the workspace's size hangs on it)
 constexpr int kGradArrays = 3;
@@ -537,7 +542,7 @@ cudaError_t forward(const NormArgs& a, int dtype, cudaStream_t st) {
   const NormShape s = shape_of(a.T, a.D, dtype, forward_arrays(a), kRegs, FP8 ? 1 : 4, ALIGNED);
   if (s.ept == 8) return go<DT, 8, FP8, ALIGNED, 64>(a, s, st);
   if (s.ept == 16) return go<DT, 16, FP8, ALIGNED, kRegs>(a, s, st);
-  return go<DT, 32, FP8, ALIGNED, 96>(a, s, st);
+  return go<DT, 32, FP8, ALIGNED, FP8 ? kWideFp8Regs : kWideRegs>(a, s, st);
 }
 
 template <int DT, int EPT, bool ALIGNED, int REGS>
@@ -551,7 +556,7 @@ cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
   if (s.grid > 0) {
     if (s.ept == 8) go_grad<DT, 8, ALIGNED, 64>(a, s, st);
     else if (s.ept == 16) go_grad<DT, 16, ALIGNED, kGradRegs>(a, s, st);
-    else go_grad<DT, 32, ALIGNED, 96>(a, s, st);
+    else go_grad<DT, 32, ALIGNED, kWideRegs>(a, s, st);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -585,7 +590,7 @@ cudaError_t set_smem() {
 template <int DT>
 cudaError_t set_all() {
   cudaError_t e = set_smem<DT, 8, 64, 64, 64>();
-  if (e == cudaSuccess) e = set_smem<DT, 32, 96, 96, 96>();
+  if (e == cudaSuccess) e = set_smem<DT, 32, kWideRegs, kWideFp8Regs, kWideRegs>();
   if (e == cudaSuccess) e = set_smem<DT, 16, kForwardRegs, kFp8Regs, kGradRegs>();
   return e;
 }

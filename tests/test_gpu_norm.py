@@ -306,3 +306,39 @@ def test_rows_begun_inside_a_chunk(T, D, kind, off):
                  <= 2 * half_step(t) * ex.double().abs() * 1.01 + 4 * U * size + 2 * TINY[t]).all())
     size_w = (dy.double() * h.double() * rstd).abs().sum(0)
     assert bool(((dw.double() - ew.double()).abs() <= 4 * U * size_w).all())
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,D", [(5, 8185), (5, 8192), (5, 8200), (400, 8200), (5, 12281),
+                                 (310, 12288), (5, 12288), (5, 12304), (310, 12304)])
+def test_rows_at_the_limits_of_a_block(T, D, kind):
+    """Around the widths at which a row's threads take more elements each; few rows and many."""
+    g = torch.Generator().manual_seed(T + D)
+    x, r, dy = (rows(g, T, D, kind) for _ in range(3))
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(TYPES[kind]).cuda()
+    t = x.dtype
+    y, h = norm.rms_norm(x, w, r)
+    ref = y64(h, w, 1e-6)
+    assert bool(((y.double() - ref).abs() <= ref.abs() * (half_step(t) * (1 + U) + U)).all())
+    ref = y64(x, w, 1e-6)
+    assert bool(((norm.rms_norm(x, w).double() - ref).abs()
+                 <= ref.abs() * (half_step(t) * (1 + U) + U)).all())
+    dx, dw = norm.rms_norm_grad(dy, x, w)
+    x6, w6 = x.double().requires_grad_(), w.double().requires_grad_()
+    want, want_w = torch.autograd.grad(y64_graph(x6, w6), (x6, w6), dy.double())
+    rstd = 1 / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+    g6 = dy.double() * w.double()
+    size = rstd * (g6.abs() + x.double().abs() * rstd.square()
+                   * (g6 * x.double()).abs().mean(-1, keepdim=True))
+    assert bool(((dx.double() - want).abs() <= half_step(t) * want.abs() + 2 * U * size).all())
+    size_w = (dy.double() * x.double() * rstd).abs().sum(0)
+    assert bool(((dw.double() - want_w).abs()
+                 <= half_step(t) * want_w.abs() + 2 * U * size_w).all())
+    if kind == "bf16" and D % 16 == 0:
+        codes, scales, h2 = norm.rms_norm_fp8(x, w, r)
+        assert torch.equal(h2, h)
+        ref = y64(h, w, 1e-6)
+        wide = scales.double().repeat_interleave(128, 0)[:D].t()
+        # half a step of E4M3: 2^-4 of the value, at least half the smallest step, 2^-10
+        assert bool(((codes.float().double() * wide - ref).abs()
+                     <= ref.abs() * 2.0 ** -4 * (1 + U) + 2.0 ** -10 * wide + U * ref.abs()).all())
