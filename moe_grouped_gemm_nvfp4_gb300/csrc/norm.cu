@@ -30,7 +30,7 @@
 // row's latency, of copies, sums and stores, on the 24 warps that the registers leave room
 // for; FP32 rows, twice the bytes, 65 us, 0.91), with residual 65 us (0.91), codes with
 // residual 61 us (0.85), gradient 69 us (0.64), with dh 74 us (0.80).  8192 x 6143: 59, 80, -,
-// 88 and 97 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 7.0:
+// 82 and 91 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 7.0:
 // latency.  In a graph, one call after the other.
 #include "fp8_quant.cuh"
 #include "norm.h"
