@@ -814,6 +814,7 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     if (warp < a.T) {
       if (a.rule.E <= 128) gate_token<4>(a, rt, warp);
       else if (a.rule.E <= 256) gate_token<8>(a, rt, warp);
+      else if (a.rule.E <= 512) gate_token<16>(a, rt, warp);
       else gate_token<32>(a, rt, warp);
     }
   } else {

@@ -15,8 +15,9 @@
 // they are needed; a quarter to a third of the copy rate).
 // In a graph, FP32 logits, 8 chosen: one token of 128 experts 2.9 us (with a bias 4.3 to 4.5),
 // 8192 tokens of 128 7.1 us (sigmoid with a bias 10, softmax with one 17: its near sums are
-// ordered on 64-bit keys of all experts), of 256 11 us, 65536 of 128 42 us; the gradient 2.1
-// to 2.7, 3.9 to 5.5 (128 experts), 4.9 to 8.0 (256) and 19 to 29 us.
+// ordered on 64-bit keys of all experts), of 256 11 us, of 512 22 us (as 1024 are done: 59),
+// 65536 of 128 42 us; the gradient 2.1 to 2.7, 3.9 to 5.5 (128 experts), 4.9 to 8.0 (256) and 19
+// to 29 us.
 #include <cuda_fp16.h>
 
 #include "gate.h"
@@ -34,11 +35,17 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const GateArgs a, i
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   if (t >= a.T) return;
   float l[L];
+  auto load = [&](int of) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < a.rule.E ? gate_logit(a.logits, t * a.ld + e, type) : -INFINITY;
-  }
+    for (int i = 0; i < L; ++i) {
+      const int e = lane + 32 * i;
+      l[i] = e < a.rule.E ? gate_logit(a.logits, t * a.ld + e, of) : -INFINITY;
+    }
+  };
+  // (one branch outside, so that the loads are on their way together)
+  if (type == NVFP4_FP32) load(NVFP4_FP32);
+  else if (type == NVFP4_BF16) load(NVFP4_BF16);
+  else load(NVFP4_FP16);
   int id;
   float w;
   gate_choose<L>(a.rule, l, &id, &w);
@@ -121,6 +128,7 @@ cudaError_t grad(const GateArgs& a, unsigned g, cudaStream_t s) {
   if (E <= 64) topk_gate_grad_kernel<DT, 2><<<g, kThreads, 0, s>>>(a);
   else if (E <= 128) topk_gate_grad_kernel<DT, 4><<<g, kThreads, 0, s>>>(a);
   else if (E <= 256) topk_gate_grad_kernel<DT, 8><<<g, kThreads, 0, s>>>(a);
+  else if (E <= 512) topk_gate_grad_kernel<DT, 16><<<g, kThreads, 0, s>>>(a);
   else topk_gate_grad_kernel<DT, 32><<<g, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -135,6 +143,7 @@ cudaError_t launch_topk_gate(const GateArgs& a, int dtype, cudaStream_t s) {
   if (E <= 64) topk_gate_kernel<2><<<g, kThreads, 0, s>>>(a, dtype);
   else if (E <= 128) topk_gate_kernel<4><<<g, kThreads, 0, s>>>(a, dtype);
   else if (E <= 256) topk_gate_kernel<8><<<g, kThreads, 0, s>>>(a, dtype);
+  else if (E <= 512) topk_gate_kernel<16><<<g, kThreads, 0, s>>>(a, dtype);
   else topk_gate_kernel<32><<<g, kThreads, 0, s>>>(a, dtype);
   return cudaGetLastError();
 }

@@ -229,3 +229,12 @@ def test_gate_streams_and_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(ids, ref[0]) and torch.equal(w, ref[1]) and torch.equal(dl, eager)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("sigmoid", False)])
+@pytest.mark.parametrize("T,E,topk,kind", [(40, 512, 8, "fp32"), (9, 511, 32, "bf16"),
+                                           (40, 513, 8, "fp16"), (3, 384, 6, "fp32")])
+def test_gate_of_many_experts(T, E, topk, kind, score, renormalize, biased):
+    test_gate(T, E, topk, kind, score, renormalize, 1.0, biased)
+    test_gate_grad(T, E, topk, kind, score, renormalize, 1.0)
