@@ -61,7 +61,7 @@ constexpr int kStageBytes = kTokOffset + kCols * 128;
 constexpr int kFacOffset = kStages * kStageBytes;           // [bufs][3][TB] floats
 constexpr int kRedOffset = kFacOffset + kAccBufs * 3 * TB * 4;   // [4][TB] maxima
 constexpr int kBarOffset = kRedOffset + 4 * TB * 4;
-constexpr int kCtlOffset = kBarOffset + 8 * (2 * kStages + 2 * kAccBufs + 6);
+constexpr int kCtlOffset = kBarOffset + 8 * (2 * kStages + 2 * kAccBufs + 7);
 constexpr int kSmemBytes = kCtlOffset + 32 + 1024;
 constexpr uint32_t kTmemCols = kAccBufs * 2 * kCols;
 
@@ -201,6 +201,9 @@ struct Block {
   }
   __device__ __forceinline__ uint32_t run_taken(int i) const {
     return bar(2 * kStages + 2 * kAccBufs + 4 + i);
+  }
+  __device__ __forceinline__ uint32_t chosen() const {
+    return bar(2 * kStages + 2 * kAccBufs + 6);
   }
   __device__ __forceinline__ float* fac(int b) const {
     return reinterpret_cast<float*>(smem + kFacOffset) + b * 3 * TB;
@@ -646,12 +649,7 @@ __device__ __forceinline__ void gate_token(const Fp8MoeArgs& a, Routes& rt, int 
       a.ids[r] = id;
       a.weights[r] = w;
     }
-    if (a.T == 1) {                         // its experts are distinct: no list to make
-      rt.live[r] = static_cast<int16_t>(id);
-      rt.start[r] = rt.route[r] = static_cast<int16_t>(r);
-      rt.tokens[r] = 1u;
-      if (r == 0) rt.n_live = a.rule.topk;
-    }
+    if (a.T == 1) rt.live[r] = static_cast<int16_t>(id);       // distinct ones
   }
 }
 
@@ -790,6 +788,7 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
       mbar_init(b.run_given(i), 1);
       mbar_init(b.run_taken(i), kRunReaders);
     }
+    mbar_init(b.chosen(), 1);
     b.ctl->abort = 0;
     b.ctl->timeout_ns = a.timeout_ns;
     fence_mbar_init();
@@ -803,19 +802,32 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     if (warp == 0 && lane < 2)
       phase[lane].set(lane, ((lane ? a.I : a.K) + 127) / 128, lane ? units2 : units1, live);
   };
-  // One token of the gate has topk experts: its phases are known now, and it needs no list
-  // (both between the choice and the first weights otherwise: 64.5 -> 63.6 us).
+  // One token of the gate has topk distinct experts: all but their numbers and weights is known
+  // now.  A warp without a role makes the choice while the others take up theirs, up to where
+  // those are needed (phases, list and first steps between the choice and the first weights
+  // otherwise: 64.5 -> ONE us).
   const bool one = a.T == 1 && a.router;
-  if (one) set_phase(a.rule.topk);
+  if (one) {
+    set_phase(a.rule.topk);
+    if (warp == 3 && lane < a.rule.topk) {
+      rt.start[lane] = rt.route[lane] = static_cast<int16_t>(lane);
+      rt.tokens[lane] = 1u;
+      if (lane == 0) rt.n_live = a.rule.topk;
+    }
+    __syncthreads();
+  }
   grid_dependency_wait();
   uint32_t ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(a.counters, 1u);     // on its way meanwhile
   if (a.router) {
-    if (warp < a.T) {
-      if (a.rule.E <= 128) gate_token<4>(a, rt, warp);
-      else if (a.rule.E <= 256) gate_token<8>(a, rt, warp);
-      else if (a.rule.E <= 512) gate_token<16>(a, rt, warp);
-      else gate_token<32>(a, rt, warp);
+    const int t = one ? warp - 3 : warp;
+    if (t >= 0 && t < a.T) {
+      if (a.rule.E <= 128) gate_token<4>(a, rt, t);
+      else if (a.rule.E <= 256) gate_token<8>(a, rt, t);
+      else if (a.rule.E <= 512) gate_token<16>(a, rt, t);
+      else gate_token<32>(a, rt, t);
+      __syncwarp();
+      if (one && lane == 0) mbar_arrive(b.chosen());
     }
   } else {
     const int r = threadIdx.x;
@@ -827,8 +839,8 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
       rt.weight[r] = __ldg(a.weights + r);
     }
   }
-  __syncthreads();
   if (!one) {
+    __syncthreads();
     list_experts(a, rt, bits, scan);
     set_phase(rt.n_live);
     __syncthreads();
@@ -843,7 +855,7 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     const uint64_t wpol = l2_policy_evict_first(), tpol = l2_policy_evict_last();
     fence_proxy_async_global();                 // the codes of x were written before
     uint32_t issued = 0;
-    bool alive = true;
+    bool alive = true, chosen = !one;
     int ph = 0;
 #pragma unroll 1
     while (alive) {
@@ -878,6 +890,10 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
           if (!wait_soon(b.empty(at.slot), at.phase ^ 1u, b.ctl, b.status)) {
             alive = false;
             break;
+          }
+          if (!chosen) {
+            alive = chosen = wait_soon(b.chosen(), 0, b.ctl, b.status);
+            if (!alive) break;
           }
           copy.weights(p, c, at.slot);
           ++issued;
@@ -922,7 +938,9 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
     wait_drain(b.drain(), 0, b.ctl->timeout_ns);
   } else if (warp == 2) {
     Run run;
-    while (runs.take(&run, true) && run.phase < 2) {
+    const bool ready =
+        !one || __all_sync(kFullWarp, wait_soon(b.chosen(), 0, b.ctl, b.status));
+    while (ready && runs.take(&run, true) && run.phase < 2) {
       if (run.phase == 1) {                     // the scales of h
         bool ok = true;
         if (lane == 0)
