@@ -34,8 +34,8 @@
 //   memory, which four warps read and add as FP32 times the factor (weight scale * token
 //   scale, for down also * routing weight) that a warp of its own lays out.
 //
-// Measured in a graph, 128 experts, 8 chosen: 6144 x 2048 one token 64 us (302 MB of weights,
-// 0.70 of the copy rate; about 8 us pass before the first weights are asked for, and 6 behind
+// Measured in a graph, 128 experts, 8 chosen: 6144 x 2048 one token 63 us (302 MB of weights,
+// 0.71 of the copy rate; about 7 us pass before the first weights are asked for, and 6 behind
 // the last ones), 2 tokens 106, 4 tokens 179, 8 tokens 303 us (1.9 GB, 0.93); 2048 x 768 27, 34,
 // 49 and 66 us.  A first form with mma.sync, eight warps with rings of their own, spent 280
 // instructions on 2 KB of weights, converting codes: one token 96 us.  One cooperative launch
@@ -805,7 +805,7 @@ fp8_moe_kernel(const __grid_constant__ CUtensorMap t1, const __grid_constant__ C
   // One token of the gate has topk distinct experts: all but their numbers and weights is known
   // now.  A warp without a role makes the choice while the others take up theirs, up to where
   // those are needed (phases, list and first steps between the choice and the first weights
-  // otherwise: 64.5 -> ONE us).
+  // otherwise: 64.5 -> 62.5 us).
   const bool one = a.T == 1 && a.router;
   if (one) {
     set_phase(a.rule.topk);
