@@ -29,9 +29,9 @@
 // Bound: HBM.  8192 x 6144 BF16, and its part of the measured copy rate: norm 41 us (0.73: a
 // row's latency, of copies, sums and stores, on the 24 warps that the registers leave room
 // for; FP32 rows, twice the bytes, 65 us, 0.91), with residual 65 us (0.91), codes with
-// residual 61 us (0.85), gradient 69 us (0.64), with dh 74 us (0.80).  8192 x 6143: 59, 80, -,
-// 82 and 91 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 7.0:
-// latency.  In a graph, one call after the other.
+// residual 61 us (0.85), gradient 68 us (0.66), with dh 73 us (0.81).  8192 x 6143: 59, 80, -,
+// 82 and 91 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 3.6,
+// of two rows and more 5.3 (its second launch): latency.  In a graph, one call after the other.
 #include "fp8_quant.cuh"
 #include "norm.h"
 
@@ -50,6 +50,8 @@ struct NormShape {
   size_t smem;
 };
 constexpr int kMostDepth = 2;
+// (with or without dh the same shape: the workspace's size hangs on it)
+constexpr int kGradArrays = 3;
 constexpr int kForwardRegs = 80, kFp8Regs = 80, kGradRegs = 128;       // of 16 elements
 constexpr int kWideRegs = 96, kWideFp8Regs = 128;                      // of 32
 
@@ -349,6 +351,12 @@ __global__ void __maxnreg__(REGS) rms_norm_kernel(const NormArgs a, int threads,
   cp_wait(0);
 }
 
+__device__ __forceinline__ void put_dw(void* dw, int type, int col, float v) {
+  if (type == NVFP4_FP32) static_cast<float*>(dw)[col] = v;
+  else static_cast<uint16_t*>(dw)[col] = static_cast<uint16_t>(
+      type == NVFP4_BF16 ? f32_to_elem<NVFP4_BF16>(v) : f32_to_elem<NVFP4_FP16>(v));
+}
+
 template <int DT, int EPT, bool ALIGNED, int REGS>
 __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int threads, int rows,
                                                        int depth) {
@@ -439,24 +447,64 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
     if constexpr (!kEarly) next();
   }
   cp_wait(0);
-  // the block's sums: of its rows side by side, where those are several, in their order
+  // the block's sums: of its rows side by side, where those are several, in their order; a
+  // block alone needs no second launch (one row of 6144 7.0 -> 3.6 us)
+  const bool alone = gridDim.x == 1;
+  if (alone && rows == 1) {
+    const bool vectors = ALIGNED && (reinterpret_cast<uintptr_t>(a.dw) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!c.any(i)) continue;
+      float f[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = dw[i * N + j];
+      if (vectors && a.w_type == NVFP4_FP32) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + c.column(i) + j) =
+              make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+      } else if (vectors) {                         // the rows' type
+        Pack<DT, N> p;
+        pack<DT, N>(p, f);
+        c.put(a.dw, 0, i, p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (c.in(i, j)) put_dw(a.dw, a.w_type, c.column(i) + j, f[j]);
+      }
+    }
+    return;
+  }
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.D;
   float* all_rows = reinterpret_cast<float*>(staged);            // [rows][D]
-  if (rows > 1) {
+  if (rows > 1 || alone) {
     __syncthreads();
     out = all_rows + sub * a.D;
   }
+  // (by sixteen bytes: few rows of 6144 7.3 -> 5.3 us, 1000 of them 17 -> 15 us)
+  const bool vectors = ALIGNED && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
+    if (vectors) {
+      if (c.any(i)) {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (c.any(i) && c.in(i, j)) out[c.column(i) + j] = dw[i * N + j];
-  if (rows > 1) {
+        for (int j = 0; j < N; j += 4)
+          *reinterpret_cast<float4*>(out + c.column(i) + j) =
+              make_float4(dw[i * N + j], dw[i * N + j + 1], dw[i * N + j + 2], dw[i * N + j + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c.any(i) && c.in(i, j)) out[c.column(i) + j] = dw[i * N + j];
+    }
+  }
+  if (rows > 1 || alone) {
     __syncthreads();
     for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
       float v = 0.f;
       for (int r = 0; r < rows; ++r) v += all_rows[r * a.D + col];
-      a.part[static_cast<int64_t>(blockIdx.x) * a.D + col] = v;
+      if (alone) put_dw(a.dw, a.w_type, col, v);
+      else a.part[static_cast<int64_t>(blockIdx.x) * a.D + col] = v;
     }
   }
 }
@@ -479,9 +527,7 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, in
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v += sums[i][lane];
-    if (type == NVFP4_FP32) static_cast<float*>(dw)[c] = v;
-    else static_cast<uint16_t*>(dw)[c] = static_cast<uint16_t>(
-        type == NVFP4_BF16 ? f32_to_elem<NVFP4_BF16>(v) : f32_to_elem<NVFP4_FP16>(v));
+    put_dw(dw, type, c, v);
   }
 }
 
@@ -527,8 +573,6 @@ NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int ro
   return s;
 }
 int forward_arrays(const NormArgs& a) { return a.r ? 2 : 1; }
-// (with or without dh the same shape: the workspace's size hangs on it)
-constexpr int kGradArrays = 3;
 
 template <int DT, int EPT, bool FP8, bool ALIGNED, int REGS>
 cudaError_t go(const NormArgs& a, const NormShape& s, cudaStream_t st) {
@@ -558,7 +602,7 @@ cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
     else if (s.ept == 16) go_grad<DT, 16, ALIGNED, kGradRegs>(a, s, st);
     else go_grad<DT, 32, ALIGNED, kWideRegs>(a, s, st);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || s.grid == 1) return e;
   }
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};

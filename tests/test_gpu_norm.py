@@ -342,3 +342,45 @@ def test_rows_at_the_limits_of_a_block(T, D, kind):
         # half a step of E4M3: 2^-4 of the value, at least half the smallest step, 2^-10
         assert bool(((codes.float().double() * wide - ref).abs()
                      <= ref.abs() * 2.0 ** -4 * (1 + U) + 2.0 ** -10 * wide + U * ref.abs()).all())
+
+
+@pytest.mark.parametrize("wtype", ["same", "fp32", "offset"])
+@pytest.mark.parametrize("T,D,kind", [(1, 1, "bf16"), (1, 7, "fp16"), (1, 64, "bf16"),
+                                      (4, 64, "fp16"), (1, 6144, "bf16"), (1, 6143, "fp16"),
+                                      (2, 6144, "bf16"), (1, 2048, "fp32"), (1, 12288, "bf16"),
+                                      (1, 12287, "fp32"), (3, 512, "bf16"), (9, 512, "fp32")])
+def test_gradient_of_one_block(T, D, kind, wtype):
+    """Rows of one block, whose weight sums are the result, and a few more; the weight (and so its
+    gradient) of either type, or beginning inside 16 bytes."""
+    g = torch.Generator().manual_seed(11 * T + D)
+    x, dy, dh = (rows(g, T, D, kind) for _ in range(3))
+    w = (1 + 0.3 * torch.randn(D, generator=g)).cuda()
+    if wtype != "fp32":
+        w = w.to(TYPES[kind])
+    if wtype == "offset":
+        w = inside(w, 1)
+    dx, dw = norm.rms_norm_grad(dy, x, w, dh, eps=1e-5)
+    assert dw.dtype == w.dtype and dw.shape == (D,)
+    x6, w6 = x.double(), w.double()
+    rstd = 1 / torch.sqrt(x6.square().mean(-1, keepdim=True) + 1e-5)
+    g6 = dy.double() * w6
+    back = x6 * rstd.square() * (g6 * x6).mean(-1, keepdim=True)
+    want = rstd * (g6 - back) + dh.double()
+    size = rstd * (g6.abs() + x6.abs() * rstd.square() * (g6 * x6).abs().mean(-1, keepdim=True)) \
+        + dh.double().abs()
+    assert bool(((dx.double() - want).abs()
+                 <= half_step(x.dtype) * want.abs() + 2 * U * size + TINY[x.dtype]).all())
+    terms = dy.double() * x6 * rstd
+    want = terms.sum(0)
+    assert bool(((dw.double() - want).abs() <= half_step(w.dtype) * want.abs()
+                 + 2 * U * terms.abs().sum(0) + TINY[w.dtype]).all())
+    again = norm.rms_norm_grad(dy, x, w, dh, eps=1e-5)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    # into the middle of a larger matrix: what lies beside the weight's gradient stays
+    around = torch.full((D + 32,), 7.0, dtype=w.dtype, device="cuda")
+    off = 1 if wtype == "offset" else 16
+    ws = torch.empty(F.nvfp4_rms_norm_grad_workspace_bytes(T, D) + 4, dtype=torch.uint8,
+                     device="cuda")[4:]
+    F.nvfp4_rms_norm_grad(dy, x, dh, w, 1e-5, torch.empty_like(x), around[off:off + D], ws)
+    assert torch.equal(around[off:off + D], dw)
+    assert bool((around[:off] == 7).all()) and bool((around[off + D:] == 7).all())
