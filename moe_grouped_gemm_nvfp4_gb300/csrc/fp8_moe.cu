@@ -125,8 +125,12 @@ struct Phase {
   }
   // Runs of whole items need no join, which takes about 4 us behind the last tile; runs of
   // single tiles are all equally long.  A tile takes 0.76 us while all SMs draw on HBM and
-  // at least 0.53 us (62 GB/s is all that one SM draws); a join 5 tiles' time.  At most about
-  // eight runs share an item: the last one reads all parts.
+  // at least 0.53 us (62 GB/s is all that one SM draws); a join 5 tiles' time and
+  // a third of one for each part, since the last run reads them all: an item of n tiles is cut
+  // into about sqrt(1.5 n) runs, eight at least (8 tokens, 39 experts of 512 x 2048, whose down
+  // items have 624 tiles: 75 -> 48 us; eight are best for small items).  As many runs of each
+  // item where that leaves no more than a fifth of the blocks idle: none then has parts of
+  // two items (one token, 4 experts of 4096 x 1024: 29 -> 26 us).
   __device__ __forceinline__ void set(int is_down, int k_blocks, int n_units, int n_experts) {
     const int blocks = static_cast<int>(gridDim.x);
     down = is_down;
@@ -142,7 +146,12 @@ struct Phase {
     const bool whole = rounds * per_item <= static_cast<float>(items) * per_item / blocks + 5.f;
     grain = whole ? per_item : 1;
     grains = whole ? items : items * per_item;
-    parts = min(blocks, min(grains, 8 * items));
+    const int share = max(8, static_cast<int>(sqrtf(1.5f * static_cast<float>(per_item))));
+    parts = min(blocks, min(grains, share * items));
+    if (!whole && parts == blocks) {
+      const int even = blocks / items * items;
+      if (5 * even >= 4 * blocks) parts = even;
+    }
   }
 };
 

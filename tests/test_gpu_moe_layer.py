@@ -274,3 +274,10 @@ def test_block_of_a_decoder():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(captured[0], out) and torch.equal(captured[1], h)
+
+
+@pytest.mark.parametrize("T,topk,E,K,inner,N", [(8, 6, 96, 512, 2048, 512), (8, 8, 64, 256, 1024, 200),
+                                                (1, 4, 16, 1024, 256, 4096), (3, 4, 32, 384, 512, 4864)])
+def test_cuts_of_the_products(T, topk, E, K, inner, N):
+    """Long items of few output columns, cut into many runs, and as many runs for each item."""
+    test_layer(T, topk, E, K, inner, N, torch.bfloat16)
