@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kThreads) topk_gate_grad_kernel(const GateArgs
   if (r.renormalize) {
     const float sum = warp_sum(p);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float mean = warp_sum(g * (p * inv));
+    // (the quotient itself: a weight that is alone is 1, and its gradient 0, not p / p's rounding)
+    const float mean = warp_sum(g * (sum == 0.f ? 0.f : p / sum));
     dp = ok ? (g - mean) * inv : 0.f;
   }
   if (whole) back = warp_sum(dp * p);

@@ -238,3 +238,15 @@ def test_gate_streams_and_capture():
 def test_gate_of_many_experts(T, E, topk, kind, score, renormalize, biased):
     test_gate(T, E, topk, kind, score, renormalize, 1.0, biased)
     test_gate_grad(T, E, topk, kind, score, renormalize, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_gradient_of_one_renormalised_weight_is_zero(kind, score):
+    """The weight is 1 whatever the logits: its gradient is 0, without any rounding's residue."""
+    g = torch.Generator().manual_seed(21)
+    l = torch.randn((300, 40), generator=g).mul_(3).to(TYPES[kind]).cuda()
+    dw = torch.randn((300, 1), generator=g).cuda()
+    ids, w = gating.topk_gate(l, 1, score=score, renormalize=True)
+    assert bool((w == 1).all())
+    assert bool((gating.topk_gate_grad(dw, l, ids, score, True) == 0).all())
