@@ -11,11 +11,11 @@
 namespace nvfp4 {
 
 // More tokens go through launches for any number (router product, gate, layout, two products,
-// sum).  In graphs, 128 experts, this call and those: 8 of 128 of 6144 x 2048, one token 63
-// and 73 us, 2 tokens 106 and 112, 4 tokens 179 and 180, 8 tokens 303 and 298; of 2048 x 768 27
-// and 38, 34 and 42, 49 and 51, 66 and 64 us; 2 of 128 of 1040 x 528 21 and 19 us, 4 tokens 25
-// and 28, 8 tokens 28 and 40.  Without a graph the host's time comes to those, several
-// calls; this is one of 9 us.  And those round gate_up's product and the experts' rows to 16 bits.
+// sum).  In graphs, 128 experts, this call and those: 8 of 128 of 6144 x 2048, one token 61
+// and 73 us, 2 tokens 108 and 114, 4 tokens 178 and 179, 8 tokens 305 and 300; of 2048 x 768 26
+// and 39, 33 and 41, 47 and 51, 61 and 65 us; 2 of 128 of 1040 x 528 21 and 19 us, 25 and 20, 26
+// and 27, 28 and 40.  Without a graph the host's time comes to those, several calls; this is one
+// of 9 us.  And those round gate_up's product and the experts' rows to 16 bits.
 constexpr int kMoeMaxTokens = 8;
 constexpr int kMoeMaxRoutes = 256;           // one thread each
 constexpr int kMoeMaxGrid = 160;
