@@ -53,7 +53,7 @@ constexpr int kMostDepth = 2;
 // (with or without dh the same shape: the workspace's size hangs on it)
 constexpr int kGradArrays = 3;
 constexpr int kForwardRegs = 80, kFp8Regs = 80, kGradRegs = 128;       // of 16 elements
-constexpr int kWideRegs = 96, kWideFp8Regs = 128;                      // of 32
+constexpr int kWideRegs = 96, kWideFp8Regs = 128, kWideGradRegs = 128; // of 32
 
 // The sum over a row's threads of N values, the same in each of them: lanes, then warps
 // in shared memory.  `part` alternates between two places from row to row: who writes one
@@ -366,7 +366,7 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
   // dh is taken with the others, so that the slot's next copies start at once (8192 x 6144
   // 78 -> 74 us); masked chunks take it behind the sums, when fewer registers are in use (8192
   // x 6143 97 -> 91 us).  32 elements a thread and their weights and sums leave no registers
-  // for a row: it is read from shared memory again behind the sums (4096 x 12288 216 -> 84 us).
+  // for a row: it is read from shared memory again behind the sums (4096 x 12288 216 -> 78 us).
   constexpr bool kKept = EPT < 32, kEarly = ALIGNED && kKept;
   extern __shared__ uint4 staged[];
   __shared__ float part[2][32][2];
@@ -536,7 +536,8 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, in
 // of 8 are too narrow, 32 for rows that are wider than the threads of 16 that an SM has
 // registers for: 768 of 80 (codes with residual of 4096 x 12288 64 us, by 32 elements 96), 512
 // of 128.  Registers a thread: 64, `most`, kWideRegs for the grid (up to five warps share the
-// 16384 of a quarter of the SM; codes have up to four, and 128 registers).
+// 16384 of a quarter of the SM; codes and gradients have up to four, and 128 registers, but for
+// the widest gradients begun inside a chunk).
 NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int rounds,
                    bool aligned) {
   const int es = dtype == NVFP4_FP32 ? 4 : 2;
@@ -600,7 +601,8 @@ cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
   if (s.grid > 0) {
     if (s.ept == 8) go_grad<DT, 8, ALIGNED, 64>(a, s, st);
     else if (s.ept == 16) go_grad<DT, 16, ALIGNED, kGradRegs>(a, s, st);
-    else go_grad<DT, 32, ALIGNED, kWideRegs>(a, s, st);
+    else if (ALIGNED || s.threads <= 512) go_grad<DT, 32, ALIGNED, kWideGradRegs>(a, s, st);
+    else go_grad<DT, 32, false, kWideRegs>(a, s, st);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || s.grid == 1) return e;
   }
@@ -634,7 +636,10 @@ cudaError_t set_smem() {
 template <int DT>
 cudaError_t set_all() {
   cudaError_t e = set_smem<DT, 8, 64, 64, 64>();
-  if (e == cudaSuccess) e = set_smem<DT, 32, kWideRegs, kWideFp8Regs, kWideRegs>();
+  if (e == cudaSuccess) e = set_smem<DT, 32, kWideRegs, kWideFp8Regs, kWideGradRegs>();
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, 32, false, kWideRegs>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmemMost);
   if (e == cudaSuccess) e = set_smem<DT, 16, kForwardRegs, kFp8Regs, kGradRegs>();
   return e;
 }
