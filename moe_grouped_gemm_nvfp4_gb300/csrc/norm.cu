@@ -29,8 +29,8 @@
 // Bound: HBM.  8192 x 6144 BF16, and its part of the measured copy rate: norm 41 us (0.73: a
 // row's latency, of copies, sums and stores, on the 24 warps that the registers leave room
 // for; FP32 rows, twice the bytes, 65 us, 0.91), with residual 65 us (0.91), codes with
-// residual 61 us (0.85), gradient 68 us (0.66), with dh 73 us (0.81).  8192 x 6143: 59, 80, -,
-// 82 and 91 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 3.6,
+// residual 61 us (0.85), gradient 68 us (0.66), with dh 73 us (0.81).  8192 x 6143: 57, 79, -,
+// 81 and 91 us (masks, and weights by the element).  One row: 2.8 to 3.3 us, the gradient 3.6,
 // of two rows and more 5.3 (its second launch): latency.  In a graph, one call after the other.
 #include "fp8_quant.cuh"
 #include "norm.h"
@@ -52,8 +52,9 @@ struct NormShape {
 constexpr int kMostDepth = 2;
 // (with or without dh the same shape: the workspace's size hangs on it)
 constexpr int kGradArrays = 3;
-constexpr int kForwardRegs = 80, kFp8Regs = 80, kGradRegs = 128;       // of 16 elements
-constexpr int kWideRegs = 96, kWideFp8Regs = 128, kWideGradRegs = 128; // of 32
+// Registers a thread of 16 elements, and of 32.
+constexpr int kForwardRegs = 80, kOddRegs = 72, kFp8Regs = 80, kGradRegs = 128;
+constexpr int kWideRegs = 96, kWideFp8Regs = 128, kWideGradRegs = 128;
 
 // The sum over a row's threads of N values, the same in each of them: lanes, then warps
 // in shared memory.  `part` alternates between two places from row to row: who writes one
@@ -550,7 +551,11 @@ NormShape shape_of(int64_t T, int64_t D, int dtype, int arrays, int most, int ro
   s.rows = s.threads >= 256 ? 1 : 256 / s.threads;
   const int block = s.threads * s.rows;
   const int regs = s.ept == 8 ? 64 : s.ept == 16 ? most : kWideRegs;
-  int per_sm = 16384 / (regs * 32 * ((block + 127) / 128));
+  const int quarter = 16384 / (regs * 32), warps = block / 32;
+  int per_sm = quarter / ((warps + 3) / 4);
+  // (rows begun anywhere have a warp more: blocks share the quarters unevenly, and two of 13
+  // warps with 72 registers fit, 8192 x 6143 59 -> 57 us, 1000 x 6143 10.4 -> 9.3)
+  if (!aligned && arrays < kGradArrays) per_sm = quarter * 4 / warps;
   if (per_sm > 2048 / block) per_sm = 2048 / block;
   if (per_sm > 8) per_sm = 8;
   if (per_sm < 1) per_sm = 1;
@@ -583,7 +588,7 @@ cudaError_t go(const NormArgs& a, const NormShape& s, cudaStream_t st) {
 }
 template <int DT, bool FP8, bool ALIGNED>
 cudaError_t forward(const NormArgs& a, int dtype, cudaStream_t st) {
-  constexpr int kRegs = FP8 ? kFp8Regs : kForwardRegs;
+  constexpr int kRegs = FP8 ? kFp8Regs : ALIGNED ? kForwardRegs : kOddRegs;
   const NormShape s = shape_of(a.T, a.D, dtype, forward_arrays(a), kRegs, FP8 ? 1 : 4, ALIGNED);
   if (s.ept == 8) return go<DT, 8, FP8, ALIGNED, 64>(a, s, st);
   if (s.ept == 16) return go<DT, 16, FP8, ALIGNED, kRegs>(a, s, st);
@@ -618,12 +623,12 @@ cudaError_t backward(const NormArgs& a, int dtype, cudaStream_t st) {
                             a.w_type, a.dw);
 }
 
-template <int DT, int EPT, int REGS, int FP8_REGS, int GRAD_REGS>
+template <int DT, int EPT, int REGS, int ODD_REGS, int FP8_REGS, int GRAD_REGS>
 cudaError_t set_smem() {
   constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, true, REGS>, kAttr, kNormSmemMost);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, false, REGS>, kAttr, kNormSmemMost);
+    e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, false, false, ODD_REGS>, kAttr, kNormSmemMost);
   if constexpr (DT != NVFP4_FP32)
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(rms_norm_kernel<DT, EPT, true, true, FP8_REGS>, kAttr, kNormSmemMost);
@@ -635,12 +640,12 @@ cudaError_t set_smem() {
 }
 template <int DT>
 cudaError_t set_all() {
-  cudaError_t e = set_smem<DT, 8, 64, 64, 64>();
-  if (e == cudaSuccess) e = set_smem<DT, 32, kWideRegs, kWideFp8Regs, kWideGradRegs>();
+  cudaError_t e = set_smem<DT, 8, 64, 64, 64, 64>();
+  if (e == cudaSuccess) e = set_smem<DT, 32, kWideRegs, kWideRegs, kWideFp8Regs, kWideGradRegs>();
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(rms_norm_grad_kernel<DT, 32, false, kWideRegs>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmemMost);
-  if (e == cudaSuccess) e = set_smem<DT, 16, kForwardRegs, kFp8Regs, kGradRegs>();
+  if (e == cudaSuccess) e = set_smem<DT, 16, kForwardRegs, kOddRegs, kFp8Regs, kGradRegs>();
   return e;
 }
 
