@@ -423,7 +423,8 @@ __global__ void __maxnreg__(REGS) rms_norm_grad_kernel(const NormArgs a, int thr
     row_sum<2>(sum, threads, part[odd]);
     odd ^= 1;
     if constexpr (kEarly) next();
-    const float rstd = 1.f / sqrtf(sum[0] * over + a.eps);
+    // (a row past T, of a block's last step, adds nothing to dw, also where eps is 0)
+    const float rstd = on ? 1.f / sqrtf(sum[0] * over + a.eps) : 0.f;
     const float back = rstd * rstd * (sum[1] * over);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
