@@ -723,8 +723,10 @@ nvfp4_status nvfp4_rms_norm_grad(const void* dy, int64_t ld_dy, const void* h, i
  * equals, a NaN as the largest value.  The order is that of the real sums
  * (neighbours nearer than FP32 rounding are compared in FP64).  The weight of a
  * chosen expert is s (without the bias), with NVFP4_GATE_RENORMALIZE over the sum
- * of the chosen scores, times `scale`.  A row of -infinities has softmax scores
- * 0, and a sum of 0 gives weights 0.  1 <= E <= 1024, topk <= min(E, 32).
+ * of the chosen scores (a ratio: it holds also where the scores themselves are
+ * below FP32's range), times `scale`.  A row of -infinities has softmax scores 0;
+ * renormalised weights are 0 where all chosen logits are -infinities.
+ * 1 <= E <= 1024, topk <= min(E, 32).
  * ------------------------------------------------------------------------ */
 #define NVFP4_GATE_SIGMOID 1u
 #define NVFP4_GATE_RENORMALIZE 2u

@@ -1,12 +1,12 @@
 // Top-k gate of an MoE layer and its gradient: a warp per token (gate.cuh).
 //
-// Gradient: with dp the gradient of the chosen scores (dw * scale, through the
-// division by their sum S where they are renormalised: (g - sum_j g_j w_j) / S),
+// Gradient: with g the gradient of the weights times scale, p and s the scores, w the weights
+// renormalised,
 //
-//   softmax  dl = p (dp - sum_j dp_j p_j),   sigmoid  dl = dp s (1 - s)
+//   softmax  dl = p (g - sum_j g_j p_j),      renormalised  dl = w (g - sum_j g_j w_j)
+//   sigmoid  dl = g s (1 - s),                renormalised  dl = w (1 - s) (g - sum_j g_j w_j)
 //
-// The sum vanishes for renormalised softmax weights: like the sigmoid's, that
-// gradient is zero outside the chosen experts and needs no other logits, so only the
+// All but the first are zero outside the chosen experts and need no other logits, so only the
 // chosen ones are read.
 //
 // Bound: the gate's latency up to some thousand tokens (a chain of topk reductions over the
@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kThreads) topk_gate_grad_kernel(const GateArgs
   if (!ok) g = 0.f;
   float l[L];
   GateScores sc{0.f, 1.f, r.sigmoid};
-  float p;                                         // the chosen expert's score
   const bool whole = !r.sigmoid && !r.renormalize;
   const float chosen = ok ? gate_logit(a.logits, t * a.ld + e, DT) : -INFINITY;
   if (whole) {
@@ -82,24 +81,23 @@ __global__ void __launch_bounds__(kThreads) topk_gate_grad_kernel(const GateArgs
       l[i] = c < r.E ? gate_logit(a.logits, t * a.ld + c, DT) : -INFINITY;
     }
     sc = gate_scores<L>(l, r.E, 0);
-  } else if (!r.sigmoid) {
-    sc.max = warp_max(chosen);
   }
-  p = ok ? sc.of(chosen) : 0.f;
-  float dp = g, back = 0.f;
-  if (r.renormalize) {
-    const float sum = warp_sum(p);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    // (the quotient itself: a weight that is alone is 1, and its gradient 0, not p / p's rounding)
-    const float mean = warp_sum(g * (sum == 0.f ? 0.f : p / sum));
-    dp = ok ? (g - mean) * inv : 0.f;
-  }
-  if (whole) back = warp_sum(dp * p);
   // what the chosen experts get, then the place of each in its lane's experts
-  float d = dp * p;
-  if (r.sigmoid && ok) {                           // s (1 - s) without the difference
-    const float q = expf(-fabsf(chosen));
-    d = dp * (q / ((1.f + q) * (1.f + q)));
+  float d = 0.f, back = 0.f;
+  const float q = expf(-fabsf(chosen));            // for sigmoids
+  if (whole) {
+    d = ok ? g * sc.of(chosen) : 0.f;
+    back = warp_sum(d);
+  } else if (r.renormalize) {
+    // (the quotient itself: a weight that is alone is 1, and its gradient 0, not p / p's rounding)
+    const float share = gate_share(chosen, warp_max(chosen), r.sigmoid);
+    const float sum = warp_sum(share);
+    const float w = sum == 0.f ? 0.f : share / sum;
+    d = w * (g - warp_sum(g * w));
+    if (r.sigmoid) d *= (chosen < 0.f ? 1.f : q) / (1.f + q);
+    if (!ok) d = 0.f;
+  } else if (ok) {                                 // s (1 - s) without the difference
+    d = g * (q / ((1.f + q) * (1.f + q)));
   }
   float add[L];
 #pragma unroll

@@ -56,7 +56,7 @@ __device__ __forceinline__ unsigned long long gate_key64(double f) {
   return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-// v: no NaN
+// (a NaN counts as the largest value)
 __device__ __forceinline__ float warp_max(float v) {
   return gate_value(__reduce_max_sync(kFullWarp, gate_key(v)));
 }
@@ -72,10 +72,25 @@ struct GateScores {
   float max, inv;
   int sigmoid;
   __device__ __forceinline__ float of(float l) const {
-    if (sigmoid) return 1.f / (1.f + expf(-l));
+    if (sigmoid) {                                  // (subnormal scores too)
+      const float q = expf(-fabsf(l));
+      return (l < 0.f ? q : 1.f) / (1.f + q);
+    }
     return max == -INFINITY && l == max ? 0.f : expf(l - max) * inv;
   }
 };
+// A chosen score times a factor that all chosen ones of the row share, by its logit and the
+// largest of theirs.  Renormalised weights are ratios of scores: they hold where those leave
+// FP32's range (sigmoids of logits below -87; softmax scores that a bias chose, far below the
+// row's largest), and only a row whose chosen logits are all -infinities has none.
+__device__ __forceinline__ float gate_share(float l, float top, int sigmoid) {
+  if (l == -INFINITY) return 0.f;
+  if (!sigmoid) return expf(l - top);
+  if (l > 0.f) return 1.f / (1.f + expf(-l));
+  return expf(l - fminf(top, 0.f)) / (1.f + expf(l));
+}
+// Scores below this are rounded to fewer bits, or to 0.
+constexpr float kGateLeastScore = 2.3509887e-38f;   // 2^-125
 template <int L>
 __device__ __forceinline__ GateScores gate_scores(const float (&l)[L], int E, int sigmoid) {
   GateScores g{-INFINITY, 1.f, sigmoid};
@@ -178,7 +193,8 @@ template <int L>
 __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[L], int* id,
                                             float* weight) {
   const int lane = threadIdx.x & 31;
-  // renormalised softmax weights need no total, nor does the choice without a bias
+  // renormalised softmax weights need no total, nor does the choice without a bias (the largest
+  // of the row is then the largest of the chosen)
   const bool total = r.sigmoid || r.bias || !r.renormalize;
   GateScores g{0.f, 1.f, r.sigmoid};
   if (total) {
@@ -302,7 +318,30 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
     }
   }
   const bool on = lane < r.topk;
-  float w = !on ? 0.f : r.bias ? chosen : g.of(chosen);
+  float w = 0.f;
+  // renormalised: by the logits, which are at hand without a bias; with one the scores are, and
+  // logits are looked up where a score is too small
+  bool shares = r.renormalize && !r.bias;
+  float logit = chosen;
+  if (r.renormalize && r.bias && __any_sync(kFullWarp, on && chosen < kGateLeastScore)) {
+    shares = true;
+#pragma unroll 1
+    for (int j = 0; j < r.topk; ++j) {              // of the expert's lane
+      const int e = __shfl_sync(kFullWarp, mine, j);
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (lane + 32 * i == e) x = l[i];
+      x = __shfl_sync(kFullWarp, x, e & 31);
+      if (j == lane) logit = x;
+    }
+  }
+  if (shares) {
+    const float top = total ? warp_max(on ? logit : -INFINITY) : g.max;
+    if (on) w = gate_share(logit, top, r.sigmoid);
+  } else if (on) {
+    w = r.bias ? chosen : g.of(chosen);
+  }
   if (r.renormalize) {
     const float sum = warp_sum(w);
     w = sum == 0.f ? 0.f : w / sum;

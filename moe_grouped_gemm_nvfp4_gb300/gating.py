@@ -4,9 +4,10 @@ their weights, and the gradient.
 Scores are softmax(logits) or sigmoid(logits).  Chosen are the topk largest logits or,
 with a bias, the topk largest score + bias: best first, the lower number first among
 equals, a NaN as the largest value.  The weights are the chosen scores (without the
-bias), divided by their sum with renormalize, times scale.  A row of -infinities has
-softmax scores 0; a sum of 0 gives weights 0.  Sums that FP32 rounding could swap are
-compared in FP64.
+bias), divided by their sum with renormalize, times scale.  Renormalised weights are ratios and
+hold also where the scores are below FP32's range.  A row of -infinities has softmax scores
+0, and renormalised weights 0 where all chosen logits are -infinities.  Sums that FP32
+rounding could swap are compared in FP64.
 
 `topk_gate` takes part in autograd (the gradient of the logits; the choice and the bias
 have none); `topk_gate_grad` is the gradient as a plain call, which enqueues kernels
