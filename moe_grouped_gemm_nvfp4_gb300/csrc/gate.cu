@@ -6,6 +6,10 @@
 //   softmax  dl = p (g - sum_j g_j p_j),      renormalised  dl = w (g - sum_j g_j w_j)
 //   sigmoid  dl = g s (1 - s),                renormalised  dl = w (1 - s) (g - sum_j g_j w_j)
 //
+// Where one score (weight) has more than half of the sum, its own gradient is a small difference
+// of large values: g is then taken relative to that expert's, which changes no result (the scores
+// add up to 1) and makes its term of the sum 0, so that the rest is left without a difference.
+//
 // All but the first are zero outside the chosen experts and need no other logits, so only the
 // chosen ones are read.
 //
@@ -70,30 +74,40 @@ __global__ void __launch_bounds__(kThreads) topk_gate_grad_kernel(const GateArgs
   }
   const bool ok = e >= 0;
   if (!ok) g = 0.f;
-  float l[L];
-  GateScores sc{0.f, 1.f, r.sigmoid};
+  float p[L], inv = 0.f;                           // scores times their total, of all experts
   const bool whole = !r.sigmoid && !r.renormalize;
   const float chosen = ok ? gate_logit(a.logits, t * a.ld + e, DT) : -INFINITY;
   if (whole) {
+    float max = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int c = lane + 32 * i;
-      l[i] = c < r.E ? gate_logit(a.logits, t * a.ld + c, DT) : -INFINITY;
+      p[i] = c < r.E ? gate_logit(a.logits, t * a.ld + c, DT) : -INFINITY;
+      max = fmaxf(max, p[i]);
     }
-    sc = gate_scores<L>(l, r.E, 0);
+    max = warp_max(max);
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      p[i] = lane + 32 * i < r.E && !(max == -INFINITY && p[i] == max) ? expf(p[i] - max) : 0.f;
+      sum += p[i];
+    }
+    sum = warp_sum(sum);
+    inv = sum == 0.f ? 0.f : 1.f / sum;
   }
-  // what the chosen experts get, then the place of each in its lane's experts
-  float d = 0.f, back = 0.f;
+  // what the chosen experts get (whole: the gradient of their scores), then the place of each
+  // in its lane's experts
+  float d = 0.f;
   const float q = expf(-fabsf(chosen));            // for sigmoids
   if (whole) {
-    d = ok ? g * sc.of(chosen) : 0.f;
-    back = warp_sum(d);
+    d = g;
   } else if (r.renormalize) {
     // (the quotient itself: a weight that is alone is 1, and its gradient 0, not p / p's rounding)
     const float share = gate_share(chosen, warp_max(chosen), r.sigmoid);
     const float sum = warp_sum(share);
     const float w = sum == 0.f ? 0.f : share / sum;
-    d = w * (g - warp_sum(g * w));
+    const uint32_t most = __ballot_sync(kFullWarp, w > 0.5f);
+    const float shift = most ? __shfl_sync(kFullWarp, g, __ffs(most) - 1) : 0.f;
+    d = w * ((g - shift) - warp_sum(w * (g - shift)));
     if (r.sigmoid) d *= (chosen < 0.f ? 1.f : q) / (1.f + q);
     if (!ok) d = 0.f;
   } else if (ok) {                                 // s (1 - s) without the difference
@@ -109,15 +123,32 @@ __global__ void __launch_bounds__(kThreads) topk_gate_grad_kernel(const GateArgs
     for (int i = 0; i < L; ++i)
       if (lane + 32 * i == ej) add[i] += dj;
   }
+  if (whole) {
+    float own = 0.f, shift = 0.f, back = 0.f;
+    bool top = false;
+    if (inv > 0.5f) {                              // the same in every lane
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (p[i] == 1.f) { top = true; own = add[i]; }
+      const uint32_t most = __ballot_sync(kFullWarp, top);
+      shift = most ? __shfl_sync(kFullWarp, own, __ffs(most) - 1) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      p[i] *= inv;
+      add[i] -= shift;
+      back = fmaf(p[i], add[i], back);
+    }
+    back = warp_sum(back);
+#pragma unroll
+    for (int i = 0; i < L; ++i) add[i] = p[i] * (add[i] - back);
+  }
   using Bits = typename Elem<DT>::Bits;
   Bits* out = static_cast<Bits*>(a.dlogits) + t * r.E;
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int c = lane + 32 * i;
-    if (c < r.E) {
-      const float v = whole ? add[i] - sc.of(l[i]) * back : add[i];
-      out[c] = static_cast<Bits>(f32_to_elem<DT>(v));
-    }
+    if (c < r.E) out[c] = static_cast<Bits>(f32_to_elem<DT>(add[i]));
   }
 }
 
