@@ -721,7 +721,7 @@ nvfp4_status nvfp4_rms_norm_grad(const void* dy, int64_t ld_dy, const void* h, i
  * exp(-logits)).  Chosen are the topk largest logits, or, with a bias (FP32
  * [E]), the topk largest s + bias; best first, the lower number first among
  * equals, a NaN as the largest value.  The order is that of the real sums
- * (neighbours nearer than FP32 rounding are compared in FP64).  The weight of a
+ * (sums that FP32 rounding could swap are compared in FP64).  The weight of a
  * chosen expert is s (without the bias), with NVFP4_GATE_RENORMALIZE over the sum
  * of the chosen scores (a ratio: it holds also where the scores themselves are
  * below FP32's range), times `scale`.  A row of -infinities has softmax scores 0;

@@ -8,9 +8,11 @@
 // order-preserving integers over the lane's own, then over the lanes (an integer
 // reduction, a vote for who has it, among equals another for the lowest number).  A NaN
 // counts as the largest value.  With a bias the chosen order hangs on sums whose 32-bit rounding
-// can swap neighbours; where two neighbours of the order (the first one left out
-// among them) are nearer than that rounding, the token is chosen again on 64-bit
-// keys.  64-bit exponentials for all would take longer than everything else here.
+// can swap experts.  Each sum has a bound of its error (gate_error), which grows with the score
+// and not with the sum.  Where the bounds of two picks that follow each other touch, or that of
+// any expert left out reaches the lowest of the picks', these experts (or, where they are too
+// many, all) are ordered again on 64-bit keys.  64-bit exponentials for all would take longer
+// than everything else here.
 #pragma once
 
 #include <cstdint>
@@ -119,13 +121,20 @@ __device__ __noinline__ int gate_choose64(GateRule r, LaneLogits<L> logits, floa
   const float (&l)[L] = logits.v;
   const int lane = threadIdx.x & 31;
   unsigned long long key[L];
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    double v = 0.0;                                 // sigmoid, or softmax before its total
+    if (lane + 32 * i < r.E) {
+      const double x = static_cast<double>(l[i]);
+      if (r.sigmoid) v = 1.0 / (1.0 + exp(-x));
+      else if (!(max == -INFINITY && l[i] == max)) v = exp(x - static_cast<double>(max));
+    }
+    sum += v;
+    key[i] = static_cast<unsigned long long>(__double_as_longlong(v));
+  }
   double inv = 1.0;
   if (!r.sigmoid) {
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-      if (lane + 32 * i < r.E && max != -INFINITY)
-        sum += exp(static_cast<double>(l[i]) - static_cast<double>(max));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     inv = sum == 0.0 ? 0.0 : 1.0 / sum;
@@ -133,14 +142,8 @@ __device__ __noinline__ int gate_choose64(GateRule r, LaneLogits<L> logits, floa
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int e = lane + 32 * i;
-    key[i] = 0;
-    if (e < r.E) {
-      const double x = static_cast<double>(l[i]);
-      double s;
-      if (r.sigmoid) s = 1.0 / (1.0 + exp(-x));
-      else s = max == -INFINITY && l[i] == max ? 0.0 : exp(x - static_cast<double>(max)) * inv;
-      key[i] = gate_key64(s + static_cast<double>(__ldg(r.bias + e)));
-    }
+    const double s = __longlong_as_double(static_cast<long long>(key[i])) * inv;
+    key[i] = e < r.E ? gate_key64(s + static_cast<double>(__ldg(r.bias + e))) : 0ull;
   }
   int mine = 0;
 #pragma unroll 1
@@ -162,6 +165,22 @@ __device__ __noinline__ int gate_choose64(GateRule r, LaneLogits<L> logits, floa
   }
   return mine;
 }
+
+// What the 32-bit sum k = s + bias can be off by, with room.  A sigmoid: its exponential (two
+// steps, of an exact argument), its sum and quotient, 6 * 2^-24 of it.  A softmax score, in units
+// of 2^-24 of it: |l - max| by its argument's rounding, which is -log(score) at most; 4 by the
+// exponential; its total's terms likewise (4 and less than 7, the mean of |l - max|), L + 4
+// additions, quotient and product.  The sum itself half a step (a whole one is taken: the
+// bounds' own sums round too).  Subnormal scores and sums: some of the smallest steps.
+// MOST: with the smallest score's logarithm, -105, for any.
+template <int L, bool MOST>
+__device__ __forceinline__ float gate_error(float s, float k, int sigmoid) {
+  float of_score = 4e-7f;
+  if (!sigmoid)
+    of_score = 6.2e-8f * (L + 28.f + (MOST ? 105.f : -__logf(fminf(fmaxf(s, 1.2e-38f), 1.f))));
+  return of_score * s + 1.2e-7f * fabsf(k) + 1e-44f;
+}
+__device__ __forceinline__ bool is_finite(float k) { return fabsf(k) < INFINITY; }
 
 // The order of n <= 32 experts by sigmoid + bias in 64 bits: lane j has expert e, its logit
 // and its score.  One 64-bit exponential a lane; gate_choose64 takes them for all experts.
@@ -241,13 +260,10 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
         at[i + 1] = swap ? a0 : at[i + 1];
       }
   }
-  // With a bias one more than wanted, and on until a pick is clear of the one before.
-  const int picks = r.bias && r.topk < r.E ? r.topk + 1 : r.topk;
-  int mine = 0, count = 0;
-  float chosen = 0.f, last_s = 0.f, last = 0.f;                   // last: the pick before
-  bool near = false, touching = false;
+  int mine = 0;
+  float chosen = 0.f;
 #pragma unroll 1
-  for (; count < picks || (touching && r.sigmoid && count < min(r.E, 32)); ++count) {
+  for (int count = 0; count < r.topk; ++count) {
     uint32_t best = key[0];
     int place = at[0];
     float v = val[0];
@@ -276,30 +292,62 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
         }
       }
     }
-    if (r.bias) {
-      const float k = top == 0xFFFFFFFFu ? NAN : gate_value(top);
-      // What 32 bits can be off by, with room: a sigmoid two steps of a value (its exponential,
-      // sum and quotient are rounded once each), a softmax score 2e-6 of it (its argument and
-      // total too), the sum with the bias half a step.
-      touching = count > 0 && !(last - k > (r.sigmoid ? 4e-7f : 2e-6f) * (fabsf(last_s) + fabsf(v)) +
-                                               1.2e-7f * (fabsf(last) + fabsf(k)));
-      near |= touching;
-      last_s = v;
-      last = k;
-    }
     if (count == lane) { mine = e; chosen = v; }
+    // (no instruction, but the compiler's order of the loop is 12% faster around it, with a bias
+    // or without: 65536 tokens of 128 experts 44.5 -> 39.6 us)
+    if (r.bias) asm volatile("" ::: "memory");
+  }
+  const bool on = lane < r.topk;
+  // Lanes: the picks.  An infinity or a NaN is certain, and so is its place.
+  bool near = false;
+  uint32_t may = 0;                                 // experts left that may belong before a pick
+  int more = 0;
+  if (r.bias) {
+    const float k = chosen + __ldg(r.bias + mine);
+    const float error = gate_error<L, false>(chosen, k, r.sigmoid);
+    const bool sure = !on || !is_finite(k);
+    const float least = sure ? INFINITY : k - error;
+    const float before = __shfl_up_sync(kFullWarp, least, 1);
+    const float low = gate_value(__reduce_min_sync(kFullWarp, gate_key(least)));
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const float x = gate_value(key[i]);
+      if (key[i] != 0 && is_finite(x) && !(x + gate_error<L, true>(val[i], x, r.sigmoid) < low))
+        may |= 1u << i;
+    }
+    if (!r.sigmoid && __any_sync(kFullWarp, may != 0)) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const float x = gate_value(key[i]);
+        if (x + gate_error<L, false>(val[i], x, 0) < low) may &= ~(1u << i);
+      }
+    }
+    more = __reduce_add_sync(kFullWarp, __popc(may));
+    near = more > 0 || __any_sync(kFullWarp, lane > 0 && !sure && !(k + error < before));
   }
   if (near) {                                       // the same in every lane
-    // (all picks are in lanes, and the last one is clear of what follows, or all are picked)
-    const bool few = r.sigmoid && count <= 32 && (!touching || count == r.E);
+    const bool few = r.sigmoid && r.topk + more <= 32;
     if (!few) {
       LaneLogits<L> row;
 #pragma unroll
       for (int i = 0; i < L; ++i) row.v[i] = l[i];
       mine = gate_choose64<L>(r, row, g.max);
+      more = 0;
+    }
+#pragma unroll 1
+    for (int j = r.topk; j < r.topk + more; ++j) {  // those behind the picks, one a lane
+      const int from = __ffs(__ballot_sync(kFullWarp, may != 0)) - 1;
+      const int i0 = __ffs(may) - 1;
+      int e = 0;
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (i == i0) e = lane + 32 * at[i];
+      e = __shfl_sync(kFullWarp, e, from);
+      if (lane == from) may &= may - 1;
+      if (j == lane) mine = e;
     }
     float logit = 0.f;
-    const int n = few ? count : r.topk;
+    const int n = r.topk + more;
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {                   // of the expert's lane
       const int e = __shfl_sync(kFullWarp, mine, j);
@@ -317,7 +365,6 @@ __device__ __forceinline__ void gate_choose(const GateRule& r, const float (&l)[
       chosen = __int_as_float(m.y);
     }
   }
-  const bool on = lane < r.topk;
   float w = 0.f;
   // renormalised: by the logits, which are at hand without a bias; with one the scores are, and
   // logits are looked up where a score is too small
