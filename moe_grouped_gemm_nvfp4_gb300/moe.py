@@ -357,8 +357,8 @@ class Fp8MLP:
         return tokens.combine(y, pos, topk_weights, offsets)
 
     def step_few(self, x, topk_ids, topk_weights, stream=None):
-        """step() of at most 8 tokens (ValueError for more) in one call of the library,
-        without a route-ordered copy of anything.  gate_up's product and the experts'
+        """step() of at most 8 tokens, 1024 experts and min(E, 32) choices a token (ValueError
+        for more) in one call of the library, without a route-ordered copy of anything.  gate_up's product and the experts'
         rows stay FP32 here, where step() rounds them to x's type.  An expert that a
         token names twice counts with both weights."""
         if forward_ad._current_level >= 0:
@@ -372,7 +372,10 @@ class Fp8MLP:
             return done[0]
         if x.shape[0] == 0:
             return x.new_empty((0, self.down[0].shape[1]))
-        raise ValueError("step_few takes at most 8 tokens: use step()")
+        if x.shape[0] > 8:
+            raise ValueError("step_few takes at most 8 tokens: use step()")
+        raise ValueError("step_few takes K and I that are multiples of 16, at most 1024 experts and "
+                         "at most min(E, 32) choices a token: use step() for more of the last two")
 
 
 class Fp8MoE:
