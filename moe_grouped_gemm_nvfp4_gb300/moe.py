@@ -357,10 +357,10 @@ class Fp8MLP:
         return tokens.combine(y, pos, topk_weights, offsets)
 
     def step_few(self, x, topk_ids, topk_weights, stream=None):
-        """step() of at most 8 tokens, 1024 experts and min(E, 32) choices a token (ValueError
-        for more) in one call of the library, without a route-ordered copy of anything.  gate_up's product and the experts'
-        rows stay FP32 here, where step() rounds them to x's type.  An expert that a
-        token names twice counts with both weights."""
+        """step() of at most 8 tokens with at most min(E, 32) choices each (ValueError for
+        more) in one call of the library, without a route-ordered copy of anything.
+        gate_up's product and the experts' rows stay FP32 here, where step() rounds them
+        to x's type.  An expert that a token names twice counts with both weights."""
         if forward_ad._current_level >= 0:
             tokens.refuse_tangents(x, topk_weights, *self.gate_up, *self.down)
         if stream is not None:
@@ -375,7 +375,7 @@ class Fp8MLP:
         if x.shape[0] > 8:
             raise ValueError("step_few takes at most 8 tokens: use step()")
         raise ValueError("step_few takes K and I that are multiples of 16, at most 1024 experts and "
-                         "at most min(E, 32) choices a token: use step() for more of the last two")
+                         "at most min(E, 32) choices a token: use step() for more choices")
 
 
 class Fp8MoE:
