@@ -378,6 +378,21 @@ class Fp8MLP:
                          "at most min(E, 32) choices a token: use step() for more choices")
 
 
+def _router_logits(x, router):
+    """x . router^T with FP32 sums, [T, E], also where the process lets torch multiply FP32
+    matrices in TF32 (11 bits): 16-bit x is exact in that, and the router is then taken in
+    three parts of 8 bits, which are."""
+    if router.dtype == x.dtype:
+        return torch.mm(x, router.t(), out_dtype=torch.float32)
+    if torch.backends.cuda.matmul.fp32_precision != "tf32":
+        return torch.mm(x.float(), router.t())
+    parts, rest = [], router
+    for _ in range(3):
+        parts.append(rest.bfloat16().float())
+        rest = rest - parts[-1]
+    return torch.mm(x.float(), torch.cat(parts).t()).view(x.shape[0], 3, router.shape[0]).sum(1)
+
+
 class Fp8MoE:
     """An MoE layer over FP8 experts: the router's product, the top-k gate and the
     experts (weights as in Fp8MLP).  router [E, K] has the tokens' type or is FP32;
@@ -414,11 +429,6 @@ class Fp8MoE:
                                     None)
         if done is not None:
             return done
-        router = self.router
-        if router.dtype == x.dtype:
-            logits = torch.mm(x, router.t(), out_dtype=torch.float32)
-        else:
-            logits = torch.mm(x.float(), router.t())
-        ids, weights = gating.topk_gate(logits, self.topk, self.bias, self.score,
-                                        self.renormalize, self.scale)
+        ids, weights = gating.topk_gate(_router_logits(x, self.router), self.topk, self.bias,
+                                        self.score, self.renormalize, self.scale)
         return self.mlp.step(x, ids, weights), ids, weights
