@@ -64,6 +64,15 @@ double real(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw BadArg("expected true or false");
+  }
+  return v != 0;
+}
+
 int dtype_of(const Tensor& t) {
   switch (t.scalar_type()) {
     case at::kBFloat16: return NVFP4_BF16;
@@ -166,7 +175,7 @@ PyObject* dispatch(PyObject* const* a) {
   x = rows_of(x);
   int64_t R = integer(a[3]);
   if (R < 0) R = pos.numel();
-  Tensor out = route_rows(on, {R, x.size(1)}, x.scalar_type(), off, PyObject_IsTrue(a[4]) == 1);
+  Tensor out = route_rows(on, {R, x.size(1)}, x.scalar_type(), off, truth(a[4]));
   check("nvfp4_tokens_dispatch",
         nvfp4_tokens_dispatch(x.data_ptr(), row_stride(x), p, off, E, pos.size(0),
                               static_cast<int32_t>(pos.size(1)), R, x.size(1), type,
@@ -220,7 +229,7 @@ PyObject* combine_grad(PyObject* const* a) {
   const int32_t* off = offsets(on, a[4], &E);
   dout = rows_of(dout);
   y = rows_of(y);
-  Tensor dy = route_rows(on, y.sizes(), y.scalar_type(), off, PyObject_IsTrue(a[5]) == 1);
+  Tensor dy = route_rows(on, y.sizes(), y.scalar_type(), off, truth(a[5]));
   Tensor dw = on.empty(pos.sizes(), at::kFloat);
   check("nvfp4_tokens_combine_grad",
         nvfp4_tokens_combine_grad(dout.data_ptr(), row_stride(dout), y.data_ptr(), row_stride(y), p,
@@ -295,7 +304,7 @@ PyObject* expert_linear(PyObject* const* a) {
   const Tensor& w = tensor(a[1], "w: expected a tensor");
   const Tensor& scale = tensor(a[2], "w_scale: expected a tensor");
   no_gradient(x, w, scale);
-  const int silu = PyObject_IsTrue(a[6]);
+  const bool silu = truth(a[6]);
   need(x.dim() == 2, "x: expected rows");
   const int64_t K = silu ? x.size(1) / 2 : x.size(1);
   need(!silu || x.size(1) % 2 == 0, "x: gate and up halves of one width");
@@ -422,7 +431,7 @@ PyObject* rms_norm(PyObject* const* a) {
   need(x.dim() == 2 && x.size(1) > 0, "x: expected rows [T, D]");
   const int type = dtype_of(x);
   const float eps = epsilon(a[3]);
-  const bool fp8 = PyObject_IsTrue(a[4]) == 1;
+  const bool fp8 = truth(a[4]);
   const On on(x);
   Tensor w = norm_weight(on, a[1], x);
   Tensor r = like_rows(on, a[2], x, "residual: expected rows of x's shape and type");
@@ -479,8 +488,8 @@ PyObject* rms_norm_grad(PyObject* const* a) {
 
 // flags from (sigmoid, renormalize)
 uint32_t gate_flags(PyObject* sigmoid, PyObject* renormalize) {
-  return (PyObject_IsTrue(sigmoid) == 1 ? NVFP4_GATE_SIGMOID : 0u) |
-         (PyObject_IsTrue(renormalize) == 1 ? NVFP4_GATE_RENORMALIZE : 0u);
+  return (truth(sigmoid) ? NVFP4_GATE_SIGMOID : 0u) |
+         (truth(renormalize) ? NVFP4_GATE_RENORMALIZE : 0u);
 }
 
 Tensor gate_bias(const On& on, PyObject* o, int64_t E) {
