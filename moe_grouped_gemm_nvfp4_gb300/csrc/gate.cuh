@@ -142,8 +142,9 @@ __device__ __noinline__ int gate_choose64(GateRule r, LaneLogits<L> logits, floa
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int e = lane + 32 * i;
-    const double s = __longlong_as_double(static_cast<long long>(key[i])) * inv;
-    key[i] = e < r.E ? gate_key64(s + static_cast<double>(__ldg(r.bias + e))) : 0ull;
+    // (rounded by itself: equal scores stay equal whichever products the compiler would fuse)
+    const double s = __dmul_rn(__longlong_as_double(static_cast<long long>(key[i])), inv);
+    key[i] = e < r.E ? gate_key64(__dadd_rn(s, static_cast<double>(__ldg(r.bias + e)))) : 0ull;
   }
   int mine = 0;
 #pragma unroll 1
