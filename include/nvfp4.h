@@ -680,7 +680,8 @@ nvfp4_status nvfp4_fp8_expert_linear(const void* x, int64_t rows, int64_t ld, in
  *   y = h / sqrt(mean(h^2) + eps) * weight
  *
  * FP32 arithmetic on the stored h, one rounding (a sum of squares past FP32's range
- * counts as infinity).  x and residual [T, D], row stride >= D; h and y dense;
+ * counts as infinity, squares below it as 0 or with fewer bits; a row of zeros with
+ * eps 0 is 0 / 0).  x and residual [T, D], row stride >= D; h and y dense;
  * weight [D] of weight_dtype: the rows' type or FP32.
  * 1 <= D <= 16384, eps >= 0.  A row of any operand lies at the same offset within
  * 16 bytes as that row of the others (dense matrices with 16-byte aligned bases
@@ -745,7 +746,8 @@ nvfp4_status nvfp4_topk_gate_grad(const float* dweights, const void* logits, int
 /* ------------------------------------------------------------------------
  * A whole MoE layer for a few tokens: router, gate, FP8 experts, weighted sum.
  *
- *   logits = x . router^T (FP32);  ids and weights by the gate (above)
+ *   logits = x . router^T;  ids and weights by the gate (above) from the FP32 sums (between
+ *   logits nearer than those are exact, the choice is that of the sums)
  *   h = SiLU(xq . gate_e^T) * (xq . up_e^T),   out = sum_k weight_k * hq_k . down_e^T
  *
  * with xq and hq the rows of x and of the FP32 h quantised as by

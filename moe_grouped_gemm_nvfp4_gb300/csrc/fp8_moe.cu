@@ -35,7 +35,7 @@
 //   scale, for down also * routing weight) that a warp of its own lays out.
 //
 // Measured in a graph, 128 experts, 8 chosen: 6144 x 2048 one token 61 us (302 MB of weights,
-// 0.73 of the copy rate; about 7 us pass before the first weights are asked for, and 5 behind
+// 0.73 of the copy rate; about 7 us pass before the first weights are asked for, and 6 behind
 // the last ones), 2 tokens 108, 4 tokens 178, 8 tokens 305 us (1.9 GB, 0.93); 2048 x 768 26, 33,
 // 47 and 61 us.  A first form with mma.sync, eight warps with rings of their own, spent 280
 // instructions on 2 KB of weights, converting codes: one token 96 us.  One cooperative launch

@@ -17,11 +17,11 @@
 // warp), then its instructions; its bytes (the logits once) would take a tenth of the time.
 // The gradient: latency, then its instructions (its rows are written once, logits read where
 // they are needed; a quarter to a third of the copy rate).
-// In a graph, FP32 logits, 8 chosen: one token of 128 experts 2.9 us (with a bias 4.3 to 4.5),
-// 8192 tokens of 128 7.1 us (sigmoid with a bias 10, softmax with one 17: its near sums are
-// ordered on 64-bit keys of all experts), of 256 11 us, of 512 22 us (as 1024 are done: 59),
-// 65536 of 128 42 us; the gradient 2.1 to 2.7, 3.9 to 5.5 (128 experts), 4.9 to 8.0 (256) and 19
-// to 29 us.
+// In a graph, FP32 logits, 8 chosen: one token of 128 experts 2.5 to 2.8 us (with a bias 3.8 to
+// 4.1), 8192 tokens of 128 6.7 us (with a bias 8.6 to 9.4, softmax 14 where a token's sums are so
+// near that it takes 64-bit keys of all experts), of 256 10 us (15), of 512 21 us (31 to 35, with
+// such a token 46; as 1024 are done: 57), 65536 of 128 40 us (52 to 58); the gradient 1.7 to 2.1,
+// 3.2 to 4.4 (128 experts), 4.2 to 6.1 (256) and 15 to 23 us.
 #include <cuda_fp16.h>
 
 #include "gate.h"

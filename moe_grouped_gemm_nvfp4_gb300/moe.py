@@ -399,12 +399,13 @@ class Fp8MoE:
     bias, score, renormalize and scale are the gate's (gating.topk_gate).
 
     step() of at most 8 tokens is one call of the library
-    (nvfp4.nvfp4_fp8_moe_layer).  More go through the router's product with FP32
-    logits, gating.topk_gate and Fp8MLP.step, whose
-    gate_up product and expert rows are rounded to the tokens' type; the router's
-    sums also have another order, which can change the choice between nearly equal
-    logits.  Both enqueue kernels only and keep no buffers; the experts are frozen
-    and neither takes part in autograd."""
+    (nvfp4.nvfp4_fp8_moe_layer).  More go through the router's product (torch's, with
+    FP32 logits whatever precision the process allows for FP32 matrices),
+    gating.topk_gate and Fp8MLP.step, whose gate_up product and expert rows are rounded
+    to the tokens' type.  The choice is that of the FP32 sums, whose order differs
+    between the two: between logits nearer than that rounding it can be another.  Both
+    enqueue kernels only and keep no buffers; the experts are frozen and neither takes
+    part in autograd."""
 
     def __init__(self, router, gate_up, down, topk: int, bias=None, score: str = "softmax",
                  renormalize: bool = True, scale: float = 1.0):

@@ -7,7 +7,9 @@ and with 8-bit output for the FP8 products.
 Rows [.., D] are BF16, FP16 or FP32 of any width up to 16384; the weight [D] has the
 rows' type or is FP32.  Rows whose elements are not neighbours, or whose stride differs
 from a dense matrix's by no multiple of 16 bytes, are copied first.  The squares are FP32:
-rows whose sum of squares leaves its range (elements from about 2^63 on) have rstd 0.
+rows whose sum of squares passes its range (elements from about 2^57 in the widest rows, 2^63
+in narrow ones) have rstd 0, squares below it (elements under 2^-63, which only tells where
+eps is as small) lose bits, and a row of zeros without an eps is 0 / 0.
 
 `rms_norm` takes part in autograd; `rms_norm_grad` is its gradient as a plain call, which
 enqueues kernels only (the one for a captured step: autograd's own bookkeeping can use other
