@@ -78,7 +78,8 @@ struct GateScores {
       const float q = expf(-fabsf(l));
       return (l < 0.f ? q : 1.f) / (1.f + q);
     }
-    return max == -INFINITY && l == max ? 0.f : expf(l - max) * inv;
+    // (times inv there too: it is NaN where a NaN stands among infinities)
+    return (max == -INFINITY && l == max ? 0.f : expf(l - max)) * inv;
   }
 };
 // A chosen score times a factor that all chosen ones of the row share, by its logit and the
